@@ -199,9 +199,6 @@ def _run_own(s):
         s["params"] = B.make_params(c["heads"], c["kv_heads"], c["head_size"], c["block_size"], _DTYPES[c["dtype"]], c["head_size"] ** -0.5,
                                     kv_cache_dtype="fp8_e4m3" if c["fp8"] else "auto", k_scale=_SCALE8 if c["fp8"] else 1.0,
                                     v_scale=_SCALE8 if c["fp8"] else 1.0)
-        if c["op"] == "sparse":
-            n = B.paged_attn_decode_sparse_workspace_size(c["seqs"], c["pick"], s["params"])
-            s["workspace"] = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
     p = s["params"]
     if c["op"] == "append":
         B.kv_cache_write_rope(s["rotated"], s["query"], s["key"], s["value"], s["cache"], s["slots"], s["positions"], s["table"], p,
@@ -214,7 +211,7 @@ def _run_own(s):
         B.paged_attn_select_blocks(s["selected"], s["query"], s["bounds"], s["tables"], s["seq_lens"], s["max_len"], p,
                                    num_sink=c["sink"], num_recent=c["recent"])
         return {"selected": s["selected"]}
-    B.paged_attn_decode_sparse(s["out"], s["query"], s["cache"], s["tables"], s["seq_lens"], s["selected"], p, s["workspace"])
+    B.paged_attn_decode_sparse(s["out"], s["query"], s["cache"], s["tables"], s["seq_lens"], s["selected"], p)
     return {"out": s["out"]}
 
 
