@@ -397,6 +397,150 @@ pkv_status kv_swap_blocks(const void *src_cache, int64_t src_num_blocks,
                           const int64_t *pairs, int64_t num_pairs,
                           const pkv_attn_params *params, pkv_stream_t stream);
 
+/*
+ * Block-sparse decode: a step over a long cache that reads only the blocks
+ * whose keys can matter.  The attention-backend pages have no counterpart of
+ * these calls; they stand beside kv_cache_write and paged_attn_decode, over
+ * the same cache, block tables and params, and a step makes them in this
+ * order:
+ *   kv_cache_write_rope (or kv_cache_write)   store the new tokens
+ *   kv_block_bounds                           bounds of the blocks they are in
+ *   paged_attn_select_blocks                  pick blocks per KV head
+ *   paged_attn_decode_sparse                  attend to the picked blocks
+ * Like the decode calls they are launched as programmatic dependents of the
+ * kernel before them in the stream and read and write nothing before it has
+ * completed.  None of them needs a workspace or keeps anything between calls.
+ */
+
+/*
+ * kv_cache_write_rope -- kv_cache_write with the rotary position embedding
+ * applied on the way: queries and keys are rotated by their positions, the
+ * keys and the (unrotated) values stored in their slots.  For pair i <
+ * rot_dim / 2 of a head, (x1, x2) = channels (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when `interleaved`, and c, s = the table's cos and sin:
+ *   y1 = x1 c - x2 s,   y2 = x2 c + x1 s
+ * in fp32, rounded once to the output's type (over an fp8 cache the key code
+ * is that of y / k_scale, with no rounding to the model dtype between).
+ * Channels rot_dim .. head_size - 1 pass through unchanged.
+ *
+ *   query_out, query   [num_tokens][num_heads * head_size] elements; query_out
+ *                  may be query (in place; then the strides must agree too)
+ *   key, value     [num_tokens][num_kv_heads * head_size] elements
+ *   *_stride       elements from one token's row to the next: at least the
+ *                  row's length and a multiple of 8, so that the three may be
+ *                  slices of one projection's output
+ *   positions      int64[num_tokens]; outside [0, max_position) is recorded
+ *                  as a bounds error and the token skipped
+ *   cos_sin        fp32 [max_position][rot_dim]: rot_dim / 2 cosines, then
+ *                  as many sines
+ *   rot_dim        multiple of 16, 16 .. head_size
+ *   interleaved    0 or 1
+ *   slot_mapping   as kv_cache_write.  A skipped token (slot < 0, or a bad
+ *                  slot or position) leaves its query_out row and the cache
+ *                  as they were.  Two tokens with the same slot race.
+ * Pointers of elements are 16-byte aligned.
+ */
+pkv_status kv_cache_write_rope(void *query_out, int64_t query_out_stride, const void *query,
+                               int64_t query_stride, const void *key, int64_t key_stride,
+                               const void *value, int64_t value_stride, int64_t num_tokens,
+                               const int64_t *positions, const float *cos_sin,
+                               int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                               void *kv_cache, int64_t num_blocks, const int64_t *slot_mapping,
+                               const pkv_attn_params *params, pkv_stream_t stream);
+
+/*
+ * kv_block_bounds -- for every cache block that holds one of the positions
+ * context_lens[b] .. seq_lens[b] - 1 of a sequence, and every KV head, the
+ * channelwise smallest and largest of the block's keys (those at positions
+ * below seq_lens[b]; slots past the end are not read).
+ *
+ *   bounds         [num_blocks][num_kv_heads][2][head_size] elements of the
+ *                  cache's type (E4M3 codes over an fp8 cache): minima, then
+ *                  maxima, exact.  A channel with a NaN key has NaN bounds.
+ *                  Blocks without a new position stay as they were.
+ *   context_lens   int32[num_seqs]: positions whose bounds are up to date
+ *                  (the cached tokens before the step); NULL: none are, every
+ *                  block of the sequences is done
+ *   seq_lens       int32[num_seqs]: length with the new tokens; 0: nothing
+ *   max_new_tokens host upper bound on seq_lens[b] - context_lens[b]
+ * A sequence with seq_len < 0 or above max_blocks_per_seq * block_size,
+ * context_len outside 0 .. seq_len, or more than max_new_tokens new tokens
+ * records PKV_ERR_BOUNDS and is skipped, as is a table entry out of range.
+ * Sequences that share a block (a common prefix) write the same bounds to it
+ * when both hold all of its keys.  Blocks that were moved (kv_copy_blocks,
+ * kv_swap_blocks) are done again with context_lens 0.
+ */
+pkv_status kv_block_bounds(void *bounds, const void *kv_cache, int64_t num_blocks,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *seq_lens,
+                           int32_t num_seqs, int32_t max_new_tokens,
+                           const pkv_attn_params *params, pkv_stream_t stream);
+
+/*
+ * paged_attn_select_blocks -- for every sequence and KV head, the
+ * max_selected blocks that a decode attends to.  Block j of the sequence
+ * scores
+ *   max over the group's query heads h of sum_d max(q_hd lo_jd, q_hd hi_jd),
+ * lo and hi its bounds: no key of the block has a larger q.k with any of the
+ * heads.  Among the visible blocks (those with a position < seq_len and
+ * inside the sliding window) the first num_sink blocks of the sequence and
+ * the last num_recent are always taken, then those with the largest scores;
+ * equal scores go to the lower block, a NaN score counts as +infinity.  The
+ * choice is that of the exact scores: where fp32 cannot tell two blocks
+ * apart, they are scored again in 64 bits.
+ *
+ *   selected       int32[num_seqs][num_kv_heads][max_selected]: logical block
+ *                  numbers, ascending, -1 behind the last one (all of the
+ *                  visible blocks when they are no more than max_selected)
+ *   max_selected   >= num_sink + num_recent
+ *   query          [num_seqs][num_heads * head_size] elements, as the decode
+ *                  will use them (rotated)
+ *   bounds         as kv_block_bounds
+ *   seq_lens       int32[num_seqs] with the new token; 0 gives -1s; < 0, or
+ *                  above max_seq_len or max_blocks_per_seq * block_size,
+ *                  records PKV_ERR_BOUNDS and gives -1s
+ *   max_seq_len    host upper bound on seq_lens
+ *   num_sink       >= 0;  num_recent >= 1 (the last block holds the query's
+ *                  own position)
+ * A table entry out of range records PKV_ERR_BOUNDS; its block is taken last.
+ * ALiBi slopes are PKV_ERR_UNSUPPORTED (the scores are unbiased), as are
+ * sequences of more than PKV_SELECT_MAX_BLOCKS blocks and KV heads with more
+ * than 16384 / head_size query heads.  scale, k_scale and
+ * non_causal do not matter.
+ */
+#define PKV_SELECT_MAX_BLOCKS 131072
+pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, const void *query,
+                                    int32_t num_seqs, const void *bounds, int64_t num_blocks,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, int32_t max_seq_len,
+                                    int32_t num_sink, int32_t num_recent,
+                                    const pkv_attn_params *params, pkv_stream_t stream);
+
+/*
+ * paged_attn_decode_sparse -- paged_attn_decode over some of each sequence's
+ * blocks: query head h of sequence b attends to the keys of the blocks
+ * selected[b][KV head of h] at positions < seq_lens[b] (and inside the
+ * sliding window), with ALiBi as there.  With every block selected it is
+ * paged_attn_decode.
+ *
+ *   selected       int32[num_seqs][num_kv_heads][max_selected]: strictly
+ *                  ascending logical block numbers, then any negative
+ *                  numbers; as paged_attn_select_blocks gives them.  A number
+ *                  that does not ascend or is not below the sequence's count
+ *                  of blocks records PKV_ERR_BOUNDS.
+ *   seq_lens       int32[num_seqs]; < 0 or above max_blocks_per_seq *
+ *                  block_size records PKV_ERR_BOUNDS and gives zero rows
+ * A row with nothing to attend to (seq_len 0, none selected, all of the
+ * selected outside the window) is zero.  Other arguments as
+ * paged_attn_decode.
+ */
+pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_seqs,
+                                    const void *kv_cache, int64_t num_blocks,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, const int32_t *selected,
+                                    int32_t max_selected, const pkv_attn_params *params,
+                                    pkv_stream_t stream);
+
 /* Static, never-NULL description of a status code. */
 const char *pkv_status_string(pkv_status status);
 

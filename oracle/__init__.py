@@ -6,3 +6,4 @@ library (``paged_kv_cache_246_gb300``) never imports it, and it imports
 nothing from the library: the two share no code.
 """
 from .paged_attention import *  # noqa: F401,F403
+from .sparse_decode import *  # noqa: F401,F403

@@ -29,6 +29,8 @@ EXPORTS = ("kv_cache_write", "paged_attn_decode", "paged_attn_decode_workspace_s
            "paged_attn_decode_multi_workspace_size", "paged_attn_decode_dcp_partial",
            "paged_attn_decode_dcp_workspace_size", "paged_attn_dcp_combine",
            "paged_attn_prefill_varlen", "kv_copy_blocks", "kv_swap_blocks",
+           "kv_cache_write_rope", "kv_block_bounds", "paged_attn_select_blocks",
+           "paged_attn_decode_sparse",
            "pkv_status_string", "pkv_device_error", "pkv_abi_version",
            "pkv_check_wait_timeout")
 
@@ -78,6 +80,12 @@ def lib() -> ctypes.CDLL:
                                                 i32, P, vp]),
             "kv_copy_blocks": (i32, [vp, i32, i64, vp, i64, P, vp]),
             "kv_swap_blocks": (i32, [vp, i64, vp, i64, vp, i64, P, vp]),
+            "kv_cache_write_rope": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64, i32,
+                                          i32, vp, i64, vp, P, vp]),
+            "kv_block_bounds": (i32, [vp, vp, i64, vp, i32, vp, vp, i32, i32, P, vp]),
+            "paged_attn_select_blocks": (i32, [vp, i32, vp, i32, vp, i64, vp, i32, vp, i32, i32,
+                                               i32, P, vp]),
+            "paged_attn_decode_sparse": (i32, [vp, vp, i32, vp, i64, vp, i32, vp, vp, i32, P, vp]),
             "pkv_status_string": (ctypes.c_char_p, [i32]),
             "pkv_device_error": (i32, [ctypes.POINTER(ctypes.c_int64)]),
             "pkv_abi_version": (i32, []),
@@ -375,6 +383,189 @@ def kv_swap_blocks(src_cache: torch.Tensor, dst_cache: torch.Tensor, pairs: torc
                                 pairs.data_ptr(), int(pairs.shape[0]), ctypes.byref(params),
                                 _stream(stream)),
            "kv_swap_blocks")
+
+
+# ---------------------------------------------------------------------------
+# Block-sparse decode: cache write with the rotation, block bounds, block
+# selection, attention over the selected blocks.  These calls run on the
+# device that holds their tensors, whichever is current; a stream given by
+# the caller must belong to it.
+# ---------------------------------------------------------------------------
+def _call_on(first: torch.Tensor, others: Sequence[torch.Tensor], stream, where: str, *args):
+    dev = first.device
+    for t in others:
+        if t.device != dev:
+            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+    if stream is not None and getattr(stream, "device", dev) != dev:
+        raise ValueError(f"{where}: a stream of {stream.device} for tensors on {dev}")
+    fn = getattr(lib(), where)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    _check(st, where)
+
+
+def _need_model_dtype(t: torch.Tensor, name: str, p: AttnParams) -> None:
+    if _DTYPES.get(t.dtype) != p.dtype:
+        raise ValueError(f"{name} must have the params' dtype, got {t.dtype}")
+
+
+def _need_cache_dtype(t: torch.Tensor, name: str, p: AttnParams) -> None:
+    if p.kv_cache_dtype == PKV_CACHE_FP8_E4M3:
+        if t.dtype != torch.uint8:
+            raise ValueError(f"{name} must be torch.uint8 over an fp8 cache, got {t.dtype}")
+    else:
+        _need_model_dtype(t, name, p)
+
+
+def _need_batch(block_tables: torch.Tensor, seq_lens: torch.Tensor) -> int:
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    if block_tables.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_tables and seq_lens sizes disagree")
+    return seq_lens.shape[0]
+
+
+def _row_stride(t: torch.Tensor, name: str, rows: int, row: int, p: AttnParams) -> int:
+    """Elements between the rows of a [rows, row] tensor whose rows may be
+    slices of wider ones."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.shape != (rows, row):
+        raise ValueError(f"{name} must be [{rows}, {row}], got {list(t.shape)}")
+    _need_model_dtype(t, name, p)
+    if t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    stride = t.stride(0) if rows > 1 else row
+    if stride < row or stride % 8 != 0:
+        raise ValueError(f"{name}'s rows must not overlap and start a multiple of 8 elements apart")
+    return stride
+
+
+def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, position_scale: float = 1.0,
+               device="cuda") -> torch.Tensor:
+    """The cos_sin table of kv_cache_write_rope: fp32 [max_position, rot_dim],
+    row p = rot_dim / 2 cosines, then sines, of the angles position_scale * p *
+    base^(-2i / rot_dim).  Angles are taken in 64 bits: in 32 those of far
+    positions are off by more than the table's rounding."""
+    if max_position <= 0 or rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("max_position and rot_dim must be positive, rot_dim even")
+    f = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = (torch.arange(max_position, dtype=torch.float64, device=device) * position_scale)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).to(torch.float32)
+
+
+def kv_cache_write_rope(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                        value: torch.Tensor, kv_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                        positions: torch.Tensor, cos_sin: torch.Tensor, params: AttnParams,
+                        interleaved: bool = False, stream=None) -> None:
+    """kv_cache_write with queries and keys rotated by their positions: rows of
+    query, key and value may be slices of one projection's output; query_out
+    may be query."""
+    _need(kv_cache, "kv_cache")
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    _need(positions, "positions", torch.int64, 1)
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    nb = _cache_blocks(kv_cache, params)
+    _need_cache_dtype(kv_cache, "kv_cache", params)
+    T = slot_mapping.shape[0]
+    if positions.shape[0] != T:
+        raise ValueError("positions and slot_mapping sizes disagree")
+    q_row = params.num_heads * params.head_size
+    kv_row = params.num_kv_heads * params.head_size
+    so = _row_stride(query_out, "query_out", T, q_row, params)
+    sq = _row_stride(query, "query", T, q_row, params)
+    sk = _row_stride(key, "key", T, kv_row, params)
+    sv = _row_stride(value, "value", T, kv_row, params)
+    _call_on(kv_cache, (query_out, query, key, value, slot_mapping, positions, cos_sin), stream,
+             "kv_cache_write_rope", query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(),
+             sk, value.data_ptr(), sv, T, positions.data_ptr(), cos_sin.data_ptr(),
+             cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), kv_cache.data_ptr(), nb,
+             slot_mapping.data_ptr(), ctypes.byref(params))
+
+
+def _need_bounds(bounds: torch.Tensor, blocks: Optional[int], p: AttnParams) -> int:
+    _need(bounds, "bounds", None, 4)
+    _need_cache_dtype(bounds, "bounds", p)
+    nb = bounds.shape[0] if blocks is None else blocks
+    if bounds.shape != (nb, p.num_kv_heads, 2, p.head_size):
+        raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_size]")
+    return nb
+
+
+def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor,
+                    seq_lens: torch.Tensor, max_new_tokens: int, params: AttnParams,
+                    context_lens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Channelwise minima and maxima of the keys of the blocks that hold
+    positions context_lens[b] .. seq_lens[b] - 1 (None: all of the sequence)."""
+    _need(kv_cache, "kv_cache")
+    nb = _cache_blocks(kv_cache, params)
+    _need_cache_dtype(kv_cache, "kv_cache", params)
+    _need_bounds(bounds, nb, params)
+    n = _need_batch(block_tables, seq_lens)
+    others = [bounds, block_tables, seq_lens]
+    if context_lens is not None:
+        _need(context_lens, "context_lens", torch.int32, 1)
+        if context_lens.shape[0] != n:
+            raise ValueError("context_lens and seq_lens sizes disagree")
+        others.append(context_lens)
+    _call_on(kv_cache, others, stream, "kv_block_bounds", bounds.data_ptr(), kv_cache.data_ptr(), nb,
+             block_tables.data_ptr(), block_tables.shape[1],
+             None if context_lens is None else context_lens.data_ptr(), seq_lens.data_ptr(), n,
+             int(max_new_tokens), ctypes.byref(params))
+
+
+def _need_selected(selected: torch.Tensor, n: int, p: AttnParams) -> int:
+    _need(selected, "selected", torch.int32, 3)
+    if selected.shape[0] != n or selected.shape[1] != p.num_kv_heads:
+        raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
+    return selected.shape[2]
+
+
+def paged_attn_select_blocks(selected: torch.Tensor, query: torch.Tensor, bounds: torch.Tensor,
+                             block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                             params: AttnParams, num_sink: int = 0, num_recent: int = 1,
+                             stream=None) -> None:
+    """selected [num_seqs, num_kv_heads, K]: each KV head's K blocks with the
+    largest bound on q.k, the first num_sink and last num_recent among them,
+    ascending, -1 behind."""
+    nb = _need_bounds(bounds, None, params)
+    _need(query, "query")
+    _need_model_dtype(query, "query", params)
+    n = _need_batch(block_tables, seq_lens)
+    k = _need_selected(selected, n, params)
+    if query.numel() != n * params.num_heads * params.head_size:
+        raise ValueError("query and seq_lens sizes disagree")
+    _call_on(bounds, (selected, query, block_tables, seq_lens), stream, "paged_attn_select_blocks",
+             selected.data_ptr(), k, query.data_ptr(), n, bounds.data_ptr(), nb,
+             block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), int(max_seq_len),
+             int(num_sink), int(num_recent), ctypes.byref(params))
+
+
+def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor,
+                             block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                             selected: torch.Tensor, params: AttnParams, stream=None) -> None:
+    """paged_attn_decode over the blocks that selected [num_seqs, num_kv_heads,
+    K] names for each sequence and KV head (ascending, negative numbers behind)."""
+    for t, name in ((out, "out"), (query, "query")):
+        _need(t, name)
+        _need_model_dtype(t, name, params)
+    _need(kv_cache, "kv_cache")
+    nb = _cache_blocks(kv_cache, params)
+    _need_cache_dtype(kv_cache, "kv_cache", params)
+    n = _need_batch(block_tables, seq_lens)
+    k = _need_selected(selected, n, params)
+    hd = params.num_heads * params.head_size
+    if query.numel() != n * hd or out.numel() != n * hd:
+        raise ValueError("query/out sizes disagree with seq_lens")
+    _call_on(kv_cache, (out, query, block_tables, seq_lens, selected), stream,
+             "paged_attn_decode_sparse", out.data_ptr(), query.data_ptr(), n, kv_cache.data_ptr(),
+             nb, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+             selected.data_ptr(), k, ctypes.byref(params))
 
 
 def check_wait_timeout(tag: int, stream=None) -> None:

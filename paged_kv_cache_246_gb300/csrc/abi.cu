@@ -1,5 +1,6 @@
 // extern "C" front end of libpkv.so: argument validation, device selection
-// and dispatch to the kernels of kv_ops.cu, decode.cu and prefill.cu.
+// and dispatch to the kernels of kv_ops.cu, decode.cu, prefill.cu, rope.cu,
+// select.cu and sparse.cu.
 // Everything here runs on the host; nothing reads device memory.
 #include <cudaTypedefs.h>
 
@@ -162,6 +163,7 @@ static pkv_status make_geometry(const pkv_attn_params *p, int64_t num_blocks, Ge
 
 static pkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
+constexpr int32_t kMaxSelectQuery = 16384;  // query elements of one KV head's group (64 KB as fp32)
 constexpr int32_t kMaxMultiQueryLen = 64;  // tokens per sequence of a multi-token decode
 
 }  // namespace pkv
@@ -428,6 +430,122 @@ pkv_status paged_attn_prefill_varlen(void *out, const void *query, int64_t num_q
                                   block_tables, max_blocks_per_seq, g, s));
 }
 
+static bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; }
+
+pkv_status kv_cache_write_rope(void *query_out, int64_t query_out_stride, const void *query,
+                               int64_t query_stride, const void *key, int64_t key_stride,
+                               const void *value, int64_t value_stride, int64_t num_tokens,
+                               const int64_t *positions, const float *cos_sin,
+                               int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                               void *kv_cache, int64_t num_blocks, const int64_t *slot_mapping,
+                               const pkv_attn_params *params, pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || max_position <= 0 || (interleaved != 0 && interleaved != 1))
+    return PKV_ERR_INVALID;
+  if (rot_dim <= 0 || rot_dim > g.D) return PKV_ERR_INVALID;
+  if (rot_dim % 16 != 0 || num_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  const int64_t q_row = static_cast<int64_t>(g.H) * g.D;
+  if (!row_stride_ok(query_out_stride, q_row) || !row_stride_ok(query_stride, q_row) ||
+      !row_stride_ok(key_stride, g.row_elems) || !row_stride_ok(value_stride, g.row_elems))
+    return PKV_ERR_INVALID;
+  if (num_tokens == 0) return PKV_OK;
+  if (!query_out || !query || !key || !value || !positions || !cos_sin || !kv_cache ||
+      !slot_mapping)
+    return PKV_ERR_INVALID;
+  if (!aligned(query_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(positions, 8) || !aligned(cos_sin, 16) || !aligned(kv_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return PKV_ERR_INVALID;
+  if (query_out == query && query_out_stride != query_stride) return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  const RopeCall r = {query_out,    query_out_stride, query,     query_stride, key,
+                      key_stride,   value,            value_stride, num_tokens, positions,
+                      cos_sin,      max_position,     rot_dim,   interleaved,  kv_cache,
+                      slot_mapping};
+  return from_cuda(launch_rope_write(r, g, s));
+}
+
+pkv_status kv_block_bounds(void *bounds, const void *kv_cache, int64_t num_blocks,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *seq_lens,
+                           int32_t num_seqs, int32_t max_new_tokens,
+                           const pkv_attn_params *params, pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || max_new_tokens < 0 || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID;
+  if (num_seqs == 0 || max_new_tokens == 0) return PKV_OK;
+  if (!bounds || !kv_cache || !block_tables || !seq_lens) return PKV_ERR_INVALID;
+  if (!aligned(bounds, 16) || !aligned(kv_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4) || !aligned(seq_lens, 4))
+    return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  return from_cuda(launch_block_bounds(bounds, kv_cache, block_tables, max_blocks_per_seq,
+                                       context_lens, seq_lens, num_seqs, max_new_tokens, g, s));
+}
+
+pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, const void *query,
+                                    int32_t num_seqs, const void *bounds, int64_t num_blocks,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, int32_t max_seq_len,
+                                    int32_t num_sink, int32_t num_recent,
+                                    const pkv_attn_params *params, pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || max_seq_len < 0 || max_blocks_per_seq <= 0 ||
+      num_sink < 0 || num_recent < 1 ||
+      max_selected < static_cast<int64_t>(num_sink) + num_recent)
+    return PKV_ERR_INVALID;
+  if (g.alibi || g.KVH > 65535 || g.QPK * g.D > kMaxSelectQuery ||
+      (static_cast<int64_t>(max_seq_len) + g.BS - 1) / g.BS > PKV_SELECT_MAX_BLOCKS)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!selected || !query || !bounds || !block_tables || !seq_lens) return PKV_ERR_INVALID;
+  if (!aligned(selected, 4) || !aligned(query, 16) || !aligned(bounds, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  const SelectCall c = {selected,     max_selected, query,       num_seqs, bounds,
+                        block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_sink,
+                        num_recent};
+  return from_cuda(launch_select(c, g, s));
+}
+
+pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_seqs,
+                                    const void *kv_cache, int64_t num_blocks,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, const int32_t *selected,
+                                    int32_t max_selected, const pkv_attn_params *params,
+                                    pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || max_selected <= 0 || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID;
+  if (num_seqs == 0) return PKV_OK;
+  if (!out || !query || !kv_cache || !block_tables || !seq_lens || !selected)
+    return PKV_ERR_INVALID;
+  if (!aligned(out, 16) || !aligned(query, 16) || !aligned(kv_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4))
+    return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  return from_cuda(launch_sparse_decode(out, query, num_seqs, kv_cache, block_tables,
+                                        max_blocks_per_seq, seq_lens, selected, max_selected, g,
+                                        s));
+}
+
 pkv_status kv_copy_blocks(void *const *kv_caches, int32_t num_layers, int64_t num_blocks,
                           const int64_t *pairs, int64_t num_pairs, const pkv_attn_params *params,
                           pkv_stream_t stream) {
@@ -504,10 +622,11 @@ pkv_status pkv_check_wait_timeout(int64_t tag, pkv_stream_t stream) {
 }
 
 pkv_status pkv_device_error(int64_t *detail) {
-  constexpr int kUnits = 3;
-  unsigned long long words[kUnits] = {0, 0, 0};
+  constexpr int kUnits = 6;
+  unsigned long long words[kUnits] = {};
   cudaError_t (*readers[kUnits])(unsigned long long *) = {
-      read_device_error_kv_ops, read_device_error_decode, read_device_error_prefill};
+      read_device_error_kv_ops, read_device_error_decode, read_device_error_prefill,
+      read_device_error_rope,   read_device_error_select, read_device_error_sparse};
   for (int k = 0; k < kUnits; ++k)
     if (readers[k](&words[k]) != cudaSuccess) return PKV_ERR_CUDA;
   for (int k = 0; k < kUnits; ++k) {

@@ -81,6 +81,78 @@ cudaError_t read_device_error_decode(unsigned long long *out);
 // must be the current device (looked up on the first call per device).
 cudaError_t static_decode_scratch(int device, void **ptr, size_t *bytes);
 
+// rope.cu
+struct RopeCall {
+  void *query_out;
+  int64_t query_out_stride;
+  const void *query;
+  int64_t query_stride;
+  const void *key;
+  int64_t key_stride;
+  const void *value;
+  int64_t value_stride;
+  int64_t num_tokens;
+  const int64_t *positions;
+  const float *cos_sin;
+  int64_t max_position;
+  int32_t rot_dim, interleaved;
+  void *kv_cache;
+  const int64_t *slot_mapping;
+};
+cudaError_t launch_rope_write(const RopeCall &r, const Geometry &g, cudaStream_t stream);
+cudaError_t read_device_error_rope(unsigned long long *out);
+
+// select.cu
+cudaError_t launch_block_bounds(void *bounds, const void *kv_cache, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int32_t *context_lens,
+                                const int32_t *seq_lens, int num_seqs, int max_new_tokens,
+                                const Geometry &g, cudaStream_t stream);
+struct SelectCall {
+  int32_t *selected;
+  int max_selected;
+  const void *query;
+  int num_seqs;
+  const void *bounds;
+  const int32_t *block_tables;
+  int max_blocks_per_seq;
+  const int32_t *seq_lens;
+  int max_seq_len, num_sink, num_recent;
+};
+cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t stream);
+cudaError_t read_device_error_select(unsigned long long *out);
+
+// sparse.cu
+cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, const void *kv_cache,
+                                 const int32_t *block_tables, int max_blocks_per_seq,
+                                 const int32_t *seq_lens, const int32_t *selected,
+                                 int max_selected, const Geometry &g, cudaStream_t stream);
+cudaError_t read_device_error_sparse(unsigned long long *out);
+
+// A kernel launch as a programmatic dependent of the kernel before it in the
+// stream, in clusters of `cluster` CTAs along x (0: none).
+struct PdlLaunch {
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute at[2];
+  PdlLaunch(dim3 grid, int threads, size_t smem, cudaStream_t stream, unsigned cluster = 0) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = at;
+    c.numAttrs = 1;
+    if (cluster) {
+      at[1].id = cudaLaunchAttributeClusterDimension;
+      at[1].val.clusterDim.x = cluster;
+      at[1].val.clusterDim.y = 1;
+      at[1].val.clusterDim.z = 1;
+      c.numAttrs = 2;
+    }
+  }
+  PdlLaunch(const PdlLaunch &) = delete;
+};
+
 // prefill.cu
 cudaError_t launch_prefill(void *out, const void *query, int64_t num_q_tokens, int num_seqs,
                            const int32_t *cu_q, const int32_t *cu_k, int max_query_len,

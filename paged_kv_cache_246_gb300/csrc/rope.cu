@@ -1,0 +1,222 @@
+// kv_cache_write_rope: the cache write with the rotary position embedding on
+// the way.  Per pair (x1, x2) of channels and the position's cos c, sin s:
+//     y1 = x1 c - x2 s,   y2 = x2 c + x1 s      (fp32, one rounding out)
+// Queries go to query_out, keys (rotated) and values to their cache slots.
+//
+// Bound by HBM: a token's row is read once and written once (24 KB at 32 + 8
+// + 8 heads of 128 and 16 bits), the rotation is 6 flops per pair.  A head is
+// D / 16 lanes wide: a lane owns two 16-byte chunks whose channels pair up
+// (half split: chunks i and i + rot_dim / 16; interleaved: any two), so no
+// pair crosses lanes and every access is an aligned 16 bytes.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pkv {
+namespace rope {
+
+struct Args {
+  uint16_t *q_out;
+  const uint16_t *q, *k, *v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements
+  int64_t num_tokens, max_position, num_slots;
+  const int64_t *positions, *slots;
+  const float *cos_sin;
+  uint8_t *k_half, *v_half;
+  int64_t row_bytes;  // of the cache
+  int H, KVH, rot;
+  float k_scale, v_scale;
+};
+
+__device__ __forceinline__ void widen(float (&f)[8], const uint4 &u, BF16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = BF16::to_f2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void widen(float (&f)[8], const uint4 &u, FP16) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = FP16::to_f2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+  return make_uint4(T::from_f2(f[0], f[1]), T::from_f2(f[2], f[3]), T::from_f2(f[4], f[5]),
+                    T::from_f2(f[6], f[7]));
+}
+
+// Eight values as E4M3 codes of f / scale (IEEE quotient, nearest even,
+// saturating), as the plain cache write makes them.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)), __NV_SATFINITE,
+        __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+__device__ __forceinline__ void rotate(float &x1, float &x2, float c, float s) {
+  const float y1 = x1 * c - x2 * s, y2 = x2 * c + x1 * s;
+  x1 = y1;
+  x2 = y2;
+}
+
+// CTA = one token; thread i takes the lane slots i, i + blockDim, ... of the
+// token's (H + 2 KVH) heads.
+template <class T, int D, bool KV8, bool INTER>
+__global__ void __launch_bounds__(512) rope_write_kernel(const Args a) {
+  constexpr int LPH = D / 16;  // lanes per head
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int64_t slot = __ldg(a.slots + t);
+  if (slot < 0) return;  // padding token
+  const int64_t pos = __ldg(a.positions + t);
+  if (slot >= a.num_slots || pos < 0 || pos >= a.max_position) {
+    if (threadIdx.x == 0) record_error(PKV_ERR_BOUNDS, t);
+    return;
+  }
+  const int items = (a.H + 2 * a.KVH) * LPH;
+  for (int i = threadIdx.x; i < items; i += blockDim.x) {
+    const int head = i / LPH, j = i % LPH;
+    // this lane's two chunks of the head
+    int c0, c1;
+    bool rot0, rot1;
+    if constexpr (INTER) {
+      c0 = 2 * j;
+      c1 = c0 + 1;
+      rot0 = c0 * 8 < a.rot;
+      rot1 = c1 * 8 < a.rot;
+    } else {
+      const int half = a.rot / 16;
+      rot0 = rot1 = j < half;
+      c0 = rot0 ? j : 2 * j;
+      c1 = rot0 ? j + half : 2 * j + 1;
+    }
+    const bool is_q = head < a.H, is_v = head >= a.H + a.KVH;
+    const int hh = is_q ? head : is_v ? head - a.H - a.KVH : head - a.H;
+    const uint16_t *src = is_q   ? a.q + t * a.q_stride
+                          : is_v ? a.v + t * a.v_stride
+                                 : a.k + t * a.k_stride;
+    const uint4 *s4 = reinterpret_cast<const uint4 *>(src + hh * D);
+    uint4 u0 = s4[c0], u1 = s4[c1];
+    float x0[8], x1[8];
+    widen(x0, u0, T{});
+    widen(x1, u1, T{});
+    if (!is_v && (rot0 || rot1)) {
+      const float *cs = a.cos_sin + pos * a.rot;
+      const int half = a.rot / 2;
+      if constexpr (INTER) {
+        // chunk c holds pairs 4c .. 4c + 3
+        const float4 ca = *reinterpret_cast<const float4 *>(cs + 4 * c0);
+        const float4 sa = *reinterpret_cast<const float4 *>(cs + half + 4 * c0);
+        rotate(x0[0], x0[1], ca.x, sa.x);
+        rotate(x0[2], x0[3], ca.y, sa.y);
+        rotate(x0[4], x0[5], ca.z, sa.z);
+        rotate(x0[6], x0[7], ca.w, sa.w);
+        if (rot1) {
+          const float4 cb = *reinterpret_cast<const float4 *>(cs + 4 * c1);
+          const float4 sb = *reinterpret_cast<const float4 *>(cs + half + 4 * c1);
+          rotate(x1[0], x1[1], cb.x, sb.x);
+          rotate(x1[2], x1[3], cb.y, sb.y);
+          rotate(x1[4], x1[5], cb.z, sb.z);
+          rotate(x1[6], x1[7], cb.w, sb.w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 cc = *reinterpret_cast<const float4 *>(cs + 8 * j + e);
+          const float4 ss = *reinterpret_cast<const float4 *>(cs + half + 8 * j + e);
+          rotate(x0[e], x1[e], cc.x, ss.x);
+          rotate(x0[e + 1], x1[e + 1], cc.y, ss.y);
+          rotate(x0[e + 2], x1[e + 2], cc.z, ss.z);
+          rotate(x0[e + 3], x1[e + 3], cc.w, ss.w);
+        }
+      }
+      if (rot0) u0 = narrow<T>(x0);
+      if (rot1) u1 = narrow<T>(x1);
+    }
+    if (is_q) {
+      uint4 *d4 = reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + hh * D);
+      d4[c0] = u0;
+      d4[c1] = u1;
+    } else {
+      uint8_t *row = (is_v ? a.v_half : a.k_half) + slot * a.row_bytes;
+      if constexpr (KV8) {
+        uint2 *d2 = reinterpret_cast<uint2 *>(row + hh * D);
+        const float scale = is_v ? a.v_scale : a.k_scale;
+        d2[c0] = codes8(x0, scale);
+        d2[c1] = codes8(x1, scale);
+      } else {
+        uint4 *d4 = reinterpret_cast<uint4 *>(row + hh * D * 2);
+        d4[c0] = u0;
+        d4[c1] = u1;
+      }
+    }
+  }
+}
+
+template <class T, int D, bool KV8>
+static cudaError_t launch_typed(const Args &a, bool interleaved, cudaStream_t stream) {
+  const int items = (a.H + 2 * a.KVH) * (D / 16);
+  PdlLaunch cfg(dim3(static_cast<unsigned>(a.num_tokens)), std::min(512, (items + 31) / 32 * 32), 0,
+                stream);
+  return interleaved ? cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, true>, a)
+                     : cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, false>, a);
+}
+
+}  // namespace rope
+
+cudaError_t launch_rope_write(const RopeCall &r, const Geometry &g, cudaStream_t stream) {
+  rope::Args a{};
+  a.q_out = static_cast<uint16_t *>(r.query_out);
+  a.q = static_cast<const uint16_t *>(r.query);
+  a.k = static_cast<const uint16_t *>(r.key);
+  a.v = static_cast<const uint16_t *>(r.value);
+  a.q_out_stride = r.query_out_stride;
+  a.q_stride = r.query_stride;
+  a.k_stride = r.key_stride;
+  a.v_stride = r.value_stride;
+  a.num_tokens = r.num_tokens;
+  a.max_position = r.max_position;
+  a.num_slots = g.num_blocks * g.BS;
+  a.positions = r.positions;
+  a.slots = r.slot_mapping;
+  a.cos_sin = r.cos_sin;
+  a.k_half = static_cast<uint8_t *>(r.kv_cache);
+  a.v_half = a.k_half + g.num_blocks * g.block_bytes;
+  a.row_bytes = g.row_bytes;
+  a.H = g.H;
+  a.KVH = g.KVH;
+  a.rot = r.rot_dim;
+  a.k_scale = g.k_scale;
+  a.v_scale = g.v_scale;
+  const bool bf = g.dtype == PKV_BF16, in = r.interleaved != 0;
+  if (g.D == 128) {
+    if (g.fp8) return bf ? rope::launch_typed<BF16, 128, true>(a, in, stream) : rope::launch_typed<FP16, 128, true>(a, in, stream);
+    return bf ? rope::launch_typed<BF16, 128, false>(a, in, stream) : rope::launch_typed<FP16, 128, false>(a, in, stream);
+  }
+  if (g.D == 64) {
+    if (g.fp8) return bf ? rope::launch_typed<BF16, 64, true>(a, in, stream) : rope::launch_typed<FP16, 64, true>(a, in, stream);
+    return bf ? rope::launch_typed<BF16, 64, false>(a, in, stream) : rope::launch_typed<FP16, 64, false>(a, in, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t read_device_error_rope(unsigned long long *out) { return read_and_clear_unit_error(out); }
+
+}  // namespace pkv
