@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mma.cuh"
 
 namespace pkv {
 namespace sel {
@@ -189,36 +190,6 @@ struct Args {
   int cluster;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();  // the barrier's aligned form wants whole warps
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
-// The 32-bit word at `p` of CTA `rank`'s shared memory.
-__device__ __forceinline__ uint32_t cluster_load(const void *p, uint32_t rank) {
-  uint32_t v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-      "ld.shared::cluster.u32 %0, [a];\n\t}"
-      : "=r"(v)
-      : "r"(smem_u32(p)), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // Order-preserving 64-bit key of a score: NaN counts as +infinity, -0 as 0.
 __device__ __forceinline__ unsigned long long key_of(double s) {
   if (s != s) s = INFINITY;
@@ -283,27 +254,6 @@ __device__ __forceinline__ double exact_score(const uint8_t *row, const float *q
     best = s > best ? s : best;
   }
   return nan ? INFINITY : best;
-}
-
-// D[16x8] = A[16x16] B[16x8], fp32 accumulate from zero.
-template <class MT>
-__device__ __forceinline__ void mma_from_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint2 b);
-template <>
-__device__ __forceinline__ void mma_from_zero<BF16>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                    uint32_t a2, uint32_t a3, uint2 b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(0.f));
-}
-template <>
-__device__ __forceinline__ void mma_from_zero<FP16>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                    uint32_t a2, uint32_t a3, uint2 b) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(0.f));
 }
 
 // acc = max(acc, |w|) on packed pairs (a NaN is left out: its score tells).
@@ -515,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
             mb = max_abs<MT>(max_abs<MT>(mb, f1[0]), f1[1]);
           }
           float d[4];
-          mma_from_zero<MT>(d, f0[0], f1[0], f0[1], f1[1], h8 == 0 ? bq[s] : sb[(h8 * kSteps + s) * 32 + lane]);
+          const uint2 q2 = h8 == 0 ? bq[s] : sb[(h8 * kSteps + s) * 32 + lane];
+          mma_16816<MT>(d, f0[0], f1[0], f0[1], f1[1], q2.x, q2.y, 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 4; ++k) c[k] += d[k];
         }

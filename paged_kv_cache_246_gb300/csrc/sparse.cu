@@ -4,107 +4,603 @@
 // over the keys j of the selected blocks with j <= i = L - 1 inside the
 // sliding window.
 //
-// The plain form of it: CTA = (query head, sequence), a warp takes every
-// fourth selected block key by key, a lane D / 32 channels; one pass with the
-// running maximum and sum of the softmax, the warps merged at the end.
+// Bound by reading the selected keys and values (2 D elements per key and KV
+// head).  A group's query heads are rows of one m16 tile of mma.sync, so they
+// share every byte of K and V; tcgen05's smallest tile, 64 rows, would be
+// mostly empty.  CTA = (part of the selection, KV head x 16 rows, sequence), 4
+// warps, each walking its own 16-key units (a block is one or two) through a
+// two-stage ring of TMA boxes (16 keys x 64 channels, 128-byte swizzle; K and
+// V), one pass with the running maximum (moved, and the output rescaled, only
+// when a score passes it by 2^8) and sum of the softmax.  The lane that will
+// need it loads a unit's block number and place, 32 units of a warp at a time,
+// so there is no table in shared memory and no limit to the selection's length.
+//
+// The parts of one selection are a cluster: their (m, l, O) are joined through
+// distributed shared memory, every CTA writing a share of the output.  No
+// second kernel, no workspace, and the same order of additions every time.
+//
+// Over an fp8 cache the boxes carry the codes.  q.k runs on them as they are:
+// each query row scaled by a power of two and split into two E4M3 terms (four
+// rows or fewer: both terms in one product, the low ones as rows 4 .. 7), the
+// channels taken in an order in which a lane's 16-byte chunk of a key is its
+// own fragment.  p.V runs transposed on fp16 operands: the weights' fragments
+// are the B operand, V^T is built from the codes by byte permutes.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
+#include "mma.cuh"
 
 namespace pkv {
 namespace sparse {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 16;    // keys per unit (one TMA box height)
+constexpr int kRows = 16;    // query heads per CTA: one m16 tile
+constexpr int kStages = 2;   // of a warp's ring
+constexpr float kLazy = 8.f;
+constexpr int kFar = 0x40000000;  // "position" of a unit that nothing may read
 
 struct Args {
   void *out;
   const uint16_t *query;
-  const uint8_t *cache;
   const int32_t *block_tables, *seq_lens, *selected;
   const float *alibi;
-  int64_t num_blocks, half_bytes;
+  int64_t num_blocks;
   int max_blocks_per_seq, max_selected, H, KVH, QPK, BS, window;
+  int row_groups, parts;
   float scale_log2, v_scale;
 };
 
-template <class T, int D, bool KV8>
-__device__ __forceinline__ float element(const uint8_t *row, int d) {
-  if constexpr (KV8) {
-    return FP16::to_f2(e4m3x4_to_h4(row[d]).x).x;
-  } else {
-    return T::to_f(reinterpret_cast<const uint16_t *>(row)[d]);
+template <int D, bool KV8>
+struct Lay {
+  static constexpr int BOX = kUnit * 128;     // 16 rows x 64 channels x 2 B
+  static constexpr int V16 = (D / 64) * BOX;  // one unit of K or V as 16-bit values
+  static constexpr int TILE = KV8 ? kUnit * D : V16;
+  static constexpr int STAGE = 2 * TILE;
+  // the warps' rings, then (16-bit cache) a zero V tile; the merge reuses it
+  static constexpr int ZERO = kWarps * kStages * STAGE;
+  static constexpr int MERGE = (kWarps + 1) * kRows * (D + 2) * 4;
+  static constexpr int RING = ZERO + (KV8 ? 0 : V16);
+  static constexpr int SMEM = 1024 + (RING > MERGE ? RING : MERGE);
+};
+
+// Byte offset of 16-byte chunk `chunk` (8 channels) of key row `tok` in a
+// 16-bit tile: 64-channel box, row, 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz16(int tok, int chunk) {
+  return static_cast<uint32_t>((chunk >> 3) * (kUnit * 128) + tok * 128 +
+                               (((chunk & 7) ^ (tok & 7)) << 4));
+}
+// The same in a tile of codes (D bytes a row; 128- or 64-byte swizzle).
+template <int D>
+__device__ __forceinline__ uint32_t swz8(int row, int chunk) {
+  if constexpr (D == 128)
+    return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+  else
+    return static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+// Bytes {a[j], b[j], a[j+1], b[j+1]}, j = 0 or 2.
+__device__ __forceinline__ uint32_t interleave2(uint32_t a, uint32_t b, int j) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(j ? 0x7362u : 0x5140u));
+  return r;
+}
+
+// HALF: 8 rows or fewer, rows 8 .. 15 of the tile are not kept.
+template <class T, int D, bool KV8, bool HALF>
+__global__ void __launch_bounds__(kThreads, KV8 && HALF ? 4 : 3)
+sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
+  using L_ = Lay<D, KV8>;
+  using MT = std::conditional_t<KV8, FP16, T>;  // type of the weights and of V
+  constexpr int NR = HALF ? 1 : 2;              // row halves a lane keeps (g, g + 8)
+  constexpr int KS = D / 16, NT = D / 8, KS8 = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ int spos[kWarps][kStages];  // position of a stage's first key
+  __shared__ int s_valid;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x;
+  const int kvh = blockIdx.y / a.row_groups, rg = blockIdx.y % a.row_groups;
+  const int b = blockIdx.z;
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmap);
+    s_valid = 0;
   }
+  uint64_t *wbar = bars[warp];
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(&wbar[st], 1);
+    fence_mbar_init();
+  }
+  if constexpr (!KV8)
+    for (int i = threadIdx.x; i < L_::V16 / 16; i += kThreads)
+      reinterpret_cast<uint4 *>(smem + L_::ZERO)[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  int L = __ldg(a.seq_lens + b);
+  if (L < 0 || L > static_cast<int64_t>(a.max_blocks_per_seq) * a.BS) {
+    if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
+    L = 0;
+  }
+  const int i_pos = L - 1, lo = a.window > 0 ? max(0, L - a.window) : 0;
+  const int nblk = (L + a.BS - 1) / a.BS;
+
+  // ---- the selection: how many of its places are used -------------------------
+  const int64_t sel0 = (static_cast<int64_t>(b) * a.KVH + kvh) * a.max_selected;
+  const int32_t *sel = a.selected + sel0;
+  const int32_t *table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
+  if (L > 0) {
+    int count = 0;
+    for (int i = threadIdx.x; i < a.max_selected; i += kThreads) {
+      const int s = __ldg(sel + i);
+      if (s < 0) continue;
+      ++count;
+      if (part == 0 && rg == 0) {
+        const int prev = i ? __ldg(sel + i - 1) : -1;
+        if (s >= nblk || (i && (prev < 0 || prev >= s))) record_error(PKV_ERR_BOUNDS, sel0 + i);
+      }
+    }
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0 && count) atomicAdd(&s_valid, count);
+  }
+  __syncthreads();
+  const int upb = a.BS / kUnit;
+  const int units = s_valid * upb;
+  const int per = (units + a.parts - 1) / a.parts;
+  const int u_begin = min(part * per, units), nu = min(per, units - u_begin);
+  const int my_count = nu > warp ? (nu - warp + kWarps - 1) / kWarps : 0;
+
+  // unit i of this warp: cache row and position of its first key
+  auto place = [&](int i, int &row, int &pos) {
+    row = 0;
+    pos = kFar;
+    if (i >= my_count) return;
+    const int u = u_begin + warp + i * kWarps;
+    const int s = __ldg(sel + u / upb);
+    if (s < 0 || s >= nblk) return;  // a bad selection, recorded above
+    const int pb = __ldg(table + s);
+    if (pb < 0 || pb >= a.num_blocks) {
+      record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(b) * a.max_blocks_per_seq + s);
+      return;
+    }
+    row = pb * a.BS + (u % upb) * kUnit;
+    pos = s * a.BS + (u % upb) * kUnit;
+  };
+  int row_c, pos_c, row_n, pos_n;  // this lane's unit of the 32 being issued, of the next 32
+  place(lane, row_c, pos_c);
+  place(32 + lane, row_n, pos_n);
+  uint8_t *wt = smem + warp * kStages * L_::STAGE;
+  int issued = 0;
+  auto issue = [&]() {  // by the whole warp
+    const int k = issued++;
+    const int row = __shfl_sync(0xffffffffu, row_c, k & 31);
+    const int pos = __shfl_sync(0xffffffffu, pos_c, k & 31);
+    if (lane == 0) {
+      const int st = k % kStages;
+      spos[warp][st] = pos;
+      mbar_arrive_expect_tx(&wbar[st], 2u * L_::TILE);
+      uint8_t *kt = wt + st * L_::STAGE;
+      if constexpr (KV8) {
+        tma_load_4d(kt, &tmap, &wbar[st], 0, kvh, row, 0);
+        tma_load_4d(kt + L_::TILE, &tmap, &wbar[st], 0, kvh, row, 1);
+      } else {
+#pragma unroll
+        for (int r = 0; r < D / 64; ++r) {
+          tma_load_4d(kt + r * L_::BOX, &tmap, &wbar[st], 64 * r, kvh, row, 0);
+          tma_load_4d(kt + L_::TILE + r * L_::BOX, &tmap, &wbar[st], 64 * r, kvh, row, 1);
+        }
+      }
+    }
+    if ((k & 31) == 31) {
+      row_c = row_n;
+      pos_c = pos_n;
+      place(k + 33 + lane, row_n, pos_n);
+    }
+  };
+  while (issued < min(kStages, my_count)) issue();
+
+  // ---- query fragments -----------------------------------------------------------
+  const int g = lane >> 2, tq = lane & 3;
+  bool valid[2];
+  int head[2];
+  float slope[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = rg * kRows + g + 8 * x;
+    valid[x] = x < NR && r < a.QPK;
+    head[x] = kvh * a.QPK + (valid[x] ? r : 0);
+    slope[x] = a.alibi && valid[x] ? __ldg(a.alibi + head[x]) * kLog2e : 0.f;
+  }
+  const uint16_t *qb = a.query + static_cast<int64_t>(b) * a.H * D;
+  uint32_t qa[KS][4];
+  float sl2 = a.scale_log2;
+  const bool fold = KV8 && HALF && a.QPK - rg * kRows <= 4;
+  if constexpr (KV8) {
+    // qa[s] = high, qa[KS8 + s] = low terms of k-step s: this lane's channels
+    // tq * D / 4 + 8 s .. + 7
+    const int srow = rg * kRows + (fold ? (g & 3) : g);
+    const bool src_valid = srow < a.QPK;
+    const int src_head = kvh * a.QPK + (src_valid ? srow : 0);
+    auto chunk = [&](int x, int s) -> uint4 {
+      const int h = x == 0 ? src_head : head[1];
+      const bool v = x == 0 ? src_valid : valid[1];
+      const uint4 *p = reinterpret_cast<const uint4 *>(qb + h * D + tq * (D / 4));
+      return v ? __ldg(p + s) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint32_t am = 0;  // largest |q| of the tile, as bits
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int s = 0; s < KS8; ++s) {
+        const uint4 u = chunk(x, s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = T::to_f2(word_of(u, k));
+          am = max(am, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+        }
+      }
+    am = __reduce_max_sync(0xffffffffu, am);
+    const int E = static_cast<int>(am >> 23);
+    const int e = E == 0 ? 0 : min(64, max(-64, E - 134));  // largest * 2^-e in [2^7, 2^8)
+    const float mul = __int_as_float((127 - e) << 23);
+    sl2 *= __int_as_float((127 + e) << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) qa[s][c] = 0u;
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int s = 0; s < KS8; ++s) {
+        const uint4 u = chunk(x, s);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = T::to_f2(word_of(u, k));
+          v[2 * k] = f.x * mul;
+          v[2 * k + 1] = f.y * mul;
+        }
+        split_e4m3x4(v[0], v[1], v[2], v[3], qa[s][x], qa[KS8 + s][x]);
+        split_e4m3x4(v[4], v[5], v[6], v[7], qa[s][2 + x], qa[KS8 + s][2 + x]);
+        if (x == 0 && fold && g >= 4) {  // rows 4 .. 7 hold the low terms
+          qa[s][0] = qa[KS8 + s][0];
+          qa[s][2] = qa[KS8 + s][2];
+        }
+      }
+  } else {
+    const uint32_t *q0 = reinterpret_cast<const uint32_t *>(qb + head[0] * D);
+    const uint32_t *q1 = reinterpret_cast<const uint32_t *>(qb + head[1] * D);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      qa[s][0] = valid[0] ? __ldg(q0 + 8 * s + tq) : 0u;
+      qa[s][1] = valid[1] ? __ldg(q1 + 8 * s + tq) : 0u;
+      qa[s][2] = valid[0] ? __ldg(q0 + 8 * s + 4 + tq) : 0u;
+      qa[s][3] = valid[1] ? __ldg(q1 + 8 * s + 4 + tq) : 0u;
+    }
+  }
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // 16-bit cache: o[n][2 x + c] of row g + 8 x, channels 8 n + 2 tq + c.
+  // fp8: the same registers as transposed tiles ot[mt][nt][c]
+  float o[NT][2 * NR];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2 * NR; ++c) o[n][c] = 0.f;
+  float(&ot)[KS][NR][4] = *reinterpret_cast<float(*)[KS][NR][4]>(&o[0][0]);
+  const bool has_alibi = a.alibi != nullptr;
+  const int mi = lane >> 3, rr = lane & 7;
+  const int k_tok = (mi >> 1) * 8 + rr, k_half = mi & 1;  // ldmatrix rows of K
+  const int v_tok = (mi & 1) * 8 + rr, v_half = mi >> 1;  // and of V^T
+  bool ok = true;
+  int consumed = 0;
+
+  for (int k = 0; k < my_count; ++k) {
+    const int st = k % kStages;
+    const bool got = mbar_wait_bounded(&wbar[st], (k / kStages) & 1, b);
+    if (!__all_sync(0xffffffffu, got)) {
+      ok = false;
+      break;
+    }
+    consumed = k + 1;
+    const uint8_t *tile = wt + st * L_::STAGE;
+    const uint32_t kt = smem_u32(tile);
+    const int j0 = spos[warp][st];
+
+    // ---- S = Q K^T: two n-tiles of 8 keys, even and odd k-steps apart --------------
+    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if constexpr (KV8) {
+      constexpr int KC = D / 64;
+      uint4 kk[2][KC];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+          kk[n][c] = *reinterpret_cast<const uint4 *>(tile + swz8<D>(g + 8 * n, tq * KC + c));
+#pragma unroll
+      for (int s = 0; s < KS8; ++s)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t b0 = word_of(kk[n][(2 * s) / 4], (2 * s) % 4);
+          const uint32_t b1 = word_of(kk[n][(2 * s + 1) / 4], (2 * s + 1) % 4);
+          auto mul = [&](float(&c)[4], const uint32_t(&q)[4]) {
+            mma_16832_e4m3(c, q[0], HALF ? 0u : q[1], q[2], HALF ? 0u : q[3], b0, b1, c[0], c[1],
+                           HALF ? 0.f : c[2], HALF ? 0.f : c[3]);
+          };
+          if (HALF && fold) {
+            mul((s & 1) ? sd[n] : sc[n], qa[s]);
+          } else {
+            mul(sc[n], qa[s]);
+            mul(sd[n], qa[KS8 + s]);
+          }
+        }
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        uint32_t kb[4];
+        ldmatrix_x4(kt + swz16(k_tok, 2 * s + k_half), kb);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float(&c)[4] = (s & 1) ? sd[n] : sc[n];
+          mma_16816<MT>(c, qa[s][0], HALF ? 0u : qa[s][1], qa[s][2], HALF ? 0u : qa[s][3],
+                        kb[2 * n], kb[2 * n + 1], c[0], c[1], HALF ? 0.f : c[2],
+                        HALF ? 0.f : c[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int c = 0; c < 2 * NR; ++c) sc[n][c] += sd[n][c];
+    if constexpr (KV8 && HALF) {
+      if (fold) {  // row g + 4 holds row g's low terms
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) sc[n][c] += __shfl_xor_sync(0xffffffffu, sc[n][c], 16);
+      }
+    }
+    // ---- scores in the log2 domain, masked -------------------------------------------
+    // sc[n][2 r + c]: row g + 8 r, key j0 + 8 n + 2 tq + c
+    const bool interior = j0 >= lo && j0 + kUnit <= L;
+    float x[2][4];
+    bool grow = false;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int j = j0 + 8 * n + 2 * tq + c;
+          float v = sc[n][2 * r + c] * sl2;
+          if (has_alibi) v = fmaf(slope[r], static_cast<float>(j - i_pos), v);
+          if (!interior && (j < lo || j >= L)) v = -INFINITY;
+          x[r][2 * n + c] = v;
+          grow |= v > m[r] + kLazy;
+        }
+    if (__any_sync(0xffffffffu, grow)) {
+      float al[2] = {1.f, 1.f};
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float mx = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], mx);
+        if (mn > m[r]) {
+          al[r] = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mn);
+          m[r] = mn;
+          l[r] *= al[r];
+          if constexpr (!KV8) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[n][2 * r] *= al[r];
+              o[n][2 * r + 1] *= al[r];
+            }
+          }
+        }
+      }
+      if constexpr (KV8) {
+        // O^T's columns are rows 8 nt + 2 tq, + 1, which lanes 8 tq, 8 tq + 4 own
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+          const float a0 = __shfl_sync(0xffffffffu, al[nt], 8 * tq);
+          const float a1 = __shfl_sync(0xffffffffu, al[nt], 8 * tq + 4);
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            ot[mt][nt][0] *= a0;
+            ot[mt][nt][1] *= a1;
+            ot[mt][nt][2] *= a0;
+            ot[mt][nt][3] *= a1;
+          }
+        }
+      }
+    }
+    // ---- weights: rounded to the product's type; their sum l is of the unrounded -----
+    uint32_t pa[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float mr = m[r] == -INFINITY ? 0.f : m[r];
+      float p[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) p[c] = fast_exp2(x[r][c] - mr);
+      l[r] += (p[0] + p[1]) + (p[2] + p[3]);
+      pa[r] = MT::from_f2(p[0], p[1]);
+      pa[2 + r] = MT::from_f2(p[2], p[3]);
+    }
+    // ---- O += P V.  A masked key's V may hold anything, NaN too, and 0 * NaN is
+    // NaN: its row is read as zeros.
+    if constexpr (KV8) {
+      constexpr int VW = D / 32;  // words of this lane's chunk of a key
+      const uint8_t *vc = tile + L_::TILE;
+      uint32_t vw[4][VW];  // keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const int kr = 2 * tq + (kk & 1) + 8 * (kk >> 1);
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(vc + swz8<D>(kr, g));
+          vw[kk][0] = u.x;
+          vw[kk][1] = u.y;
+          vw[kk][2] = u.z;
+          vw[kk][3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(vc + swz8<D>(kr, g >> 1) + 8 * (g & 1));
+          vw[kk][0] = u.x;
+          vw[kk][1] = u.y;
+        }
+        if (!interior && (j0 + kr < lo || j0 + kr >= L)) {
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vw[kk][w] = 0u;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const int w = mt >> 1, j = (mt & 1) * 2;
+        const uint2 h01 = e4m3x4_to_h4(interleave2(vw[0][w], vw[1][w], j));
+        const uint2 h89 = e4m3x4_to_h4(interleave2(vw[2][w], vw[3][w], j));
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+          float(&c)[4] = ot[mt][nt];
+          mma_16816<FP16>(c, h01.x, h01.y, h89.x, h89.y, pa[nt], pa[2 + nt], c[0], c[1], c[2],
+                          c[3]);
+        }
+      }
+    } else {
+      uint32_t vt = kt + L_::TILE;
+      if (!interior && (j0 + v_tok < lo || j0 + v_tok >= L)) vt = smem_u32(smem + L_::ZERO);
+#pragma unroll
+      for (int n2 = 0; n2 < NT / 2; ++n2) {
+        uint32_t vb[4];
+        ldmatrix_x4_trans(vt + swz16(v_tok, 2 * n2 + v_half), vb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float c[4] = {o[2 * n2 + i][0], o[2 * n2 + i][1], 0.f, 0.f};
+          if constexpr (!HALF) {
+            c[2] = o[2 * n2 + i][2];
+            c[3] = o[2 * n2 + i][3];
+          }
+          mma_16816<MT>(c, pa[0], HALF ? 0u : pa[1], pa[2], HALF ? 0u : pa[3], vb[2 * i],
+                        vb[2 * i + 1], c[0], c[1], c[2], c[3]);
+          o[2 * n2 + i][0] = c[0];
+          o[2 * n2 + i][1] = c[1];
+          if constexpr (!HALF) {
+            o[2 * n2 + i][2] = c[2];
+            o[2 * n2 + i][3] = c[3];
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage: refill it
+    if (issued < my_count) issue();
+  }
+  if (!ok)  // this warp's copies still in flight
+    for (int k = consumed; k < issued; ++k) mbar_wait_bounded(&wbar[k % kStages], (k / kStages) & 1, b);
+
+  // ---- the warps' (m, l, O) joined, then the cluster's --------------------------------
+#pragma unroll
+  for (int r = 0; r < NR; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  __syncthreads();  // all copies have landed: the rings are free
+  float *sm = reinterpret_cast<float *>(smem);   // [kWarps + 1][row]: the warps', the CTA's
+  float *sl = sm + (kWarps + 1) * kRows;          // [kWarps + 1][row]
+  float *so = sl + (kWarps + 1) * kRows;          // [kWarps + 1][row][D]
+  if (tq == 0) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sm[warp * kRows + g + 8 * r] = ok ? m[r] : -INFINITY;
+      sl[warp * kRows + g + 8 * r] = ok ? l[r] : 0.f;
+    }
+  }
+  if constexpr (KV8) {
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
+        float *p = so + (warp * kRows + 8 * nt + 2 * tq) * D + (D == 128 ? 16 : 8) * g + 2 * mt;
+        p[0] = ot[mt][nt][0];
+        p[D] = ot[mt][nt][1];
+        p[1] = ot[mt][nt][2];
+        p[D + 1] = ot[mt][nt][3];
+      }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float *p = so + (warp * kRows + g) * D + 8 * n + 2 * tq;
+      p[0] = o[n][0];
+      p[1] = o[n][1];
+      if constexpr (!HALF) {
+        p[8 * D] = o[n][2];
+        p[8 * D + 1] = o[n][3];
+      }
+    }
+  }
+  __syncthreads();
+  const int rows = min(a.QPK - rg * kRows, kRows);
+  uint16_t *out = static_cast<uint16_t *>(a.out) +
+                  (static_cast<int64_t>(b) * a.H + kvh * a.QPK + rg * kRows) * D;
+  for (int i = threadIdx.x; i < rows * D; i += kThreads) {
+    const int r = i / D;
+    float M = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * kRows + r]);
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float e = fast_exp2(sm[w * kRows + r] - M);
+        num = fmaf(e, so[(w * kRows) * D + i], num);
+        den = fmaf(e, sl[w * kRows + r], den);
+      }
+    }
+    if (a.parts == 1) {
+      const float v = den == 0.f ? 0.f : num / den * a.v_scale;
+      out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
+    } else {
+      so[kWarps * kRows * D + i] = num;
+      if (i % D == 0) {
+        sm[kWarps * kRows + r] = M;
+        sl[kWarps * kRows + r] = den;
+      }
+    }
+  }
+  if (a.parts == 1) return;
+  cluster_sync();
+  for (int i = part * kThreads + threadIdx.x; i < rows * D; i += a.parts * kThreads) {
+    const int r = i / D;
+    float M = -INFINITY, num = 0.f, den = 0.f;
+    for (int c = 0; c < a.parts; ++c) M = fmaxf(M, cluster_loadf(sm + kWarps * kRows + r, c));
+    if (M != -INFINITY) {
+      for (int c = 0; c < a.parts; ++c) {
+        const float e = fast_exp2(cluster_loadf(sm + kWarps * kRows + r, c) - M);
+        num = fmaf(e, cluster_loadf(so + kWarps * kRows * D + i, c), num);
+        den = fmaf(e, cluster_loadf(sl + kWarps * kRows + r, c), den);
+      }
+    }
+    const float v = den == 0.f ? 0.f : num / den * a.v_scale;
+    out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
+  }
+  cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
 template <class T, int D, bool KV8>
-__global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const Args a) {
-  constexpr int E = D / 32;
-  constexpr int EB = KV8 ? 1 : 2;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int h = blockIdx.x, b = blockIdx.y, kvh = h / a.QPK;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int L = __ldg(a.seq_lens + b);
-  if (L < 0 || L > static_cast<int64_t>(a.max_blocks_per_seq) * a.BS) {
-    if (h == 0 && threadIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
-    L = 0;
-  }
-  const int nblk = (L + a.BS - 1) / a.BS, lo = a.window > 0 ? max(0, L - a.window) : 0;
-  const int64_t row0 = (static_cast<int64_t>(b) * a.KVH + kvh) * a.max_selected;
-  const float slope = a.alibi ? __ldg(a.alibi + h) * kLog2e : 0.f;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = T::to_f(a.query[(static_cast<int64_t>(b) * a.H + h) * D + lane + 32 * e]);
-    o[e] = 0.f;
-  }
-  for (int i = warp; i < a.max_selected; i += kWarps) {
-    const int s = __ldg(a.selected + row0 + i), prev = i ? __ldg(a.selected + row0 + i - 1) : -1;
-    if (s < 0 || L == 0) continue;
-    if (s >= nblk || (i && (prev < 0 || prev >= s))) {
-      if (lane == 0) record_error(PKV_ERR_BOUNDS, row0 + i);
-      continue;
-    }
-    const int64_t at = static_cast<int64_t>(b) * a.max_blocks_per_seq + s;
-    const int pb = __ldg(a.block_tables + at);
-    if (pb < 0 || pb >= a.num_blocks) {
-      if (lane == 0) record_error(PKV_ERR_BOUNDS, at);
-      continue;
-    }
-    for (int t = 0; t < a.BS; ++t) {
-      const int j = s * a.BS + t;
-      if (j >= L || j < lo) continue;
-      const uint8_t *kr =
-          a.cache + ((static_cast<int64_t>(pb) * a.BS + t) * a.KVH + kvh) * (D * EB);
-      float x = 0.f;
-      for (int e = 0; e < E; ++e) x = fmaf(q[e], element<T, D, KV8>(kr, lane + 32 * e), x);
-      for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-      x = x * a.scale_log2 + slope * static_cast<float>(j - (L - 1));
-      const float mn = fmaxf(m, x);
-      const float al = m == -INFINITY ? 0.f : exp2f(m - mn), p = x == -INFINITY ? 0.f : exp2f(x - mn);
-      m = mn;
-      l = l * al + p;
-      for (int e = 0; e < E; ++e)
-        o[e] = fmaf(p, element<T, D, KV8>(kr + a.half_bytes, lane + 32 * e), o[e] * al);
-    }
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
-  __syncthreads();
-  float M = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float num = 0.f, den = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float e = sl[w] == 0.f ? 0.f : exp2f(sm[w] - M);
-      num = fmaf(e, so[w][d], num);
-      den = fmaf(e, sl[w], den);
-    }
-    static_cast<uint16_t *>(a.out)[(static_cast<int64_t>(b) * a.H + h) * D + d] =
-        static_cast<uint16_t>(T::from_f2(den == 0.f ? 0.f : num / den * a.v_scale, 0.f) & 0xffffu);
-  }
+static cudaError_t launch_typed(const Args &a, const CUtensorMap &tmap, int num_seqs,
+                                cudaStream_t stream) {
+  auto kern = a.QPK <= kRows / 2 ? sparse_kernel<T, D, KV8, true> : sparse_kernel<T, D, KV8, false>;
+  constexpr int smem = Lay<D, KV8>::SMEM;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch cfg(dim3(a.parts, a.KVH * a.row_groups, num_seqs), kThreads, smem, stream, a.parts);
+  return cudaLaunchKernelEx(&cfg.c, kern, a, tmap);
 }
 
 }  // namespace sparse
@@ -113,16 +609,35 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
                                  const int32_t *block_tables, int max_blocks_per_seq,
                                  const int32_t *seq_lens, const int32_t *selected,
                                  int max_selected, const Geometry &g, cudaStream_t stream) {
+  DeviceInfo dev;
+  cudaError_t e = current_device_info(&dev);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tmap;
+  const cuuint64_t eb = static_cast<cuuint64_t>(g.elem_bytes);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(g.D), static_cast<cuuint64_t>(g.KVH),
+                              static_cast<cuuint64_t>(g.num_blocks * g.BS), 2};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(g.D) * eb,
+                                 static_cast<cuuint64_t>(g.row_bytes),
+                                 static_cast<cuuint64_t>(g.num_blocks * g.block_bytes)};
+  const cuuint32_t box[4] = {g.fp8 ? static_cast<cuuint32_t>(g.D) : 64u, 1,
+                             static_cast<cuuint32_t>(sparse::kUnit), 1};
+  const bool bf = g.dtype == PKV_BF16;
+  const CUtensorMapDataType dt =
+      g.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : (bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+  const CUtensorMapSwizzle swz =
+      !g.fp8 || g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (encode_tensor_map(&tmap, dt, 4, const_cast<void *>(kv_cache), dims, strides, box, swz) !=
+      CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   sparse::Args a{};
   a.out = out;
   a.query = static_cast<const uint16_t *>(query);
-  a.cache = static_cast<const uint8_t *>(kv_cache);
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
   a.selected = selected;
   a.alibi = g.alibi;
   a.num_blocks = g.num_blocks;
-  a.half_bytes = g.num_blocks * g.block_bytes;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_selected = max_selected;
   a.H = g.H;
@@ -130,14 +645,18 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
   a.QPK = g.QPK;
   a.BS = g.BS;
   a.window = g.window;
+  a.row_groups = (g.QPK + sparse::kRows - 1) / sparse::kRows;
   a.scale_log2 = g.scale * kLog2e * g.k_scale;
   a.v_scale = g.v_scale;
-  PdlLaunch cfg(dim3(g.H, num_seqs), sparse::kWarps * 32, 0, stream);
-  const bool bf = g.dtype == PKV_BF16;
-#define PKV_SP(TT, DD)                                                            \
-  if (g.D == DD)                                                                  \
-    return g.fp8 ? cudaLaunchKernelEx(&cfg.c, sparse::sparse_kernel<TT, DD, true>, a) \
-                 : cudaLaunchKernelEx(&cfg.c, sparse::sparse_kernel<TT, DD, false>, a);
+  const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH * a.row_groups;
+  const int64_t units =
+      static_cast<int64_t>(std::min(max_selected, max_blocks_per_seq)) * (g.BS / sparse::kUnit);
+  a.parts = 1;
+  while (a.parts < 8 && items * a.parts < 8LL * dev.sms && units / a.parts >= 16) a.parts *= 2;
+#define PKV_SP(TT, DD)                                                                \
+  if (g.D == DD)                                                                      \
+    return g.fp8 ? sparse::launch_typed<TT, DD, true>(a, tmap, num_seqs, stream)      \
+                 : sparse::launch_typed<TT, DD, false>(a, tmap, num_seqs, stream);
   if (bf) {
     PKV_SP(BF16, 128) PKV_SP(BF16, 64)
   } else {
