@@ -508,7 +508,7 @@ pkv_status kv_block_bounds(void *bounds, const void *kv_cache, int64_t num_block
  * than 16384 / head_size query heads.  scale, k_scale and
  * non_causal do not matter.
  */
-#define PKV_SELECT_MAX_BLOCKS 131072
+#define PKV_SELECT_MAX_BLOCKS 32768
 pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, const void *query,
                                     int32_t num_seqs, const void *bounds, int64_t num_blocks,
                                     const int32_t *block_tables, int32_t max_blocks_per_seq,

@@ -21,6 +21,7 @@ PKV_OK, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_BOUNDS, PKV_
 PKV_FP16, PKV_BF16 = 0, 1
 PKV_CACHE_AUTO, PKV_CACHE_FP8_E4M3 = 0, 1
 PKV_DECODE_STATIC_SCRATCH_BYTES = 64 << 20   # include/pkv.h: paged_attn_decode_noalloc's limit
+PKV_SELECT_MAX_BLOCKS = 32768   # include/pkv.h: blocks per sequence of paged_attn_select_blocks
 _DTYPES = {torch.float16: PKV_FP16, torch.bfloat16: PKV_BF16}
 
 # Every function include/pkv.h declares.

@@ -4,6 +4,7 @@
 // Everything here runs on the host; nothing reads device memory.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -480,6 +481,10 @@ pkv_status kv_block_bounds(void *bounds, const void *kv_cache, int64_t num_block
   if (num_seqs < 0 || num_seqs > 65535 || max_new_tokens < 0 || max_blocks_per_seq <= 0)
     return PKV_ERR_INVALID;
   if (num_seqs == 0 || max_new_tokens == 0) return PKV_OK;
+  // 16-byte chunks of a sequence's touched rows are counted in 31 bits
+  if (std::min<int64_t>(max_blocks_per_seq, max_new_tokens / g.BS + 2LL) * (g.row_bytes / 16) >
+      0x7fffff00LL)
+    return PKV_ERR_UNSUPPORTED;
   if (!bounds || !kv_cache || !block_tables || !seq_lens) return PKV_ERR_INVALID;
   if (!aligned(bounds, 16) || !aligned(kv_cache, 16) || !aligned(block_tables, 4) ||
       !aligned(context_lens, 4) || !aligned(seq_lens, 4))

@@ -2,6 +2,7 @@
 is enqueued (CPU only)."""
 import ctypes
 import os
+import re
 
 import pytest
 import torch
@@ -65,6 +66,7 @@ def test_bounds_refusals(lib):
                 dict(ctx=ctypes.c_void_p((1 << 20) + 2))):
         assert _bounds(lib, **bad) == B.PKV_ERR_INVALID, bad
     assert _bounds(lib, _p(block_size=8)) == B.PKV_ERR_UNSUPPORTED
+    assert _bounds(lib, mb=1 << 27, new=0x7fffffff) == B.PKV_ERR_UNSUPPORTED
 
 
 def _select(lib, p=None, **kw):
@@ -81,7 +83,7 @@ def test_select_refusals(lib):
                 dict(recent=0), dict(k=1), dict(k=0, sink=0), dict(sink=0x7fffffff, recent=0x7fffffff)):
         assert _select(lib, **bad) == B.PKV_ERR_INVALID, bad
     assert _select(lib, _p(alibi_slopes=1 << 20)) == B.PKV_ERR_UNSUPPORTED
-    assert _select(lib, maxl=16 * 131072 + 1) == B.PKV_ERR_UNSUPPORTED
+    assert _select(lib, maxl=16 * B.PKV_SELECT_MAX_BLOCKS + 1) == B.PKV_ERR_UNSUPPORTED
     assert _select(lib, _p(num_heads=129, num_kv_heads=1)) == B.PKV_ERR_UNSUPPORTED
 
 
@@ -98,6 +100,12 @@ def test_sparse_refusals(lib):
                 dict(cache=ctypes.c_void_p((1 << 20) + 8))):
         assert _sparse(lib, **bad) == B.PKV_ERR_INVALID, bad
     assert _sparse(lib, _p(dtype=5)) == B.PKV_ERR_UNSUPPORTED
+
+
+def test_select_limit_matches_the_header():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    m = re.search(r"#define PKV_SELECT_MAX_BLOCKS (\d+)", open(os.path.join(root, "include", "pkv.h")).read())
+    assert m and int(m.group(1)) == B.PKV_SELECT_MAX_BLOCKS
 
 
 def test_binding_wants_cuda_tensors():
