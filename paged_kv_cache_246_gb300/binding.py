@@ -392,20 +392,32 @@ def kv_swap_blocks(src_cache: torch.Tensor, dst_cache: torch.Tensor, pairs: torc
 # device that holds their tensors, whichever is current; a stream given by
 # the caller must belong to it.
 # ---------------------------------------------------------------------------
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object made on the way
+
+
+def _current_stream(index: int) -> int:
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _call_on(first: torch.Tensor, others: Sequence[torch.Tensor], stream, where: str, *args):
-    dev = first.device
+    index = first.get_device()
     for t in others:
-        if t.device != dev:
-            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-    if stream is not None and getattr(stream, "device", dev) != dev:
-        raise ValueError(f"{where}: a stream of {stream.device} for tensors on {dev}")
-    fn = getattr(lib(), where)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, _stream(stream))
+        if t.get_device() != index:
+            raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
+    if stream is None:
+        handle = _current_stream(index)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
-    _check(st, where)
+        if getattr(stream, "device", first.device) != first.device:
+            raise ValueError(f"{where}: a stream of {stream.device} for tensors on {first.device}")
+        handle = _stream(stream)
+    fn = getattr(lib(), where)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
+    if st != PKV_OK:
+        raise PkvError(st, where)
 
 
 def _need_model_dtype(t: torch.Tensor, name: str, p: AttnParams) -> None:
@@ -436,12 +448,14 @@ def _row_stride(t: torch.Tensor, name: str, rows: int, row: int, p: AttnParams) 
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.shape != (rows, row):
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != row:
         raise ValueError(f"{name} must be [{rows}, {row}], got {list(t.shape)}")
     _need_model_dtype(t, name, p)
-    if t.stride(1) != 1:
+    stride, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    stride = t.stride(0) if rows > 1 else row
+    if rows <= 1:
+        return row
     if stride < row or stride % 8 != 0:
         raise ValueError(f"{name}'s rows must not overlap and start a multiple of 8 elements apart")
     return stride

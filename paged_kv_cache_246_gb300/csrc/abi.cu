@@ -95,7 +95,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32_t rank,
                            void *base, const cuuint64_t *dims, const cuuint64_t *strides_bytes,
-                           const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
+                           const cuuint32_t *box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion) {
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!g_encode) {
@@ -110,7 +111,7 @@ CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32
   }
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return g_encode(map, dtype, rank, base, dims, strides_bytes, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

@@ -39,7 +39,8 @@ cudaError_t current_device_info(DeviceInfo *out);
 // Driver entry point for cuTensorMapEncodeTiled, resolved once.
 CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, cuuint32_t rank,
                            void *base, const cuuint64_t *dims, const cuuint64_t *strides_bytes,
-                           const cuuint32_t *box, CUtensorMapSwizzle swizzle);
+                           const cuuint32_t *box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // kv_ops.cu
 cudaError_t launch_kv_write(const void *key, const void *value, int64_t num_tokens, void *kv_cache,

@@ -7,8 +7,8 @@
 // Bound by reading the selected keys and values (2 D elements per key and KV
 // head).  A group's query heads are rows of one m16 tile of mma.sync, so they
 // share every byte of K and V; tcgen05's smallest tile, 64 rows, would be
-// mostly empty.  CTA = (part of the selection, KV head x 16 rows, sequence), 4
-// warps, each walking its own 16-key units (a block is one or two) through a
+// mostly empty.  CTA = (part of the selection, KV head x 16 rows, sequence), 3 to
+// 8 warps, each walking its own 16-key units (a block is one or two) through a
 // two-stage ring of TMA boxes (16 keys x 64 channels, 128-byte swizzle; K and
 // V), one pass with the running maximum (moved, and the output rescaled, only
 // when a score passes it by 2^8) and sum of the softmax.  The lane that will
@@ -18,6 +18,11 @@
 // The parts of one selection are a cluster: their (m, l, O) are joined through
 // distributed shared memory, every CTA writing a share of the output.  No
 // second kernel, no workspace, and the same order of additions every time.
+//
+// The tensor map fetches no more of a line than a head's row: with the 256-byte
+// promotion of the dense kernels a 128-byte row brought its neighbour's along (32
+// sequences, 16 KV heads of 64: 69 against 52 us).  Measured: 64 sequences, 128
+// blocks of 16 for each of 8 KV heads of 128, 538 MB in 89 us (6.1 TB/s).
 //
 // Over an fp8 cache the boxes carry the codes.  q.k runs on them as they are:
 // each query row scaled by a power of two and split into two E4M3 terms (four
@@ -35,11 +40,10 @@
 namespace pkv {
 namespace sparse {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 16;    // keys per unit (one TMA box height)
 constexpr int kRows = 16;    // query heads per CTA: one m16 tile
 constexpr int kStages = 2;   // of a warp's ring
+constexpr int kMaxParts = 8;  // CTAs of a cluster
 constexpr float kLazy = 8.f;
 constexpr int kFar = 0x40000000;  // "position" of a unit that nothing may read
 
@@ -54,15 +58,16 @@ struct Args {
   float scale_log2, v_scale;
 };
 
-template <int D, bool KV8>
+template <int D, bool KV8, int W>
 struct Lay {
   static constexpr int BOX = kUnit * 128;     // 16 rows x 64 channels x 2 B
   static constexpr int V16 = (D / 64) * BOX;  // one unit of K or V as 16-bit values
   static constexpr int TILE = KV8 ? kUnit * D : V16;
   static constexpr int STAGE = 2 * TILE;
   // the warps' rings, then (16-bit cache) a zero V tile; the merge reuses it
-  static constexpr int ZERO = kWarps * kStages * STAGE;
-  static constexpr int MERGE = (kWarps + 1) * kRows * (D + 2) * 4;
+  static constexpr int ZERO = W * kStages * STAGE;
+  static constexpr int PAD = D + 8;  // floats of a row of the merge: no bank conflicts
+  static constexpr int MERGE = (W + 1) * kRows * (PAD + 2) * 4;
   static constexpr int RING = ZERO + (KV8 ? 0 : V16);
   static constexpr int SMEM = 1024 + (RING > MERGE ? RING : MERGE);
 };
@@ -91,11 +96,22 @@ __device__ __forceinline__ uint32_t interleave2(uint32_t a, uint32_t b, int j) {
   return r;
 }
 
+// Warps of a CTA: kFew for grids of less than a CTA per SM, else as many as
+// let four to five CTAs share an SM (their copies go on while one starts or
+// joins).
+constexpr int kFew = 8;
+template <int D, bool KV8>
+constexpr int kMany = D == 128 && !KV8 ? 3 : 4;
+// CTAs per SM that registers are kept for (shared memory allows as many).
+template <int D, bool KV8, bool HALF, int W>
+constexpr int kCtasPerSm = W == kFew ? 1 : D == 64 ? (HALF ? 5 : 4) : KV8 && !HALF ? 3 : 4;
+
 // HALF: 8 rows or fewer, rows 8 .. 15 of the tile are not kept.
-template <class T, int D, bool KV8, bool HALF>
-__global__ void __launch_bounds__(kThreads, KV8 && HALF ? 4 : 3)
+template <class T, int D, bool KV8, bool HALF, int W>
+__global__ void __launch_bounds__(32 * W, kCtasPerSm<D, KV8, HALF, W>)
 sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
-  using L_ = Lay<D, KV8>;
+  constexpr int kWarps = W, kThreads = 32 * W;
+  using L_ = Lay<D, KV8, W>;
   using MT = std::conditional_t<KV8, FP16, T>;  // type of the weights and of V
   constexpr int NR = HALF ? 1 : 2;              // row halves a lane keeps (g, g + 8)
   constexpr int KS = D / 16, NT = D / 8, KS8 = D / 32;
@@ -104,16 +120,11 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ int spos[kWarps][kStages];  // position of a stage's first key
-  __shared__ int s_valid;
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x;
   const int kvh = blockIdx.y / a.row_groups, rg = blockIdx.y % a.row_groups;
   const int b = blockIdx.z;
-  if (threadIdx.x == 0) {
-    prefetch_tensormap(&tmap);
-    s_valid = 0;
-  }
+  if (threadIdx.x == 0) prefetch_tensormap(&tmap);
   uint64_t *wbar = bars[warp];
   if (lane == 0) {
     for (int st = 0; st < kStages; ++st) mbar_init(&wbar[st], 1);
@@ -134,39 +145,30 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   const int i_pos = L - 1, lo = a.window > 0 ? max(0, L - a.window) : 0;
   const int nblk = (L + a.BS - 1) / a.BS;
 
-  // ---- the selection: how many of its places are used -------------------------
+  // ---- this part of the selection's places, as 16-key units ------------------------
   const int64_t sel0 = (static_cast<int64_t>(b) * a.KVH + kvh) * a.max_selected;
   const int32_t *sel = a.selected + sel0;
   const int32_t *table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
-  if (L > 0) {
-    int count = 0;
-    for (int i = threadIdx.x; i < a.max_selected; i += kThreads) {
-      const int s = __ldg(sel + i);
-      if (s < 0) continue;
-      ++count;
-      if (part == 0 && rg == 0) {
-        const int prev = i ? __ldg(sel + i - 1) : -1;
-        if (s >= nblk || (i && (prev < 0 || prev >= s))) record_error(PKV_ERR_BOUNDS, sel0 + i);
-      }
-    }
-    count = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0 && count) atomicAdd(&s_valid, count);
-  }
-  __syncthreads();
   const int upb = a.BS / kUnit;
-  const int units = s_valid * upb;
+  const int units = a.max_selected * upb;
   const int per = (units + a.parts - 1) / a.parts;
   const int u_begin = min(part * per, units), nu = min(per, units - u_begin);
-  const int my_count = nu > warp ? (nu - warp + kWarps - 1) / kWarps : 0;
+  const int places = nu > warp ? (nu - warp + kWarps - 1) / kWarps : 0;
 
-  // unit i of this warp: cache row and position of its first key
+  // unit i of this warp: cache row and position of its first key (row -1: no
+  // block is selected there)
   auto place = [&](int i, int &row, int &pos) {
-    row = 0;
+    row = -1;
     pos = kFar;
-    if (i >= my_count) return;
-    const int u = u_begin + warp + i * kWarps;
-    const int s = __ldg(sel + u / upb);
-    if (s < 0 || s >= nblk) return;  // a bad selection, recorded above
+    if (i >= places) return;
+    const int u = u_begin + warp + i * kWarps, e = u / upb;
+    const int s = __ldg(sel + e), prev = e ? __ldg(sel + e - 1) : -1;
+    if (s < 0 || L == 0) return;
+    row = 0;
+    if (s >= nblk || (e && (prev < 0 || prev >= s))) {
+      record_error(PKV_ERR_BOUNDS, sel0 + e);
+      return;
+    }
     const int pb = __ldg(table + s);
     if (pb < 0 || pb >= a.num_blocks) {
       record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(b) * a.max_blocks_per_seq + s);
@@ -175,15 +177,27 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     row = pb * a.BS + (u % upb) * kUnit;
     pos = s * a.BS + (u % upb) * kUnit;
   };
-  int row_c, pos_c, row_n, pos_n;  // this lane's unit of the 32 being issued, of the next 32
+  // this lane's unit of the 32 being issued and of the next 32, and which of
+  // the former are still to come
+  int row_c, pos_c, row_n, pos_n, base = 0;
   place(lane, row_c, pos_c);
   place(32 + lane, row_n, pos_n);
+  uint32_t left = __ballot_sync(0xffffffffu, row_c >= 0);
   uint8_t *wt = smem + warp * kStages * L_::STAGE;
   int issued = 0;
-  auto issue = [&]() {  // by the whole warp
-    const int k = issued++;
-    const int row = __shfl_sync(0xffffffffu, row_c, k & 31);
-    const int pos = __shfl_sync(0xffffffffu, pos_c, k & 31);
+  auto issue = [&]() {  // by the whole warp: the next unit's copies, if there is one
+    while (left == 0 && base + 32 < places) {
+      base += 32;
+      row_c = row_n;
+      pos_c = pos_n;
+      place(base + 32 + lane, row_n, pos_n);
+      left = __ballot_sync(0xffffffffu, row_c >= 0);
+    }
+    if (left == 0) return;
+    const int k = issued++, from = __ffs(left) - 1;
+    left &= left - 1;
+    const int row = __shfl_sync(0xffffffffu, row_c, from);
+    const int pos = __shfl_sync(0xffffffffu, pos_c, from);
     if (lane == 0) {
       const int st = k % kStages;
       spos[warp][st] = pos;
@@ -200,13 +214,8 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         }
       }
     }
-    if ((k & 31) == 31) {
-      row_c = row_n;
-      pos_c = pos_n;
-      place(k + 33 + lane, row_n, pos_n);
-    }
   };
-  while (issued < min(kStages, my_count)) issue();
+  for (int st = 0; st < kStages; ++st) issue();
 
   // ---- query fragments -----------------------------------------------------------
   const int g = lane >> 2, tq = lane & 3;
@@ -304,7 +313,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   bool ok = true;
   int consumed = 0;
 
-  for (int k = 0; k < my_count; ++k) {
+  for (int k = 0; k < issued; ++k) {
     const int st = k % kStages;
     const bool got = mbar_wait_bounded(&wbar[st], (k / kStages) & 1, b);
     if (!__all_sync(0xffffffffu, got)) {
@@ -500,7 +509,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       }
     }
     __syncwarp();  // every lane has read the stage: refill it
-    if (issued < my_count) issue();
+    issue();
   }
   if (!ok)  // this warp's copies still in flight
     for (int k = consumed; k < issued; ++k) mbar_wait_bounded(&wbar[k % kStages], (k / kStages) & 1, b);
@@ -527,22 +536,19 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt) {
-        float *p = so + (warp * kRows + 8 * nt + 2 * tq) * D + (D == 128 ? 16 : 8) * g + 2 * mt;
-        p[0] = ot[mt][nt][0];
-        p[D] = ot[mt][nt][1];
-        p[1] = ot[mt][nt][2];
-        p[D + 1] = ot[mt][nt][3];
+        float *p = so + (warp * kRows + 8 * nt + 2 * tq) * L_::PAD + (D == 128 ? 16 : 8) * g + 2 * mt;
+        if (rg * kRows + 8 * nt + 2 * tq >= a.QPK) continue;
+        *reinterpret_cast<float2 *>(p) = make_float2(ot[mt][nt][0], ot[mt][nt][2]);
+        *reinterpret_cast<float2 *>(p + L_::PAD) = make_float2(ot[mt][nt][1], ot[mt][nt][3]);
       }
   } else {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float *p = so + (warp * kRows + g) * D + 8 * n + 2 * tq;
-      p[0] = o[n][0];
-      p[1] = o[n][1];
-      if constexpr (!HALF) {
-        p[8 * D] = o[n][2];
-        p[8 * D + 1] = o[n][3];
-      }
+      float *p = so + (warp * kRows + g) * L_::PAD + 8 * n + 2 * tq;
+      if (valid[0]) *reinterpret_cast<float2 *>(p) = make_float2(o[n][0], o[n][1]);
+      if constexpr (!HALF)
+        if (valid[1])
+          *reinterpret_cast<float2 *>(p + 8 * L_::PAD) = make_float2(o[n][2], o[n][3]);
     }
   }
   __syncthreads();
@@ -550,7 +556,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   uint16_t *out = static_cast<uint16_t *>(a.out) +
                   (static_cast<int64_t>(b) * a.H + kvh * a.QPK + rg * kRows) * D;
   for (int i = threadIdx.x; i < rows * D; i += kThreads) {
-    const int r = i / D;
+    const int r = i / D, d = i % D;
     float M = -INFINITY, num = 0.f, den = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w * kRows + r]);
@@ -558,7 +564,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float e = fast_exp2(sm[w * kRows + r] - M);
-        num = fmaf(e, so[(w * kRows) * D + i], num);
+        num = fmaf(e, so[(w * kRows + r) * L_::PAD + d], num);
         den = fmaf(e, sl[w * kRows + r], den);
       }
     }
@@ -566,8 +572,8 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       const float v = den == 0.f ? 0.f : num / den * a.v_scale;
       out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
     } else {
-      so[kWarps * kRows * D + i] = num;
-      if (i % D == 0) {
+      so[(kWarps * kRows + r) * L_::PAD + d] = num;
+      if (d == 0) {
         sm[kWarps * kRows + r] = M;
         sl[kWarps * kRows + r] = den;
       }
@@ -576,14 +582,24 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   if (a.parts == 1) return;
   cluster_sync();
   for (int i = part * kThreads + threadIdx.x; i < rows * D; i += a.parts * kThreads) {
-    const int r = i / D;
-    float M = -INFINITY, num = 0.f, den = 0.f;
-    for (int c = 0; c < a.parts; ++c) M = fmaxf(M, cluster_loadf(sm + kWarps * kRows + r, c));
+    const int r = i / D, d = i % D;
+    float pm[kMaxParts], pl[kMaxParts], po[kMaxParts], M = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+    for (int c = 0; c < kMaxParts; ++c) {
+      const uint32_t from = min(c, a.parts - 1);
+      pm[c] = cluster_loadf(sm + kWarps * kRows + r, from);
+      pl[c] = cluster_loadf(sl + kWarps * kRows + r, from);
+      po[c] = cluster_loadf(so + (kWarps * kRows + r) * L_::PAD + d, from);
+    }
+#pragma unroll
+    for (int c = 0; c < kMaxParts; ++c) M = fmaxf(M, pm[c]);
     if (M != -INFINITY) {
-      for (int c = 0; c < a.parts; ++c) {
-        const float e = fast_exp2(cluster_loadf(sm + kWarps * kRows + r, c) - M);
-        num = fmaf(e, cluster_loadf(so + kWarps * kRows * D + i, c), num);
-        den = fmaf(e, cluster_loadf(sl + kWarps * kRows + r, c), den);
+#pragma unroll
+      for (int c = 0; c < kMaxParts; ++c) {
+        if (c >= a.parts) break;
+        const float e = fast_exp2(pm[c] - M);
+        num = fmaf(e, po[c], num);
+        den = fmaf(e, pl[c], den);
       }
     }
     const float v = den == 0.f ? 0.f : num / den * a.v_scale;
@@ -592,15 +608,26 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
-template <class T, int D, bool KV8>
-static cudaError_t launch_typed(const Args &a, const CUtensorMap &tmap, int num_seqs,
-                                cudaStream_t stream) {
-  auto kern = a.QPK <= kRows / 2 ? sparse_kernel<T, D, KV8, true> : sparse_kernel<T, D, KV8, false>;
-  constexpr int smem = Lay<D, KV8>::SMEM;
+template <class T, int D, bool KV8, bool HALF, int W>
+static cudaError_t launch_w(const Args &a, const CUtensorMap &tmap, int num_seqs,
+                            cudaStream_t stream) {
+  auto kern = sparse_kernel<T, D, KV8, HALF, W>;
+  constexpr int smem = Lay<D, KV8, W>::SMEM;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  PdlLaunch cfg(dim3(a.parts, a.KVH * a.row_groups, num_seqs), kThreads, smem, stream, a.parts);
+  PdlLaunch cfg(dim3(a.parts, a.KVH * a.row_groups, num_seqs), 32 * W, smem, stream, a.parts);
   return cudaLaunchKernelEx(&cfg.c, kern, a, tmap);
+}
+
+template <class T, int D, bool KV8>
+static cudaError_t launch_typed(const Args &a, const CUtensorMap &tmap, int num_seqs, bool few,
+                                cudaStream_t stream) {
+  if (few)
+    return a.QPK <= kRows / 2 ? launch_w<T, D, KV8, true, kFew>(a, tmap, num_seqs, stream)
+                              : launch_w<T, D, KV8, false, kFew>(a, tmap, num_seqs, stream);
+  constexpr int W = kMany<D, KV8>;
+  return a.QPK <= kRows / 2 ? launch_w<T, D, KV8, true, W>(a, tmap, num_seqs, stream)
+                            : launch_w<T, D, KV8, false, W>(a, tmap, num_seqs, stream);
 }
 
 }  // namespace sparse
@@ -627,8 +654,15 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
             : (bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
   const CUtensorMapSwizzle swz =
       !g.fp8 || g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (encode_tensor_map(&tmap, dt, 4, const_cast<void *>(kv_cache), dims, strides, box, swz) !=
-      CUDA_SUCCESS)
+  // no wider fetches than a head's row: the next head's rows of this block are
+  // read only if it selected the block too
+  const cuuint64_t row = static_cast<cuuint64_t>(g.D) * eb;
+  const CUtensorMapL2promotion promotion =
+      row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+      : row == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                   : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+  if (encode_tensor_map(&tmap, dt, 4, const_cast<void *>(kv_cache), dims, strides, box, swz,
+                        promotion) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   sparse::Args a{};
   a.out = out;
@@ -651,12 +685,24 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
   const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH * a.row_groups;
   const int64_t units =
       static_cast<int64_t>(std::min(max_selected, max_blocks_per_seq)) * (g.BS / sparse::kUnit);
-  a.parts = 1;
-  while (a.parts < 8 && items * a.parts < 8LL * dev.sms && units / a.parts >= 16) a.parts *= 2;
+  // Measured (2048 keys of 8 or 16 KV heads, us): 8-warp CTAs, one to an SM, are
+  // faster up to a CTA per SM (128 items: 26 / 28 and 16 / 17 against the best of
+  // the others), with as many parts as then fit (8 items: 14 / 10 / 8 / 7 in 1 / 2 /
+  // 4 / 8 parts); clusters of 8 such CTAs fit a GPC's SMs badly (16 of them: 13
+  // against 8 in fours).  From there on parts only add prologues and joins (512
+  // items: 90 / 91 / 101 / 116), but for 8-bit caches at half a wave (256 items:
+  // 36 / 32, 16-bit 49 / 50).
+  const bool few = items <= dev.sms;
+  if (few) {
+    a.parts = items * 8 <= dev.sms / 2 ? 8 : items * 4 <= dev.sms ? 4 : items * 2 <= dev.sms ? 2 : 1;
+    while (a.parts > 1 && units < a.parts * sparse::kFew) a.parts /= 2;
+  } else {
+    a.parts = items * 2 <= 4LL * dev.sms ? 2 : 1;
+  }
 #define PKV_SP(TT, DD)                                                                \
   if (g.D == DD)                                                                      \
-    return g.fp8 ? sparse::launch_typed<TT, DD, true>(a, tmap, num_seqs, stream)      \
-                 : sparse::launch_typed<TT, DD, false>(a, tmap, num_seqs, stream);
+    return g.fp8 ? sparse::launch_typed<TT, DD, true>(a, tmap, num_seqs, few, stream)      \
+                 : sparse::launch_typed<TT, DD, false>(a, tmap, num_seqs, few, stream);
   if (bf) {
     PKV_SP(BF16, 128) PKV_SP(BF16, 64)
   } else {
