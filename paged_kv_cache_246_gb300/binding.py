@@ -399,16 +399,19 @@ def _current_stream(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _call_on(first: torch.Tensor, others: Sequence[torch.Tensor], stream, where: str, *args):
-    index = first.get_device()
-    for t in others:
-        if t.get_device() != index:
-            raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
+def _call_on(where: str, stream, tensors: Sequence[torch.Tensor], *args):
+    """The entry point `where` on the device that holds `tensors`."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index or index < 0:
+            raise ValueError(f"{where}: tensors must be on one CUDA device, not "
+                             f"{tensors[0].device} and {t.device}")
     if stream is None:
         handle = _current_stream(index)
     else:
-        if getattr(stream, "device", first.device) != first.device:
-            raise ValueError(f"{where}: a stream of {stream.device} for tensors on {first.device}")
+        if getattr(stream, "device", tensors[0].device) != tensors[0].device:
+            raise ValueError(f"{where}: a stream of {stream.device} for tensors on "
+                             f"{tensors[0].device}")
         handle = _stream(stream)
     fn = getattr(lib(), where)
     if torch.cuda.current_device() == index:
@@ -420,37 +423,54 @@ def _call_on(first: torch.Tensor, others: Sequence[torch.Tensor], stream, where:
         raise PkvError(st, where)
 
 
-def _need_model_dtype(t: torch.Tensor, name: str, p: AttnParams) -> None:
-    if _DTYPES.get(t.dtype) != p.dtype:
-        raise ValueError(f"{name} must have the params' dtype, got {t.dtype}")
+_TORCH_DTYPES = {code: dtype for dtype, code in _DTYPES.items()}
 
 
-def _need_cache_dtype(t: torch.Tensor, name: str, p: AttnParams) -> None:
-    if p.kv_cache_dtype == PKV_CACHE_FP8_E4M3:
-        if t.dtype != torch.uint8:
-            raise ValueError(f"{name} must be torch.uint8 over an fp8 cache, got {t.dtype}")
-    else:
-        _need_model_dtype(t, name, p)
+def _is(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> tuple:
+    """The sizes of a contiguous tensor of this type (its device is checked at the call)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {len(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return shape
 
 
-def _need_batch(block_tables: torch.Tensor, seq_lens: torch.Tensor) -> int:
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    if block_tables.shape[0] != seq_lens.shape[0]:
+def _types(p: AttnParams) -> tuple:
+    """(dtype of queries, keys, values and outputs; dtype of the cache)."""
+    dtype = _TORCH_DTYPES.get(p.dtype)
+    if dtype is None:
+        raise ValueError(f"unsupported params dtype {p.dtype}")
+    return dtype, torch.uint8 if p.kv_cache_dtype == PKV_CACHE_FP8_E4M3 else dtype
+
+
+def _is_cache(t: torch.Tensor, dtype: torch.dtype, p: AttnParams) -> int:
+    two, blocks, elems = _is(t, "kv_cache", dtype, 3)
+    if two != 2 or elems != p.block_size * p.num_kv_heads * p.head_size:
+        raise ValueError("kv_cache must be [2, num_blocks, block_size*num_kv_heads*head_size]")
+    return blocks
+
+
+def _is_batch(block_tables: torch.Tensor, seq_lens: torch.Tensor) -> tuple:
+    n, wide = _is(block_tables, "block_tables", torch.int32, 2)
+    if _is(seq_lens, "seq_lens", torch.int32, 1)[0] != n:
         raise ValueError("block_tables and seq_lens sizes disagree")
-    return seq_lens.shape[0]
+    return n, wide
 
 
-def _row_stride(t: torch.Tensor, name: str, rows: int, row: int, p: AttnParams) -> int:
+def _row_stride(t: torch.Tensor, name: str, rows: int, row: int, dtype: torch.dtype) -> int:
     """Elements between the rows of a [rows, row] tensor whose rows may be
     slices of wider ones."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != row:
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, row):
         raise ValueError(f"{name} must be [{rows}, {row}], got {list(t.shape)}")
-    _need_model_dtype(t, name, p)
     stride, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
@@ -481,35 +501,31 @@ def kv_cache_write_rope(query_out: torch.Tensor, query: torch.Tensor, key: torch
     """kv_cache_write with queries and keys rotated by their positions: rows of
     query, key and value may be slices of one projection's output; query_out
     may be query."""
-    _need(kv_cache, "kv_cache")
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    _need(positions, "positions", torch.int64, 1)
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    nb = _cache_blocks(kv_cache, params)
-    _need_cache_dtype(kv_cache, "kv_cache", params)
-    T = slot_mapping.shape[0]
-    if positions.shape[0] != T:
+    dtype, cache_dtype = _types(params)
+    nb = _is_cache(kv_cache, cache_dtype, params)
+    T = _is(slot_mapping, "slot_mapping", torch.int64, 1)[0]
+    if _is(positions, "positions", torch.int64, 1)[0] != T:
         raise ValueError("positions and slot_mapping sizes disagree")
+    max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
     q_row = params.num_heads * params.head_size
     kv_row = params.num_kv_heads * params.head_size
-    so = _row_stride(query_out, "query_out", T, q_row, params)
-    sq = _row_stride(query, "query", T, q_row, params)
-    sk = _row_stride(key, "key", T, kv_row, params)
-    sv = _row_stride(value, "value", T, kv_row, params)
-    _call_on(kv_cache, (query_out, query, key, value, slot_mapping, positions, cos_sin), stream,
-             "kv_cache_write_rope", query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(),
-             sk, value.data_ptr(), sv, T, positions.data_ptr(), cos_sin.data_ptr(),
-             cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), kv_cache.data_ptr(), nb,
-             slot_mapping.data_ptr(), ctypes.byref(params))
+    so = _row_stride(query_out, "query_out", T, q_row, dtype)
+    sq = _row_stride(query, "query", T, q_row, dtype)
+    sk = _row_stride(key, "key", T, kv_row, dtype)
+    sv = _row_stride(value, "value", T, kv_row, dtype)
+    _call_on("kv_cache_write_rope", stream,
+             (kv_cache, query_out, query, key, value, slot_mapping, positions, cos_sin),
+             query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(),
+             sv, T, positions.data_ptr(), cos_sin.data_ptr(), max_position, rot_dim,
+             1 if interleaved else 0, kv_cache.data_ptr(), nb, slot_mapping.data_ptr(),
+             ctypes.byref(params))
 
 
-def _need_bounds(bounds: torch.Tensor, blocks: Optional[int], p: AttnParams) -> int:
-    _need(bounds, "bounds", None, 4)
-    _need_cache_dtype(bounds, "bounds", p)
-    nb = bounds.shape[0] if blocks is None else blocks
-    if bounds.shape != (nb, p.num_kv_heads, 2, p.head_size):
+def _is_bounds(bounds: torch.Tensor, dtype: torch.dtype, p: AttnParams) -> int:
+    blocks, heads, two, size = _is(bounds, "bounds", dtype, 4)
+    if heads != p.num_kv_heads or two != 2 or size != p.head_size:
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_size]")
-    return nb
+    return blocks
 
 
 def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -517,28 +533,32 @@ def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: 
                     context_lens: Optional[torch.Tensor] = None, stream=None) -> None:
     """Channelwise minima and maxima of the keys of the blocks that hold
     positions context_lens[b] .. seq_lens[b] - 1 (None: all of the sequence)."""
-    _need(kv_cache, "kv_cache")
-    nb = _cache_blocks(kv_cache, params)
-    _need_cache_dtype(kv_cache, "kv_cache", params)
-    _need_bounds(bounds, nb, params)
-    n = _need_batch(block_tables, seq_lens)
-    others = [bounds, block_tables, seq_lens]
+    cache_dtype = _types(params)[1]
+    nb = _is_cache(kv_cache, cache_dtype, params)
+    if _is_bounds(bounds, cache_dtype, params) != nb:
+        raise ValueError("bounds and kv_cache must have the same number of blocks")
+    n, wide = _is_batch(block_tables, seq_lens)
+    tensors, ctx = (kv_cache, bounds, block_tables, seq_lens), None
     if context_lens is not None:
-        _need(context_lens, "context_lens", torch.int32, 1)
-        if context_lens.shape[0] != n:
+        if _is(context_lens, "context_lens", torch.int32, 1)[0] != n:
             raise ValueError("context_lens and seq_lens sizes disagree")
-        others.append(context_lens)
-    _call_on(kv_cache, others, stream, "kv_block_bounds", bounds.data_ptr(), kv_cache.data_ptr(), nb,
-             block_tables.data_ptr(), block_tables.shape[1],
-             None if context_lens is None else context_lens.data_ptr(), seq_lens.data_ptr(), n,
-             int(max_new_tokens), ctypes.byref(params))
+        tensors, ctx = tensors + (context_lens,), context_lens.data_ptr()
+    _call_on("kv_block_bounds", stream, tensors, bounds.data_ptr(), kv_cache.data_ptr(), nb,
+             block_tables.data_ptr(), wide, ctx, seq_lens.data_ptr(), n, int(max_new_tokens),
+             ctypes.byref(params))
 
 
-def _need_selected(selected: torch.Tensor, n: int, p: AttnParams) -> int:
-    _need(selected, "selected", torch.int32, 3)
-    if selected.shape[0] != n or selected.shape[1] != p.num_kv_heads:
+def _is_selected(selected: torch.Tensor, n: int, p: AttnParams) -> int:
+    seqs, heads, k = _is(selected, "selected", torch.int32, 3)
+    if seqs != n or heads != p.num_kv_heads:
         raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
-    return selected.shape[2]
+    return k
+
+
+def _is_rows(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, p: AttnParams) -> None:
+    rows, row = _is(t, name, dtype, 2)
+    if rows != n or row != p.num_heads * p.head_size:
+        raise ValueError(f"{name} must be [num_seqs, num_heads*head_size]")
 
 
 def paged_attn_select_blocks(selected: torch.Tensor, query: torch.Tensor, bounds: torch.Tensor,
@@ -548,17 +568,15 @@ def paged_attn_select_blocks(selected: torch.Tensor, query: torch.Tensor, bounds
     """selected [num_seqs, num_kv_heads, K]: each KV head's K blocks with the
     largest bound on q.k, the first num_sink and last num_recent among them,
     ascending, -1 behind."""
-    nb = _need_bounds(bounds, None, params)
-    _need(query, "query")
-    _need_model_dtype(query, "query", params)
-    n = _need_batch(block_tables, seq_lens)
-    k = _need_selected(selected, n, params)
-    if query.numel() != n * params.num_heads * params.head_size:
-        raise ValueError("query and seq_lens sizes disagree")
-    _call_on(bounds, (selected, query, block_tables, seq_lens), stream, "paged_attn_select_blocks",
+    dtype, cache_dtype = _types(params)
+    nb = _is_bounds(bounds, cache_dtype, params)
+    n, wide = _is_batch(block_tables, seq_lens)
+    k = _is_selected(selected, n, params)
+    _is_rows(query, "query", dtype, n, params)
+    _call_on("paged_attn_select_blocks", stream, (bounds, selected, query, block_tables, seq_lens),
              selected.data_ptr(), k, query.data_ptr(), n, bounds.data_ptr(), nb,
-             block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), int(max_seq_len),
-             int(num_sink), int(num_recent), ctypes.byref(params))
+             block_tables.data_ptr(), wide, seq_lens.data_ptr(), int(max_seq_len), int(num_sink),
+             int(num_recent), ctypes.byref(params))
 
 
 def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor,
@@ -566,21 +584,16 @@ def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: t
                              selected: torch.Tensor, params: AttnParams, stream=None) -> None:
     """paged_attn_decode over the blocks that selected [num_seqs, num_kv_heads,
     K] names for each sequence and KV head (ascending, negative numbers behind)."""
-    for t, name in ((out, "out"), (query, "query")):
-        _need(t, name)
-        _need_model_dtype(t, name, params)
-    _need(kv_cache, "kv_cache")
-    nb = _cache_blocks(kv_cache, params)
-    _need_cache_dtype(kv_cache, "kv_cache", params)
-    n = _need_batch(block_tables, seq_lens)
-    k = _need_selected(selected, n, params)
-    hd = params.num_heads * params.head_size
-    if query.numel() != n * hd or out.numel() != n * hd:
-        raise ValueError("query/out sizes disagree with seq_lens")
-    _call_on(kv_cache, (out, query, block_tables, seq_lens, selected), stream,
-             "paged_attn_decode_sparse", out.data_ptr(), query.data_ptr(), n, kv_cache.data_ptr(),
-             nb, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-             selected.data_ptr(), k, ctypes.byref(params))
+    dtype, cache_dtype = _types(params)
+    nb = _is_cache(kv_cache, cache_dtype, params)
+    n, wide = _is_batch(block_tables, seq_lens)
+    k = _is_selected(selected, n, params)
+    _is_rows(out, "out", dtype, n, params)
+    _is_rows(query, "query", dtype, n, params)
+    _call_on("paged_attn_decode_sparse", stream,
+             (kv_cache, out, query, block_tables, seq_lens, selected), out.data_ptr(),
+             query.data_ptr(), n, kv_cache.data_ptr(), nb, block_tables.data_ptr(), wide,
+             seq_lens.data_ptr(), selected.data_ptr(), k, ctypes.byref(params))
 
 
 def check_wait_timeout(tag: int, stream=None) -> None:
