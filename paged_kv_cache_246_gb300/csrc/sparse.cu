@@ -25,9 +25,11 @@
 // blocks of 16 for each of 8 KV heads of 128, 538 MB in 89 us (6.1 TB/s).
 //
 // Over an fp8 cache the boxes carry the codes.  q.k runs on them as they are:
-// each query row scaled by a power of two and split into two E4M3 terms (four
-// rows or fewer: both terms in one product, the low ones as rows 4 .. 7), the
-// channels taken in an order in which a lane's 16-byte chunk of a key is its
+// each query row scaled by a power of two and split into two E4M3 terms for
+// bf16, three for fp16 (4 bits each: the 8 and 11 bits of a component, exact
+// within 2^10 of the tile's largest and off by 2^-17 of it below); with four
+// rows or fewer the first two in one product, the low ones as rows 4 .. 7.  The
+// channels are taken in an order in which a lane's 16-byte chunk of a key is its
 // own fragment.  p.V runs transposed on fp16 operands: the weights' fragments
 // are the B operand, V^T is built from the codes by byte permutes.
 #include <algorithm>
@@ -102,6 +104,17 @@ __device__ __forceinline__ uint32_t interleave2(uint32_t a, uint32_t b, int j) {
 constexpr int kFew = 8;
 template <int D, bool KV8>
 constexpr int kMany = D == 128 && !KV8 ? 3 : 4;
+// E4M3 codes of what two terms leave of four values.
+__device__ __forceinline__ uint32_t rest_e4m3x4(const float *v, uint32_t hi, uint32_t lo) {
+  const uint2 a = e4m3x4_to_h4(hi), b = e4m3x4_to_h4(lo);
+  const float2 a0 = FP16::to_f2(a.x), a1 = FP16::to_f2(a.y);
+  const float2 b0 = FP16::to_f2(b.x), b1 = FP16::to_f2(b.y);
+  uint32_t c, none;
+  split_e4m3x4(v[0] - a0.x - b0.x, v[1] - a0.y - b0.y, v[2] - a1.x - b1.x, v[3] - a1.y - b1.y, c,
+               none);
+  return c;
+}
+
 // CTAs per SM that registers are kept for (shared memory allows as many).
 template <int D, bool KV8, bool HALF, int W>
 constexpr int kCtasPerSm = W == kFew ? 1 : D == 64 ? (HALF ? 5 : 4) : KV8 && !HALF ? 3 : 4;
@@ -115,6 +128,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   using MT = std::conditional_t<KV8, FP16, T>;  // type of the weights and of V
   constexpr int NR = HALF ? 1 : 2;              // row halves a lane keeps (g, g + 8)
   constexpr int KS = D / 16, NT = D / 8, KS8 = D / 32;
+  constexpr bool kThird = KV8 && std::is_same<T, FP16>::value;  // a third query term
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -230,7 +244,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     slope[x] = a.alibi && valid[x] ? __ldg(a.alibi + head[x]) * kLog2e : 0.f;
   }
   const uint16_t *qb = a.query + static_cast<int64_t>(b) * a.H * D;
-  uint32_t qa[KS][4];
+  uint32_t qa[KS][4], qc[kThird ? KS8 : 1][4];
   float sl2 = a.scale_log2;
   const bool fold = KV8 && HALF && a.QPK - rg * kRows <= 4;
   if constexpr (KV8) {
@@ -266,6 +280,11 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int c = 0; c < 4; ++c) qa[s][c] = 0u;
+    if constexpr (kThird)
+#pragma unroll
+      for (int s = 0; s < KS8; ++s)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) qc[s][c] = 0u;
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -280,6 +299,11 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         }
         split_e4m3x4(v[0], v[1], v[2], v[3], qa[s][x], qa[KS8 + s][x]);
         split_e4m3x4(v[4], v[5], v[6], v[7], qa[s][2 + x], qa[KS8 + s][2 + x]);
+        if constexpr (kThird) {
+          qc[s][x] = rest_e4m3x4(v, qa[s][x], qa[KS8 + s][x]);
+          qc[s][2 + x] = rest_e4m3x4(v + 4, qa[s][2 + x], qa[KS8 + s][2 + x]);
+          if (x == 0 && fold && g >= 4) qc[s][0] = qc[s][2] = 0u;  // rows 0 .. 3 alone
+        }
         if (x == 0 && fold && g >= 4) {  // rows 4 .. 7 hold the low terms
           qa[s][0] = qa[KS8 + s][0];
           qa[s][2] = qa[KS8 + s][2];
@@ -352,6 +376,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
             mul(sc[n], qa[s]);
             mul(sd[n], qa[KS8 + s]);
           }
+          if constexpr (kThird) mul((s & 1) ? sc[n] : sd[n], qc[s]);
         }
     } else {
 #pragma unroll

@@ -74,8 +74,8 @@ def attention_tolerance(s: Scene, out: torch.Tensor, spread: torch.Tensor) -> to
     weights = torch.finfo(torch.float16).eps / 2 if s.fp8 else half
     q = s.query.double().abs().max().item()
     k = 448 * SCALE8 if s.fp8 else s.cache[0].double().nan_to_num(0.0).abs().max().item()
-    # fp32 sums of D products, and over an fp8 cache the query's two E4M3
-    # terms: off by 2^-17 of the row's largest component
+    # fp32 sums of D products, and over an fp8 cache the query's E4M3 terms:
+    # off by 2^-17 of the largest component
     per = s.D * 2.0 ** -24 + (2.0 ** -17 if s.fp8 else 0.0)
     d = s.D ** -0.5 * s.D * q * k * per
     # ALiBi: slope * distance in fp32, and 2^x of the special-function unit

@@ -404,6 +404,31 @@ def test_sparse_reads_nothing_else(fp8):
     within(got.cpu().double(), want, attention_tolerance(s, want, spread), "sparse")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [2, 8, 16])
+@pytest.mark.parametrize("dtype,low", [(FP, 2.0 ** -10), (BF, 2.0 ** -7)])
+def test_sparse_every_bit_of_a_query_counts_over_fp8(dtype, low, heads, D):
+    # q = (1 + low, ..., 1, ...) against keys (c, ..., -c, ...): the ones cancel
+    # and the score is that of the queries' last bits
+    s = Scene([32], heads, 1, D, 16, dtype, fp8=True)
+    q = torch.ones(heads, D)
+    q[:, :D // 2] += low
+    s.query = q.to(dtype).view(1, -1)
+    assert torch.equal(s.query.float().view(heads, D), q)
+    k = torch.zeros(32, D)
+    k[:7, :D // 2], k[:7, D // 2:] = 448.0, -448.0
+    for j in range(2):
+        s.cache[0, int(s.tables[0, j])] = k[16 * j:16 * j + 16].reshape(-1).to(torch.float8_e4m3fn).view(torch.uint8)
+    sel = s.selection(2)
+    got = run_sparse(s, sel)
+    clean("sparse")
+    want, spread = O.paged_attn_decode_sparse(s.query, s.cache, s.tables, s.lens, sel, s.op)
+    # products and their fp32 sums are exact here (powers of two times 7 bits);
+    # the softmax's own arithmetic is fp32: 2^-16 is ample
+    half, weights = torch.finfo(dtype).eps / 2, torch.finfo(FP).eps / 2
+    within(got.cpu().double(), want, 1.01 * (half * want.abs() + (weights + 2.0 ** -16) * spread), "sparse")
+
+
 def test_sparse_climbing_scores():
     # the running maximum moves at every block, by far more than any slack
     s = Scene([640], 2, 1, 64, 16)
