@@ -538,6 +538,9 @@ pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_se
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || num_seqs > 65535 || max_selected <= 0 || max_blocks_per_seq <= 0)
     return PKV_ERR_INVALID;
+  // grid rows of 16 query heads; places in 16-key units counted in 31 bits
+  if (static_cast<int64_t>(g.KVH) * ((g.QPK + 15) / 16) > 65535 || max_selected > 1 << 28)
+    return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   if (!out || !query || !kv_cache || !block_tables || !seq_lens || !selected)
     return PKV_ERR_INVALID;

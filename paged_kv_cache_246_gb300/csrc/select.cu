@@ -199,6 +199,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;  // of the score histogram; later a bit per block
 static_assert(PKV_SELECT_MAX_BLOCKS <= 32 * kBins, "a bit per block");
+static_assert(kBins % (4 * kThreads) == 0 && 256 % kThreads == 0, "whole 16-byte loads of bins");
 constexpr int kList = 256;   // open blocks that are ranked at once
 
 struct Args {
@@ -291,8 +292,8 @@ __device__ __forceinline__ void split_value(uint32_t x, int &m, int &e, FP16) {
 
 // The same for finite scores, in 64-bit fixed point with 54 bits below 2^top,
 // which no product reaches: sums of 128 products do not overflow and do not
-// depend on their order; terms are cut below 2^(top - 54), as the largest
-// term's double is, so that a sum is exact whenever its double is.
+// depend on their order.  Terms are cut below 2^(top - 54); products have 22 bits
+// at most, so those within 2^32 of the largest possible one are exact.
 template <class T, int D, bool KV8>
 __device__ __noinline__ unsigned long long key_fixed(const uint8_t *row, const uint16_t *q, int qpk,
                                                      int top) {

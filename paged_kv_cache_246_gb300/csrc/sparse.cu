@@ -47,7 +47,7 @@ constexpr int kRows = 16;    // query heads per CTA: one m16 tile
 constexpr int kStages = 2;   // of a warp's ring
 constexpr int kMaxParts = 8;  // CTAs of a cluster
 constexpr float kLazy = 8.f;
-constexpr int kFar = 0x40000000;  // "position" of a unit that nothing may read
+constexpr int kFar = 0x7fffffe0;  // "position" of a unit that nothing may read
 
 struct Args {
   void *out;

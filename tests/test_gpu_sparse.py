@@ -254,6 +254,37 @@ def test_select_ties(fp8):
     check_select(s, b, 20)
 
 
+@pytest.mark.parametrize("what", ["ties", "nan"])
+def test_select_border_of_more_blocks_than_keys_are_kept_for(what):
+    # 5000 blocks whose scores take few values (or one of which is NaN, which
+    # sends all of them through the exact scores): more than the first CTA has
+    # room for in 64 bits, so they are made again for every digit
+    s = Scene([80000], 2, 2, 64, 16)
+    b = torch.randint(-1, 2, (s.blocks, 2, 1, 64), generator=s.gen) * 0.5
+    b[:, :, :, 2:] = 0.0
+    b = torch.cat([b, b], 2).to(s.dtype)
+    s.query = torch.randint(1, 3, s.query.shape, generator=s.gen).to(s.dtype)
+    if what == "nan":
+        b[s.tables[0, 3000].long(), :, 1, 9] = float("nan")
+    check_select(s, b, 40)
+    check_select(s, b, 2500, sink=2)
+
+
+def test_select_zeros_and_bad_entries():
+    s = Scene([500], 2, 2, 64, 16)
+    b = s.random_bounds()
+    s.query.zero_()
+    check_select(s, b, 12)
+    t = s.tables.clone()
+    t[0, 0] = t[0, 4] = s.blocks          # equal scores: bad ones last all the same
+    got = run_select(s, b, 30, tables=t)
+    assert error()[0] == B.PKV_ERR_BOUNDS
+    assert got[0, 0].tolist() == [j for j in range(32) if j not in (0, 4)]
+    got = run_select(s, b, 31, tables=t)
+    assert error()[0] == B.PKV_ERR_BOUNDS
+    assert got[0, 0].tolist() == [j for j in range(32) if j != 4]
+
+
 def test_select_tells_scores_apart_that_fp32_cannot():
     # a large sum hides differences of its last place: scores 2^20 + i * 2^-12
     s = Scene([2400], 2, 2, 64, 16)
@@ -597,6 +628,38 @@ def test_two_streams_at_once():
     clean("streams")
     for r, g in zip(ref, got):
         assert torch.equal(r.out, g.out) and torch.equal(r.sel, g.sel) and torch.equal(r.cache, g.cache)
+
+
+def test_explicit_stream():
+    s = Scene([900, 333], 8, 2, 128, 16)
+    p, sel = s.params(), s.selection(20).to(DEV)
+    q, cache, t, lens = s.query.to(DEV), s.cache.to(DEV), s.tables.to(DEV), s.lens.to(DEV)
+    a, b = torch.zeros_like(q), torch.zeros_like(q)
+    B.paged_attn_decode_sparse(a, q, cache, t, lens, sel, p)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    B.paged_attn_decode_sparse(b, q, cache, t, lens, sel, p, stream=st)
+    st.synchronize()
+    clean("stream")
+    assert torch.equal(a, b)
+    B.paged_attn_decode_sparse(b.zero_(), q, cache, t, lens, sel, p, stream=torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(a, b)
+
+
+def test_empty_batches():
+    s = Scene([40], 4, 2, 64, 16)
+    p, e = s.params(), dict(device=DEV)
+    cache, i32 = s.cache.to(DEV), torch.zeros(0, dtype=torch.int32, **e)
+    none = torch.zeros(0, 256, dtype=BF, **e)
+    kv, i64 = torch.zeros(0, 128, dtype=BF, **e), torch.zeros(0, dtype=torch.int64, **e)
+    t, sel = torch.zeros(0, 3, dtype=torch.int32, **e), torch.zeros(0, 2, 4, dtype=torch.int32, **e)
+    bounds = s.random_bounds().to(DEV)
+    B.kv_cache_write_rope(none, none, kv, kv, cache, i64, i64, B.rope_table(8, 64), p)
+    B.kv_block_bounds(bounds, cache, t, i32, 5, p)
+    B.paged_attn_select_blocks(sel, none, bounds, t, i32, 40, p)
+    B.paged_attn_decode_sparse(none, none, cache, t, i32, sel, p)
+    clean("empty")
+    assert torch.equal(cache.cpu(), s.cache)
 
 
 def test_repeats_bit_for_bit():

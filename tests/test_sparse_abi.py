@@ -85,6 +85,7 @@ def test_select_refusals(lib):
     assert _select(lib, _p(alibi_slopes=1 << 20)) == B.PKV_ERR_UNSUPPORTED
     assert _select(lib, maxl=16 * B.PKV_SELECT_MAX_BLOCKS + 1) == B.PKV_ERR_UNSUPPORTED
     assert _select(lib, _p(num_heads=129, num_kv_heads=1)) == B.PKV_ERR_UNSUPPORTED
+    assert _select(lib, _p(num_heads=65536, num_kv_heads=65536)) == B.PKV_ERR_UNSUPPORTED
 
 
 def _sparse(lib, p=None, **kw):
@@ -100,6 +101,8 @@ def test_sparse_refusals(lib):
                 dict(cache=ctypes.c_void_p((1 << 20) + 8))):
         assert _sparse(lib, **bad) == B.PKV_ERR_INVALID, bad
     assert _sparse(lib, _p(dtype=5)) == B.PKV_ERR_UNSUPPORTED
+    assert _sparse(lib, k=(1 << 28) + 1) == B.PKV_ERR_UNSUPPORTED
+    assert _sparse(lib, _p(num_heads=65536, num_kv_heads=65536)) == B.PKV_ERR_UNSUPPORTED
 
 
 def test_select_limit_matches_the_header():
