@@ -10,6 +10,7 @@ library has not been built (``python -m paged_kv_cache_246_gb300.build_lib``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -392,6 +393,7 @@ def kv_swap_blocks(src_cache: torch.Tensor, dst_cache: torch.Tensor, pairs: torc
 # device that holds their tensors, whichever is current; a stream given by
 # the caller must belong to it.
 # ---------------------------------------------------------------------------
+_Tensor = torch.Tensor
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object made on the way
 
 
@@ -399,13 +401,21 @@ def _current_stream(index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+@functools.lru_cache(maxsize=None)
+def _one_gpu() -> bool:
+    return torch.cuda.device_count() == 1
+
+
 def _call_on(where: str, stream, tensors: Sequence[torch.Tensor], *args):
     """The entry point `where` on the device that holds `tensors`."""
-    index = tensors[0].get_device()
+    index = -1
     for t in tensors:
-        if t.get_device() != index or index < 0:
-            raise ValueError(f"{where}: tensors must be on one CUDA device, not "
-                             f"{tensors[0].device} and {t.device}")
+        at = t.get_device()
+        if at != index or at < 0:
+            if index >= 0 or at < 0:
+                raise ValueError(f"{where}: tensors must be on one CUDA device, not "
+                                 f"{tensors[0].device} and {t.device}")
+            index = at
     if stream is None:
         handle = _current_stream(index)
     else:
@@ -414,7 +424,7 @@ def _call_on(where: str, stream, tensors: Sequence[torch.Tensor], *args):
                              f"{tensors[0].device}")
         handle = _stream(stream)
     fn = getattr(lib(), where)
-    if torch.cuda.current_device() == index:
+    if _one_gpu() or torch.cuda.current_device() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -426,31 +436,38 @@ def _call_on(where: str, stream, tensors: Sequence[torch.Tensor], *args):
 _TORCH_DTYPES = {code: dtype for dtype, code in _DTYPES.items()}
 
 
-def _is(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> tuple:
-    """The sizes of a contiguous tensor of this type (its device is checked at the call)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {len(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return shape
-
-
-def _types(p: AttnParams) -> tuple:
-    """(dtype of queries, keys, values and outputs; dtype of the cache)."""
+@functools.lru_cache(maxsize=64)
+def _facts_of(raw: bytes) -> tuple:
+    p = AttnParams.from_buffer_copy(raw)
     dtype = _TORCH_DTYPES.get(p.dtype)
     if dtype is None:
         raise ValueError(f"unsupported params dtype {p.dtype}")
-    return dtype, torch.uint8 if p.kv_cache_dtype == PKV_CACHE_FP8_E4M3 else dtype
+    return (dtype, torch.uint8 if p.kv_cache_dtype == PKV_CACHE_FP8_E4M3 else dtype,
+            p.num_kv_heads, p.head_size, p.num_heads * p.head_size, p.num_kv_heads * p.head_size,
+            p.block_size * p.num_kv_heads * p.head_size)
 
 
-def _is_cache(t: torch.Tensor, dtype: torch.dtype, p: AttnParams) -> int:
+def _facts(p: AttnParams) -> tuple:
+    """(dtype of queries, keys, values and outputs; dtype of the cache; KV
+    heads; head size; elements of a query row, a key row, a cache block)."""
+    return _facts_of(bytes(p))
+
+
+def _is(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> tuple:
+    """The sizes of a contiguous tensor of this type (its device is checked at the call)."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == ndim:
+            return shape
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    raise ValueError(f"{name} must be contiguous, {dtype}, of {ndim} dims; got "
+                     f"{'contiguous' if t.is_contiguous() else 'strided'}, {t.dtype}, {list(t.shape)}")
+
+
+def _is_cache(t: torch.Tensor, dtype: torch.dtype, block: int) -> int:
     two, blocks, elems = _is(t, "kv_cache", dtype, 3)
-    if two != 2 or elems != p.block_size * p.num_kv_heads * p.head_size:
+    if two != 2 or elems != block:
         raise ValueError("kv_cache must be [2, num_blocks, block_size*num_kv_heads*head_size]")
     return blocks
 
@@ -465,7 +482,7 @@ def _is_batch(block_tables: torch.Tensor, seq_lens: torch.Tensor) -> tuple:
 def _row_stride(t: torch.Tensor, name: str, rows: int, row: int, dtype: torch.dtype) -> int:
     """Elements between the rows of a [rows, row] tensor whose rows may be
     slices of wider ones."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -501,14 +518,12 @@ def kv_cache_write_rope(query_out: torch.Tensor, query: torch.Tensor, key: torch
     """kv_cache_write with queries and keys rotated by their positions: rows of
     query, key and value may be slices of one projection's output; query_out
     may be query."""
-    dtype, cache_dtype = _types(params)
-    nb = _is_cache(kv_cache, cache_dtype, params)
+    dtype, cache_dtype, _, _, q_row, kv_row, block = _facts(params)
+    nb = _is_cache(kv_cache, cache_dtype, block)
     T = _is(slot_mapping, "slot_mapping", torch.int64, 1)[0]
     if _is(positions, "positions", torch.int64, 1)[0] != T:
         raise ValueError("positions and slot_mapping sizes disagree")
     max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
-    q_row = params.num_heads * params.head_size
-    kv_row = params.num_kv_heads * params.head_size
     so = _row_stride(query_out, "query_out", T, q_row, dtype)
     sq = _row_stride(query, "query", T, q_row, dtype)
     sk = _row_stride(key, "key", T, kv_row, dtype)
@@ -521,9 +536,9 @@ def kv_cache_write_rope(query_out: torch.Tensor, query: torch.Tensor, key: torch
              ctypes.byref(params))
 
 
-def _is_bounds(bounds: torch.Tensor, dtype: torch.dtype, p: AttnParams) -> int:
+def _is_bounds(bounds: torch.Tensor, dtype: torch.dtype, kv_heads: int, head_size: int) -> int:
     blocks, heads, two, size = _is(bounds, "bounds", dtype, 4)
-    if heads != p.num_kv_heads or two != 2 or size != p.head_size:
+    if heads != kv_heads or two != 2 or size != head_size:
         raise ValueError("bounds must be [num_blocks, num_kv_heads, 2, head_size]")
     return blocks
 
@@ -533,9 +548,9 @@ def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: 
                     context_lens: Optional[torch.Tensor] = None, stream=None) -> None:
     """Channelwise minima and maxima of the keys of the blocks that hold
     positions context_lens[b] .. seq_lens[b] - 1 (None: all of the sequence)."""
-    cache_dtype = _types(params)[1]
-    nb = _is_cache(kv_cache, cache_dtype, params)
-    if _is_bounds(bounds, cache_dtype, params) != nb:
+    _, cache_dtype, kv_heads, head_size, _, _, block = _facts(params)
+    nb = _is_cache(kv_cache, cache_dtype, block)
+    if _is_bounds(bounds, cache_dtype, kv_heads, head_size) != nb:
         raise ValueError("bounds and kv_cache must have the same number of blocks")
     n, wide = _is_batch(block_tables, seq_lens)
     tensors, ctx = (kv_cache, bounds, block_tables, seq_lens), None
@@ -548,16 +563,16 @@ def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: 
              ctypes.byref(params))
 
 
-def _is_selected(selected: torch.Tensor, n: int, p: AttnParams) -> int:
+def _is_selected(selected: torch.Tensor, n: int, kv_heads: int) -> int:
     seqs, heads, k = _is(selected, "selected", torch.int32, 3)
-    if seqs != n or heads != p.num_kv_heads:
+    if seqs != n or heads != kv_heads:
         raise ValueError("selected must be [num_seqs, num_kv_heads, max_selected]")
     return k
 
 
-def _is_rows(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, p: AttnParams) -> None:
+def _is_rows(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, q_row: int) -> None:
     rows, row = _is(t, name, dtype, 2)
-    if rows != n or row != p.num_heads * p.head_size:
+    if rows != n or row != q_row:
         raise ValueError(f"{name} must be [num_seqs, num_heads*head_size]")
 
 
@@ -568,11 +583,11 @@ def paged_attn_select_blocks(selected: torch.Tensor, query: torch.Tensor, bounds
     """selected [num_seqs, num_kv_heads, K]: each KV head's K blocks with the
     largest bound on q.k, the first num_sink and last num_recent among them,
     ascending, -1 behind."""
-    dtype, cache_dtype = _types(params)
-    nb = _is_bounds(bounds, cache_dtype, params)
+    dtype, cache_dtype, kv_heads, head_size, q_row, _, _ = _facts(params)
+    nb = _is_bounds(bounds, cache_dtype, kv_heads, head_size)
     n, wide = _is_batch(block_tables, seq_lens)
-    k = _is_selected(selected, n, params)
-    _is_rows(query, "query", dtype, n, params)
+    k = _is_selected(selected, n, kv_heads)
+    _is_rows(query, "query", dtype, n, q_row)
     _call_on("paged_attn_select_blocks", stream, (bounds, selected, query, block_tables, seq_lens),
              selected.data_ptr(), k, query.data_ptr(), n, bounds.data_ptr(), nb,
              block_tables.data_ptr(), wide, seq_lens.data_ptr(), int(max_seq_len), int(num_sink),
@@ -584,12 +599,12 @@ def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: t
                              selected: torch.Tensor, params: AttnParams, stream=None) -> None:
     """paged_attn_decode over the blocks that selected [num_seqs, num_kv_heads,
     K] names for each sequence and KV head (ascending, negative numbers behind)."""
-    dtype, cache_dtype = _types(params)
-    nb = _is_cache(kv_cache, cache_dtype, params)
+    dtype, cache_dtype, kv_heads, _, q_row, _, block = _facts(params)
+    nb = _is_cache(kv_cache, cache_dtype, block)
     n, wide = _is_batch(block_tables, seq_lens)
-    k = _is_selected(selected, n, params)
-    _is_rows(out, "out", dtype, n, params)
-    _is_rows(query, "query", dtype, n, params)
+    k = _is_selected(selected, n, kv_heads)
+    _is_rows(out, "out", dtype, n, q_row)
+    _is_rows(query, "query", dtype, n, q_row)
     _call_on("paged_attn_decode_sparse", stream,
              (kv_cache, out, query, block_tables, seq_lens, selected), out.data_ptr(),
              query.data_ptr(), n, kv_cache.data_ptr(), nb, block_tables.data_ptr(), wide,

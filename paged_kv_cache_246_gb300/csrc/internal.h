@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pkv.h"
 
 namespace pkv {
@@ -128,6 +130,22 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
                                  const int32_t *seq_lens, const int32_t *selected,
                                  int max_selected, const Geometry &g, cudaStream_t stream);
 cudaError_t read_device_error_sparse(unsigned long long *out);
+
+// Lets a kernel take as much dynamic shared memory as the device grants beside
+// its static `reserved` bytes; asked once per kernel and device (`done`: a bit
+// per device).
+template <class K>
+cudaError_t allow_shared_memory(K *kernel, std::atomic<uint64_t> &done, size_t reserved) {
+  DeviceInfo dev;
+  cudaError_t e = current_device_info(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << dev.device;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           dev.max_smem_optin - static_cast<int>(reserved));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A kernel launch as a programmatic dependent of the kernel before it in the
 // stream, in clusters of `cluster` CTAs along x (0: none).

@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 // an order in which a lane's 16-byte loads are its A fragments as they stand.
 //
 // Exactness.  Products of 16-bit values are exact; a product step sums 16 of
-// them with an error of at most 2^-19 of their magnitudes' sum (each term cut
-// at 2^-23 of the largest), and starts from zero, so that errors scale with the
+// them with an error of at most 2^-19 of the largest (each term cut at 2^-23 of
+// it; 2^-19.6 measured over random terms), and starts from zero, so that errors scale with the
 // step's terms and not with the sum so far; the steps' sums are added in fp32.
 // With m_h the sum of the steps' largest |q| and twice what that comes to, a
 // score is within
@@ -201,6 +201,7 @@ constexpr int kBins = 1024;  // of the score histogram; later a bit per block
 static_assert(PKV_SELECT_MAX_BLOCKS <= 32 * kBins, "a bit per block");
 static_assert(kBins % (4 * kThreads) == 0 && 256 % kThreads == 0, "whole 16-byte loads of bins");
 constexpr int kList = 256;   // open blocks that are ranked at once
+constexpr size_t kStatic = 12 * 1024;  // the kernel's own shared memory, rounded up
 
 struct Args {
   int32_t *selected;
@@ -898,8 +899,8 @@ template <class T, int D, bool KV8>
 static cudaError_t launch_select_typed(const Args &a, int num_seqs, size_t smem,
                                        cudaStream_t stream) {
   auto kern = select_kernel<T, D, KV8>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(kern, allowed, kStatic);
   if (e != cudaSuccess) return e;
   PdlLaunch cfg(dim3(a.cluster, a.KVH, num_seqs), kThreads, smem, stream, a.cluster);
   return cudaLaunchKernelEx(&cfg.c, kern, a);
@@ -967,8 +968,7 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
   const int64_t items = static_cast<int64_t>(s.num_seqs) * g.KVH;
   const size_t heads8 = (g.QPK + 7) / 8;
   const size_t fixed = (heads8 - 1) * (8 * 4 + (g.D / 8) * 32 * 8);
-  constexpr size_t kStatic = 12 * 1024;  // the kernel's own shared memory, rounded up
-  const size_t room = static_cast<size_t>(dev.max_smem_optin) - kStatic - fixed;
+  const size_t room = static_cast<size_t>(dev.max_smem_optin) - sel::kStatic - fixed;
   if (static_cast<size_t>(blocks) * 4 > room) return cudaErrorInvalidValue;
   // 64-bit keys for all candidates where that costs no resident CTA
   a.keys_fit = static_cast<size_t>(blocks) * 8 <= 32 * 1024;

@@ -638,7 +638,8 @@ static cudaError_t launch_w(const Args &a, const CUtensorMap &tmap, int num_seqs
                             cudaStream_t stream) {
   auto kern = sparse_kernel<T, D, KV8, HALF, W>;
   constexpr int smem = Lay<D, KV8, W>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(kern, allowed, 1024);
   if (e != cudaSuccess) return e;
   PdlLaunch cfg(dim3(a.parts, a.KVH * a.row_groups, num_seqs), 32 * W, smem, stream, a.parts);
   return cudaLaunchKernelEx(&cfg.c, kern, a, tmap);
