@@ -970,13 +970,13 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
   const size_t fixed = (heads8 - 1) * (8 * 4 + (g.D / 8) * 32 * 8);
   const size_t room = static_cast<size_t>(dev.max_smem_optin) - sel::kStatic - fixed;
   if (static_cast<size_t>(blocks) * 4 > room) return cudaErrorInvalidValue;
-  // 64-bit keys for all candidates where that costs no resident CTA
-  a.keys_fit = static_cast<size_t>(blocks) * 8 <= 32 * 1024;
+  // 64-bit keys for all candidates where that costs no resident CTA (two to an SM)
+  a.keys_fit = fixed + static_cast<size_t>(blocks) * 8 <= 96 * 1024;
   const size_t smem = fixed + static_cast<size_t>(blocks) * (a.keys_fit ? 8 : 4);
-  // a CTA per SM or more, and 64 blocks or more to each: measured, 64 sequences
-  // of 16k..32k take 84 us with one CTA per (sequence, KV head) and 93 / 103 us
-  // with two / four, 16 of 64k..128k (fp8) 28 us with two and 33 / 40 us with
-  // four / eight, one of 32k 11.8 us with eight
+  // A CTA per SM or more, and 64 blocks or more to each.  Measured with 1 / 2 / 4 / 8
+  // CTAs per (sequence, KV head), 8 KV heads, us: 64 sequences of 16k .. 32k 80 / 90 /
+  // 101 / 143, 16 of them 36 / 28 / 31 / 40, 4 30 / 20 / 15 / 15, one of 32k 20 / 15 /
+  // 12 / 10; 16 of 64k .. 128k, 8-bit heads of 64, 34 / 27 / 32 / 37.
   a.cluster = 1;
   while (a.cluster < sel::kMaxCluster && items * a.cluster < dev.sms && blocks / a.cluster >= 64)
     a.cluster *= 2;

@@ -256,11 +256,11 @@ def test_select_ties(fp8):
 
 @pytest.mark.parametrize("what", ["ties", "nan"])
 def test_select_border_of_more_blocks_than_keys_are_kept_for(what):
-    # 5000 blocks whose scores take few values (or one of which is NaN, which
+    # 12400 blocks whose scores take few values (or one of which is NaN, which
     # sends all of them through the exact scores): more than the first CTA has
     # room for in 64 bits, so they are made again for every digit
-    s = Scene([80000], 2, 2, 64, 16)
-    b = torch.randint(-1, 2, (s.blocks, 2, 1, 64), generator=s.gen) * 0.5
+    s = Scene([198400], 1, 1, 64, 16)
+    b = torch.randint(-1, 2, (s.blocks, 1, 1, 64), generator=s.gen) * 0.5
     b[:, :, :, 2:] = 0.0
     b = torch.cat([b, b], 2).to(s.dtype)
     s.query = torch.randint(1, 3, s.query.shape, generator=s.gen).to(s.dtype)
