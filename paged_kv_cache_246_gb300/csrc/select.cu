@@ -179,12 +179,12 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 // an order in which a lane's 16-byte loads are its A fragments as they stand.
 //
 // Exactness.  Products of 16-bit values are exact; a product step sums 16 of
-// them with an error of at most 2^-19 of the largest (each term cut at 2^-23 of
-// it; 2^-19.6 measured over random terms), and starts from zero, so that errors scale with the
-// step's terms and not with the sum so far; the steps' sums are added in fp32.
-// With m_h the sum of the steps' largest |q| and twice what that comes to, a
-// score is within
-//     E = max_h (2^-18 m_h + 2^-20 |q_h|_1) * max |bound|
+// them with an error of at most 1.5 * 2^-19 of the largest (each term cut at 2^-23
+// of it, the sum at 2^-24; 2^-19.6 measured over random terms), and starts from
+// zero, so that errors scale with the step's terms and not with the sum so far;
+// the steps' sums are added in fp32, 8 at most in a row and the two rows' sums.
+// With m_h the sum of the steps' largest |q| a score is within
+//     E = max_h (1.5 * 2^-19 m_h + 9 * 2^-24 |q_h|_1) * max |bound|
 // of the exact one, so only scores within 2E of the border can belong on its
 // other side.  A histogram of 1024 equal bins finds the border's bin, everything
 // above it and 2E is taken, and what lies in it or within 2E (one to five
@@ -301,39 +301,54 @@ __device__ __noinline__ unsigned long long key_fixed(const uint8_t *row, const u
   using MT = std::conditional_t<KV8, FP16, T>;
   constexpr int E = D / 32;  // channels per lane
   const int lane = threadIdx.x & 31;
-  uint32_t bits[2][E];  // this lane's minima, maxima
+  int mb[2][E], eb[2][E];  // this lane's minima and maxima as m * 2^e
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
+    uint32_t w[(E + 1) / 2];
     if constexpr (KV8) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int k = 0; k < E; ++k) w |= static_cast<uint32_t>(row[x * D + lane * E + k]) << (8 * k);
-      const uint2 h = e4m3x4_to_h4(w);
-#pragma unroll
-      for (int k = 0; k < E; ++k) bits[x][k] = ((k < 2 ? h.x : h.y) >> (16 * (k & 1))) & 0xffffu;
+      uint32_t c;  // E codes
+      if constexpr (E == 4) c = __ldg(reinterpret_cast<const uint32_t *>(row + x * D) + lane);
+      else c = __ldg(reinterpret_cast<const uint16_t *>(row + x * D) + lane);
+      const uint2 h = e4m3x4_to_h4(c);
+      w[0] = h.x;
+      if constexpr (E == 4) w[1] = h.y;
+    } else if constexpr (E == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + x * D * 2) + lane);
+      w[0] = v.x;
+      w[1] = v.y;
     } else {
-      const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + x * D + lane * E;
-#pragma unroll
-      for (int k = 0; k < E; ++k) bits[x][k] = p[k];
+      w[0] = __ldg(reinterpret_cast<const uint32_t *>(row + x * D * 2) + lane);
     }
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      split_value((w[k / 2] >> (16 * (k & 1))) & 0xffffu, mb[x][k], eb[x][k], MT{});
   }
   long long best = LLONG_MIN;
   for (int h0 = 0; h0 < qpk; h0 += 4) {  // four heads' chains side by side
+    uint32_t w[4][E / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t *qh = q + min(h0 + i, qpk - 1) * D;
+      if constexpr (E == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(qh) + lane);
+        w[i][0] = v.x;
+        w[i][1] = v.y;
+      } else {
+        w[i][0] = __ldg(reinterpret_cast<const uint32_t *>(qh) + lane);
+      }
+    }
     long long s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint16_t *qh = q + min(h0 + i, qpk - 1) * D + lane * E;
-      uint32_t w[E / 2];
-#pragma unroll
-      for (int k = 0; k < E / 2; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t *>(qh) + k);
       s[i] = 0;
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        const uint32_t qb = (w[k / 2] >> (16 * (k & 1))) & 0xffffu;
-        int mq, eq, mb, eb;
+        const uint32_t qb = (w[i][k / 2] >> (16 * (k & 1))) & 0xffffu;
+        const bool neg = qb & 0x8000u;  // max(q lo, q hi) is that of q's sign
+        int mq, eq;
         split_value(qb, mq, eq, T{});
-        split_value(bits[qb & 0x8000u ? 0 : 1][k], mb, eb, MT{});
-        const int p = mq * mb, sh = eq + eb - top + 54;  // p * 2^sh stays below 2^54
+        const int p = mq * (neg ? mb[0][k] : mb[1][k]);
+        const int sh = eq + (neg ? eb[0][k] : eb[1][k]) - top + 54;  // p * 2^sh is below 2^54
         const long long m = abs(p);
         const long long v = p == 0 ? 0 : sh >= 0 ? m << min(sh, 63) : m >> min(-sh, 63);
         s[i] += p < 0 ? -v : v;
@@ -358,7 +373,7 @@ __device__ __forceinline__ float warp_max(float x) {
 // s of lane (g, tq) covers elements 4 u .. 4 u + 3 of the bounds row's 16-byte
 // chunk 4 (s / P) + tq, u = s % P, P steps per chunk; min(q, 0) against minima,
 // max(q, 0) against maxima.  Also for the lane's head: the error's factor
-// 2^-18 m + 2^-20 |q|_1, the largest |q| and, where bf16 queries meet fp8 bounds,
+// 1.5 * 2^-19 m + 9 * 2^-24 |q|_1, the largest |q| and, where bf16 queries meet fp8 bounds,
 // the power of two that they are scaled down by (the largest of a head becomes
 // [2^14, 2^15) in fp16, which is exact for components within 2^28 of it and off
 // by 2^-39 of it below).
@@ -391,7 +406,8 @@ __device__ __forceinline__ void make_b(const Args &a, const uint16_t *q, int h8,
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  factor = steps * 0x1p-17f + sum * 0x1p-20f;
+  // (2 m: both halves; a little more for the sums made here)
+  factor = 1.001f * (steps * 0x1.8p-18f + sum * 0x1.2p-21f);
   unit = 1.f;
   if constexpr (KV8 && std::is_same<T, BF16>::value) {
     const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // top in [2^e, 2^(e+1))
@@ -594,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
       if (t + 16 * v >= i1) break;
       float best0 = -INFINITY, best1 = -INFINITY;
       for (int h8 = 0; h8 < heads8; ++h8) {
-        unsigned long long c01 = 0, c23 = 0;  // packed fp32 pairs
+        unsigned long long c01[2] = {0, 0}, c23[2] = {0, 0};  // packed fp32 pairs, even and odd steps
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const uint32_t w0[4] = {u0[v][i].x, u0[v][i].y, u0[v][i].z, u0[v][i].w};
@@ -625,14 +641,14 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
             float d[4];
             const uint2 q2 = h8 == 0 ? bq[s] : sb[((h8 - 1) * kSteps + s) * 32 + lane];
             mma_16816<MT>(d, f0[0], f1[0], f0[1], f1[1], q2.x, q2.y, 0.f, 0.f, 0.f, 0.f);
-            c01 = fadd2(c01, f2pack(d[0], d[1]));
-            c23 = fadd2(c23, f2pack(d[2], d[3]));
+            c01[s & 1] = fadd2(c01[s & 1], f2pack(d[0], d[1]));
+            c23[s & 1] = fadd2(c23[s & 1], f2pack(d[2], d[3]));
           }
         }
         // heads 8 h8 + 2 tq, + 1 of blocks g (c[0], c[1]) and g + 8
         float c[4];
-        f2unpack(c01, c[0], c[1]);
-        f2unpack(c23, c[2], c[3]);
+        f2unpack(fadd2(c01[0], c01[1]), c[0], c[1]);
+        f2unpack(fadd2(c23[0], c23[1]), c[2], c[3]);
         if constexpr (kScaled) {
           const float e0 = h8 == 0 ? unit0 : sunit[(h8 - 1) * 8 + 2 * tq];
           const float e1 = h8 == 0 ? unit1 : sunit[(h8 - 1) * 8 + 2 * tq + 1];
