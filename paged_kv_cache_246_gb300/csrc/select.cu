@@ -194,12 +194,9 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 // fit, all that is open is scored again and the border found digit by digit;
 // where a score is not finite, the same in doubles.
 // ---------------------------------------------------------------------------
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;  // of the score histogram; later a bit per block
 static_assert(PKV_SELECT_MAX_BLOCKS <= 32 * kBins, "a bit per block");
-static_assert(kBins % (4 * kThreads) == 0 && 256 % kThreads == 0, "whole 16-byte loads of bins");
 constexpr int kList = 256;   // open blocks that are ranked at once
 constexpr size_t kStatic = 12 * 1024;  // the kernel's own shared memory, rounded up
 
@@ -221,7 +218,8 @@ __device__ __forceinline__ unsigned long long key_of(double s) {
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-// Exclusive prefix sum of v over the CTA's threads.
+// Exclusive prefix sum of v over the CTA's W warps.
+template <int W>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
@@ -235,7 +233,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *scratch) {
   __syncthreads();
   uint32_t base = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
+  for (int w = 0; w < W; ++w)
     if (w < warp) base += scratch[w];
   return base + x - v;
 }
@@ -428,11 +426,11 @@ __device__ __forceinline__ void make_b(const Args &a, const uint16_t *q, int h8,
 
 // Blocks p0 + i, i < n, for which taken(i) to `out` in order; tie(i): taken too
 // as long as `left` of them are not used up.
-template <class F, class G>
+template <int W, class F, class G>
 __device__ __forceinline__ void put_taken(int32_t *out, uint32_t left, int p0, int n,
                                           uint32_t (*scratch)[2], const F &taken, const G &tie) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seg = (n + 32 * kWarps - 1) / (32 * kWarps) * 32;  // consecutive blocks per warp
+  const int seg = (n + 32 * W - 1) / (32 * W) * 32;  // consecutive blocks per warp
   const int w0 = warp * seg, w1 = min(w0 + seg, n);
   uint32_t up = 0, at = 0;
   for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -464,8 +462,11 @@ __device__ __forceinline__ void put_taken(int32_t *out, uint32_t left, int p0, i
   }
 }
 
-template <class T, int D, bool KV8>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
+// W warps: 8, two CTAs to an SM, or 4, four of them.
+template <class T, int D, bool KV8, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
+  constexpr int kWarps = W, kThreads = 32 * W;
+  static_assert(kBins % (4 * kThreads) == 0 && 256 % kThreads == 0, "whole 16-byte loads of bins");
   using MT = std::conditional_t<KV8, FP16, T>;  // operand type
   constexpr int kRowBytes = 2 * D * (KV8 ? 1 : 2);
   constexpr int kSteps = 2 * D / 16;
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) sum += cnt[k];
-    uint32_t above = block_scan(sum, scratch);
+    uint32_t above = block_scan<W>(sum, scratch);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (above < static_cast<uint32_t>(need) && static_cast<uint32_t>(need) <= above + cnt[k])
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
       const int k0 = min(tid * each, words), k1 = min(k0 + each, words);
       uint32_t count = 0;
       for (int k = k0; k < k1; ++k) count += __popc(taken[k]);
-      uint32_t place = block_scan(count, scratch);
+      uint32_t place = block_scan<W>(count, scratch);
       for (int k = k0; k < k1; ++k)
         for (uint32_t m = taken[k]; m; m &= m - 1) out[n_front + place++] = c_lo + 32 * k + __ffs(m) - 1;
       return;
@@ -881,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
     uint32_t cnt[kPer], sum = 0;  // of digits 255 - kPer tid - k
 #pragma unroll
     for (int k = 0; k < kPer; ++k) sum += cnt[k] = bins[255 - kPer * tid - k];
-    uint32_t above = block_scan(sum, scratch);
+    uint32_t above = block_scan<W>(sum, scratch);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       if (above < left && left <= above + cnt[k]) {
@@ -903,22 +904,22 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const Args a) {
       if (lane == 0) score[i] = x > border ? 2.f : x == border ? 1.f : 0.f;
     }
     __syncthreads();
-    put_taken(out + n_front, left, c_lo, n, warp_counts, [&](int i) { return score[i] == 2.f; },
+    put_taken<W>(out + n_front, left, c_lo, n, warp_counts, [&](int i) { return score[i] == 2.f; },
                  [&](int i) { return score[i] == 1.f; });
   } else {
-    put_taken(out + n_front, left, c_lo, n, warp_counts, [&](int i) { return keys[i] > border; },
+    put_taken<W>(out + n_front, left, c_lo, n, warp_counts, [&](int i) { return keys[i] > border; },
                  [&](int i) { return keys[i] == border; });
   }
 }
 
-template <class T, int D, bool KV8>
+template <class T, int D, bool KV8, int W>
 static cudaError_t launch_select_typed(const Args &a, int num_seqs, size_t smem,
                                        cudaStream_t stream) {
-  auto kern = select_kernel<T, D, KV8>;
+  auto kern = select_kernel<T, D, KV8, W>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared_memory(kern, allowed, kStatic);
   if (e != cudaSuccess) return e;
-  PdlLaunch cfg(dim3(a.cluster, a.KVH, num_seqs), kThreads, smem, stream, a.cluster);
+  PdlLaunch cfg(dim3(a.cluster, a.KVH, num_seqs), 32 * W, smem, stream, a.cluster);
   return cudaLaunchKernelEx(&cfg.c, kern, a);
 }
 
@@ -986,8 +987,12 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
   const size_t fixed = (heads8 - 1) * (8 * 4 + (g.D / 8) * 32 * 8);
   const size_t room = static_cast<size_t>(dev.max_smem_optin) - sel::kStatic - fixed;
   if (static_cast<size_t>(blocks) * 4 > room) return cudaErrorInvalidValue;
-  // 64-bit keys for all candidates where that costs no resident CTA (two to an SM)
-  a.keys_fit = fixed + static_cast<size_t>(blocks) * 8 <= 96 * 1024;
+  // More (sequence, KV head) pairs than 8-warp CTAs fit: 4 warps, four CTAs to an
+  // SM (64 sequences of 2k .. 4k, 8 KV heads: 17 against 22 us; of 16k .. 32k: 80 both;
+  // with fewer pairs 8 warps, 32 sequences: 12 against 14 and 45 against 60).
+  const bool many = items > 2LL * dev.sms;
+  // 64-bit keys for all candidates where that costs no resident CTA
+  a.keys_fit = fixed + static_cast<size_t>(blocks) * 8 <= (many ? 40 : 96) * 1024;
   const size_t smem = fixed + static_cast<size_t>(blocks) * (a.keys_fit ? 8 : 4);
   // A CTA per SM or more, and 64 blocks or more to each.  Measured with 1 / 2 / 4 / 8
   // CTAs per (sequence, KV head), 8 KV heads, us: 64 sequences of 16k .. 32k 80 / 90 /
@@ -997,9 +1002,10 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
   while (a.cluster < sel::kMaxCluster && items * a.cluster < dev.sms && blocks / a.cluster >= 64)
     a.cluster *= 2;
   const bool bf = g.dtype == PKV_BF16;
-#define PKV_SEL(TT, DD, KK)          \
-  if (g.D == DD && g.fp8 == KK)      \
-    return sel::launch_select_typed<TT, DD, KK>(a, s.num_seqs, smem, stream);
+#define PKV_SEL(TT, DD, KK)                                                             \
+  if (g.D == DD && g.fp8 == KK)                                                         \
+    return many ? sel::launch_select_typed<TT, DD, KK, 4>(a, s.num_seqs, smem, stream)  \
+                : sel::launch_select_typed<TT, DD, KK, 8>(a, s.num_seqs, smem, stream);
   if (bf) {
     PKV_SEL(BF16, 128, false) PKV_SEL(BF16, 64, false) PKV_SEL(BF16, 128, true) PKV_SEL(BF16, 64, true)
   } else {

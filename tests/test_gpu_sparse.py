@@ -104,6 +104,14 @@ def test_rope_in_place_and_many_tokens():
     check_rope(s, 3001, 128, False, True)
 
 
+@pytest.mark.parametrize("dtype,D,heads,kv_heads,rot,inter,fp8", [
+    (BF, 128, 4, 1, 128, True, False), (FP, 64, 3, 3, 32, False, False), (FP, 64, 2, 1, 64, True, True),
+    (BF, 128, 2, 2, 64, False, True)])
+def test_rope_bulk(dtype, D, heads, kv_heads, rot, inter, fp8):
+    # more tokens than 6 per SM: the streaming form
+    check_rope(Scene([1400], heads, kv_heads, D, 16, dtype, fp8), 1111, rot, inter, True)
+
+
 def test_rope_without_rotation_is_the_cache_write():
     s = Scene([100], 8, 2, 128, 16)
     p = s.params()
@@ -169,6 +177,15 @@ def test_bounds(dtype, D, BS, kv_heads, fp8):
     check_bounds(mk(), max(lens), nan=True)
 
 
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (FP, False), (BF, True)])
+def test_bounds_bulk(dtype, fp8):
+    # tables and a bound on the new tokens wide enough for the streaming form
+    s = Scene([100, 0, 37], 8, 8, 128, 16, dtype, fp8)
+    s.tables = torch.cat([s.tables, torch.zeros(3, 2200, dtype=torch.int32)], 1)
+    check_bounds(s, 35000)
+    check_bounds(s, 35000, [90, 0, 16], nan=True)
+
+
 def test_bounds_leave_unwritten_slots_out():
     s = Scene([17, 40], 2, 2, 64, 16)
     flat = s.cache.view(2, -1, 16, s.row)
@@ -231,6 +248,25 @@ def test_select(heads, kv_heads, D, BS, dtype, fp8, window):
     check_select(s, b, 1)
     check_select(s, b, 60, sink=1, max_len=5000)
     check_select(s, b, 300)                     # all
+
+
+@pytest.mark.parametrize("heads,kv_heads,D,BS,dtype,fp8", [
+    (4, 4, 128, 16, BF, False), (8, 4, 64, 16, FP, False), (4, 4, 64, 32, FP, True), (8, 4, 128, 16, BF, True),
+    (44, 4, 64, 16, BF, False)])
+def test_select_many_pairs(heads, kv_heads, D, BS, dtype, fp8):
+    # more (sequence, KV head) pairs than two per SM; one sequence to a CTA
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, 700, (90,), generator=g).tolist()
+    s = Scene(lens, heads, kv_heads, D, BS, dtype, fp8)
+    b = s.random_bounds()
+    check_select(s, b, 9, sink=1, recent=2)
+    s.query.zero_()
+    check_select(s, b, 5)
+    t = torch.randint(-1, 2, (s.blocks, kv_heads, 1, D), generator=g) * 0.5
+    t[:, :, :, 3:] = 0.0
+    t = torch.cat([t, t], 2)
+    s.query = torch.randint(-2, 3, s.query.shape, generator=g).to(dtype)
+    check_select(s, codes(t) if fp8 else t.to(dtype), 12)
 
 
 def test_select_long():
@@ -396,6 +432,18 @@ def test_sparse_many_blocks(fp8, D):
     # long enough for the keys to be spread over CTAs
     s = Scene([9000, 8999, 40, 5000], 8, 2, D, 16, fp8=fp8)
     check_sparse(s, s.selection(300), seqs=[0, 2])
+
+
+@pytest.mark.parametrize("seqs", [80, 160])
+@pytest.mark.parametrize("heads,kv_heads,D,BS,dtype,fp8", [
+    (4, 2, 128, 16, BF, False), (18, 2, 128, 32, FP, False), (4, 2, 64, 32, FP, False), (24, 2, 64, 16, BF, False),
+    (8, 2, 128, 16, BF, True), (20, 2, 128, 16, FP, True), (12, 2, 64, 16, FP, True), (34, 2, 64, 32, BF, True)])
+def test_sparse_many_pairs(heads, kv_heads, D, BS, dtype, fp8, seqs):
+    # more (sequence, KV head) pairs than SMs: smaller CTAs, two parts or one
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 130, (seqs,), generator=g).tolist()
+    s = Scene(lens, heads, kv_heads, D, BS, dtype, fp8, window=100)
+    check_sparse(s, s.selection(6, short=True), seqs=list(range(0, seqs, 7)))
 
 
 def test_sparse_of_all_blocks_is_the_decode():
