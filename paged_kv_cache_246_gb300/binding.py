@@ -398,7 +398,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream 
 
 
 def _current_stream(index: int) -> int:
-    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 @functools.lru_cache(maxsize=None)

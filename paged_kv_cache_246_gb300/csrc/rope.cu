@@ -28,7 +28,7 @@ struct Args {
   uint8_t *k_half, *v_half;
   int64_t row_bytes;  // of the cache
   int H, KVH, rot;
-  float k_scale, v_scale, k_inv, v_inv;  // and their reciprocals
+  float k_scale, v_scale, k_inv, v_inv;  // and their reciprocals (0: divide)
 };
 
 __device__ __forceinline__ void widen(float (&f)[8], const uint4 &u, BF16) {
@@ -56,12 +56,14 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
                     T::from_f2(f[6], f[7]));
 }
 
-// x / scale as IEEE division rounds it, for inv = 1 / scale rounded and a scale
-// of ordinary size: the remainder of the first product corrects it (Markstein
-// 1990).  Quotients of 512 and more saturate as they are.
+// x / scale as IEEE division rounds it, for inv = 1 / scale rounded and a scale in
+// 2^-100 .. 2^100: the remainder of the first product corrects it (Markstein 1990).
+// Quotients of 512 and more saturate as they are, zeros keep their sign (0x44000000
+// is 512).
 __device__ __forceinline__ float quotient(float x, float scale, float inv) {
   const float q = x * inv;
-  return fabsf(q) < 512.f ? fmaf(fmaf(-q, scale, x), inv, q) : q;
+  const bool ordinary = __float_as_uint(fabsf(q)) - 1u < 0x44000000u - 1u;
+  return ordinary ? fmaf(fmaf(-q, scale, x), inv, q) : q;
 }
 
 // Eight values as E4M3 codes of f / scale (fp32 quotient, nearest even,
@@ -69,10 +71,14 @@ __device__ __forceinline__ float quotient(float x, float scale, float inv) {
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float scale, float inv) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(f[2 * i], scale, inv),
-                                                quotient(f[2 * i + 1], scale, inv)),
-                                    __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    // inv = 0: a scale outside that range
+    const float2 q = inv != 0.f ? make_float2(quotient(f[2 * i], scale, inv),
+                                              quotient(f[2 * i + 1], scale, inv))
+                                : make_float2(__fdiv_rn(f[2 * i], scale),
+                                              __fdiv_rn(f[2 * i + 1], scale));
+    w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -94,7 +100,8 @@ __device__ __forceinline__ void rotate(float &x1, float &x2, float c, float s) {
 // and plain accesses: 9.2 / 12.0 us for 2048 tokens, 31.8 / 40.2 for 8192, 61 /
 // 78 for 16384 (6.7 TB/s); for 512 tokens 3.2 / 3.0 and for 64 2.3 / 1.9.
 template <class T, int D, bool KV8, bool INTER, bool BULK>
-__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? (KV8 ? 7 : 8) : 1) rope_write_kernel(const Args a) {
+__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? (KV8 ? 7 : 8) : 1)
+rope_write_kernel(const Args a) {
   constexpr int LPH = D / 16;  // lanes per head
   grid_dependency_wait();
   grid_launch_dependents();
@@ -237,17 +244,20 @@ cudaError_t launch_rope_write(const RopeCall &r, const Geometry &g, cudaStream_t
   a.rot = r.rot_dim;
   a.k_scale = g.k_scale;
   a.v_scale = g.v_scale;
-  a.k_inv = 1.f / g.k_scale;
-  a.v_inv = 1.f / g.v_scale;
+  auto inverse = [](float x) { return x >= 0x1p-100f && x <= 0x1p100f ? 1.f / x : 0.f; };
+  a.k_inv = inverse(g.k_scale);
+  a.v_inv = inverse(g.v_scale);
   const bool bf = g.dtype == PKV_BF16, in = r.interleaved != 0;
-  if (g.D == 128) {
-    if (g.fp8) return bf ? rope::launch_typed<BF16, 128, true>(a, in, stream) : rope::launch_typed<FP16, 128, true>(a, in, stream);
-    return bf ? rope::launch_typed<BF16, 128, false>(a, in, stream) : rope::launch_typed<FP16, 128, false>(a, in, stream);
+#define PKV_ROPE(TT, DD)                                                     \
+  if (g.D == DD)                                                             \
+    return g.fp8 ? rope::launch_typed<TT, DD, true>(a, in, stream)           \
+                 : rope::launch_typed<TT, DD, false>(a, in, stream);
+  if (bf) {
+    PKV_ROPE(BF16, 128) PKV_ROPE(BF16, 64)
+  } else {
+    PKV_ROPE(FP16, 128) PKV_ROPE(FP16, 64)
   }
-  if (g.D == 64) {
-    if (g.fp8) return bf ? rope::launch_typed<BF16, 64, true>(a, in, stream) : rope::launch_typed<FP16, 64, true>(a, in, stream);
-    return bf ? rope::launch_typed<BF16, 64, false>(a, in, stream) : rope::launch_typed<FP16, 64, false>(a, in, stream);
-  }
+#undef PKV_ROPE
   return cudaErrorInvalidValue;
 }
 

@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
   float *score = sunit + (heads8 - 1) * 8;
   unsigned long long *keys = reinterpret_cast<unsigned long long *>(score);
   __shared__ __align__(16) uint32_t bins[kBins];
-  __shared__ float4 span[kMaxCluster * kWarps];  // of every warp: -smallest, largest score, largest |bound|, flags
+  // of every warp: -smallest, largest score, largest |bound|, flags
+  __shared__ float4 span[kMaxCluster * kWarps];
   __shared__ float2 list[kList];            // open blocks: score, place (as bits)
   __shared__ unsigned long long list_key[kList];
   __shared__ uint32_t scratch[kWarps], warp_counts[kWarps][2];
@@ -575,7 +576,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
   float mn = INFINITY, mx = -INFINITY;
   float nan = 0.f;      // 0, or NaN after a score that is not finite
   bool bad = false;     // a bad entry
-  uint32_t blo[2] = {0, 0}, bhi[2] = {0, 0};  // the smallest minima, the largest maxima (with 0), packed
+  // the smallest minima, the largest maxima (with 0), packed
+  uint32_t blo[2] = {0, 0}, bhi[2] = {0, 0};
   bool started = alone;
   for (int t = i0 + warp * 16 * U; t < i1; t += kWarps * 16 * U) {
     uint4 u0[U][kLoads], u1[U][kLoads];
@@ -697,7 +699,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
     const float2 lo = MT::to_f2(P::mn(blo[0], blo[1])), hi = MT::to_f2(P::mx(bhi[0], bhi[1]));
     const float w[4] = {warp_max(-mn), warp_max(mx),
                         warp_max(fmaxf(fmaxf(-lo.x, -lo.y), fmaxf(hi.x, hi.y))),
-                        __any_sync(0xffffffffu, nan != nan) ? 2.f : __any_sync(0xffffffffu, bad) ? 1.f : 0.f};
+                        __any_sync(0xffffffffu, nan != nan) ? 2.f
+                        : __any_sync(0xffffffffu, bad)      ? 1.f
+                                                            : 0.f};
     float *mine = reinterpret_cast<float *>(&span[rank * kWarps + warp]);
     if (lane == 0) {
 #pragma unroll
@@ -737,7 +741,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
   bool fits = !odd && mx >= mn && mx - mn < INFINITY && err < INFINITY && inv < INFINITY;
   float t_lo = -INFINITY, t_hi = INFINITY;  // above t_hi taken, below t_lo not
   // 2^top: more than any product
-  const int top = static_cast<int>(__float_as_uint(qtop) >> 23) + static_cast<int>(__float_as_uint(btop) >> 23) - 252;
+  const int top =
+      static_cast<int>(__float_as_uint(qtop) >> 23) + static_cast<int>(__float_as_uint(btop) >> 23) - 252;
   auto key = [&](int i) -> unsigned long long {  // a bad entry's is below every score's
     const int pb = __ldg(table + i);
     if (pb < 0 || pb >= a.num_blocks) return 0;
@@ -799,7 +804,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
         const float2 e = list[k];
         uint32_t ahead = 0;
         for (uint32_t j = 0; j < open; ++j)
-          ahead += list[j].x > e.x || (list[j].x == e.x && __float_as_int(list[j].y) < __float_as_int(e.y));
+          ahead += list[j].x > e.x ||
+                   (list[j].x == e.x && __float_as_int(list[j].y) < __float_as_int(e.y));
         if (ahead == left - 1) s_border = e.x;
       }
       __syncthreads();
@@ -826,7 +832,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
           uint32_t ahead = 0;
           for (uint32_t j = 0; j < open; ++j)
             ahead += list_key[j] > list_key[k] ||
-                     (list_key[j] == list_key[k] && __float_as_int(list[j].y) < at && list[j].x >= lo);
+                     (list_key[j] == list_key[k] && __float_as_int(list[j].y) < at &&
+                      list[j].x >= lo);
           take = ahead < left;
         }
         if (take) atomicOr(&taken[at >> 5], 1u << (at & 31));
@@ -838,7 +845,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) select_kernel(const Args a) {
       for (int k = k0; k < k1; ++k) count += __popc(taken[k]);
       uint32_t place = block_scan<W>(count, scratch);
       for (int k = k0; k < k1; ++k)
-        for (uint32_t m = taken[k]; m; m &= m - 1) out[n_front + place++] = c_lo + 32 * k + __ffs(m) - 1;
+        for (uint32_t m = taken[k]; m; m &= m - 1)
+          out[n_front + place++] = c_lo + 32 * k + __ffs(m) - 1;
       return;
     }
   }
@@ -1007,9 +1015,11 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
     return many ? sel::launch_select_typed<TT, DD, KK, 4>(a, s.num_seqs, smem, stream)  \
                 : sel::launch_select_typed<TT, DD, KK, 8>(a, s.num_seqs, smem, stream);
   if (bf) {
-    PKV_SEL(BF16, 128, false) PKV_SEL(BF16, 64, false) PKV_SEL(BF16, 128, true) PKV_SEL(BF16, 64, true)
+    PKV_SEL(BF16, 128, false) PKV_SEL(BF16, 64, false)
+    PKV_SEL(BF16, 128, true) PKV_SEL(BF16, 64, true)
   } else {
-    PKV_SEL(FP16, 128, false) PKV_SEL(FP16, 64, false) PKV_SEL(FP16, 128, true) PKV_SEL(FP16, 64, true)
+    PKV_SEL(FP16, 128, false) PKV_SEL(FP16, 64, false)
+    PKV_SEL(FP16, 128, true) PKV_SEL(FP16, 64, true)
   }
 #undef PKV_SEL
   return cudaErrorInvalidValue;

@@ -537,7 +537,8 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     issue();
   }
   if (!ok)  // this warp's copies still in flight
-    for (int k = consumed; k < issued; ++k) mbar_wait_bounded(&wbar[k % kStages], (k / kStages) & 1, b);
+    for (int k = consumed; k < issued; ++k)
+      mbar_wait_bounded(&wbar[k % kStages], (k / kStages) & 1, b);
 
   // ---- the warps' (m, l, O) joined, then the cluster's --------------------------------
 #pragma unroll

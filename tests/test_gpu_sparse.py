@@ -124,6 +124,27 @@ def test_rope_without_rotation_is_the_cache_write():
     assert torch.equal(a, b) and torch.equal(out.cpu()[slots >= 0], dq.cpu()[slots >= 0])
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("scale", [0.02, 1.0, 0.37, 300.0, 2.0 ** -110, 1e-40, 1e35])
+@pytest.mark.parametrize("T", [1024, 512])   # the streaming form and the other
+def test_rope_codes_are_the_cache_write_s(dtype, scale, T):
+    # every 16-bit value as a value row, every finite one as a key row, unrotated:
+    # bit for bit the codes of the plain cache write, which divides
+    s = Scene([8], 1, 1, 64, 16, dtype, fp8=True, extra_blocks=64)
+    p = B.make_params(1, 1, 64, 16, dtype, 0.125, kv_cache_dtype="fp8_e4m3", k_scale=scale, v_scale=scale)
+    v = (torch.arange(1024 * 64, device=DEV) - 32768).to(torch.int16).view(dtype).view(1024, 64)[:T].contiguous()
+    k = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    slots = torch.randperm(s.blocks * 16, generator=s.gen)[:T].to(DEV)
+    still = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).to(DEV)
+    a, b = s.cache.to(DEV), s.cache.to(DEV)
+    B.kv_cache_write(k, v, a, slots, p)
+    B.kv_cache_write_rope(torch.zeros_like(v), v, k, v, b, slots, torch.zeros_like(slots), still, p)
+    clean("rope")
+    # (-0 turned by 0 is +0)
+    same = (a == b) | ((a == 0x80) & (b == 0))
+    assert same[0].all() and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("what", ["slot", "position", "negative position"])
 def test_rope_bad_index(what):
     s = Scene([100], 8, 2, 128, 16)
