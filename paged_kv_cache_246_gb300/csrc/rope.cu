@@ -98,9 +98,10 @@ __device__ __forceinline__ void rotate(float &x1, float &x2, float c, float s) {
 // BULK, for more than 6 tokens per SM: CTAs of 192 threads and streaming loads
 // and stores (the rows are more than L2 keeps).  Measured against 512 threads
 // and plain accesses: 9.2 / 12.0 us for 2048 tokens, 31.8 / 40.2 for 8192, 61 /
-// 78 for 16384 (6.7 TB/s); for 512 tokens 3.2 / 3.0 and for 64 2.3 / 1.9.
+// 78 for 16384 (6.7 TB/s); for 512 tokens 3.2 / 3.0 and for 64 2.3 / 1.9.  Registers
+// for 8 such CTAs per SM: over an 8-bit cache 67 us for 16384 tokens, 71 with 5 or 6.
 template <class T, int D, bool KV8, bool INTER, bool BULK>
-__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? (KV8 ? 7 : 8) : 1)
+__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? 8 : 1)
 rope_write_kernel(const Args a) {
   constexpr int LPH = D / 16;  // lanes per head
   grid_dependency_wait();
