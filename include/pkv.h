@@ -520,8 +520,8 @@ pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, con
  * paged_attn_decode_sparse -- paged_attn_decode over some of each sequence's
  * blocks: query head h of sequence b attends to the keys of the blocks
  * selected[b][KV head of h] at positions < seq_lens[b] (and inside the
- * sliding window), with ALiBi as there.  With every block selected it is
- * paged_attn_decode.
+ * sliding window), with ALiBi as there.  With every block selected it computes
+ * what paged_attn_decode does.
  *
  *   selected       int32[num_seqs][num_kv_heads][max_selected]: strictly
  *                  ascending logical block numbers, then any negative
@@ -531,8 +531,10 @@ pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, con
  *   seq_lens       int32[num_seqs]; < 0 or above max_blocks_per_seq *
  *                  block_size records PKV_ERR_BOUNDS and gives zero rows
  * A row with nothing to attend to (seq_len 0, none selected, all of the
- * selected outside the window) is zero.  Other arguments as
- * paged_attn_decode.
+ * selected outside the window) is zero.  Values that are not finite go the way
+ * of the formula: a head whose scores hold a NaN or +infinity, or nothing but
+ * -infinity, is NaN, the other heads are not touched by it (paged_attn_decode
+ * writes zeros where a sum is NaN).  Other arguments as paged_attn_decode.
  */
 pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_seqs,
                                     const void *kv_cache, int64_t num_blocks,

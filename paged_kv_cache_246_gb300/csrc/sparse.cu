@@ -48,6 +48,7 @@ constexpr int kStages = 2;   // of a warp's ring
 constexpr int kMaxParts = 8;  // CTAs of a cluster
 constexpr float kLazy = 8.f;
 constexpr int kFar = 0x7fffffe0;  // "position" of a unit that nothing may read
+constexpr float kLowest = -3.4028234663852886e38f;
 
 struct Args {
   void *out;
@@ -335,6 +336,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   const int k_tok = (mi >> 1) * 8 + rr, k_half = mi & 1;  // ldmatrix rows of K
   const int v_tok = (mi & 1) * 8 + rr, v_half = mi >> 1;  // and of V^T
   bool ok = true;
+  bool seen = false;  // a visible key
   int consumed = 0;
 
   for (int k = 0; k < issued; ++k) {
@@ -407,6 +409,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     // ---- scores in the log2 domain, masked -------------------------------------------
     // sc[n][2 r + c]: row g + 8 r, key j0 + 8 n + 2 tq + c
     const bool interior = j0 >= lo && j0 + kUnit <= L;
+    seen |= j0 < L && j0 + kUnit > lo;
     float x[2][4];
     bool grow = false;
 #pragma unroll
@@ -541,8 +544,13 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       mbar_wait_bounded(&wbar[k % kStages], (k / kStages) & 1, b);
 
   // ---- the warps' (m, l, O) joined, then the cluster's --------------------------------
+  // m is -infinity still where no key was visible, and where every score was NaN
+  // (l and O are NaN) or -infinity (they are 0): these rows take the lowest finite
+  // m, so that they weigh nothing beside a finite score, NaN stays, and 0 / 0 is NaN
+  // where a row had no other
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
+    if (seen && m[r] == -INFINITY) m[r] = kLowest;
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
   }
@@ -595,7 +603,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       }
     }
     if (a.parts == 1) {
-      const float v = den == 0.f ? 0.f : num / den * a.v_scale;
+      const float v = M == -INFINITY ? 0.f : num / den * a.v_scale;
       out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
     } else {
       so[(kWarps * kRows + r) * L_::PAD + d] = num;
@@ -628,7 +636,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         den = fmaf(e, pl[c], den);
       }
     }
-    const float v = den == 0.f ? 0.f : num / den * a.v_scale;
+    const float v = M == -INFINITY ? 0.f : num / den * a.v_scale;
     out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
   }
   cluster_sync();  // no CTA leaves while its shared memory is read

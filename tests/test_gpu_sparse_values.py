@@ -1,0 +1,120 @@
+"""The sparse decode over values out of the ordinary, against the fp64 oracle:
+queries that are not finite, heads of very different size in one group, keys
+that are not finite, and weights whose last bits show."""
+import dataclasses
+
+import pytest
+import torch
+
+import oracle as O
+from paged_kv_cache_246_gb300 import binding as B
+from sparse_helpers import SCALE8, Scene
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, FP = torch.bfloat16, torch.float16
+NAN, INF = float("nan"), float("inf")
+
+
+def decode(s, sel):
+    p = B.make_params(s.H, s.KVH, s.D, s.BS, s.dtype, s.op.scale, None, s.window, **s._k)
+    q = s.query.to(DEV)
+    out = torch.full_like(q, 7.0)
+    B.paged_attn_decode_sparse(out, q, s.cache.to(DEV), s.tables.to(DEV), s.lens.to(DEV), sel.to(DEV), p)
+    torch.cuda.synchronize()
+    st, d = B.device_error()
+    assert st == B.PKV_OK, f"{B.status_string(st)} at {d}"
+    return out.cpu().double().view(q.shape[0], s.H, s.D)
+
+
+def expected(s, sel):
+    """The first four sequences' and the last one's (NaN in the rows between)."""
+    n = s.lens.numel()
+    want, spread = O.paged_attn_decode_sparse(s.query, s.cache, s.tables, s.lens, sel, s.op,
+                                              sorted({*range(min(n, 4)), n - 1}))
+    shape = (s.lens.numel(), s.H, s.D)
+    return want.view(shape), spread.view(shape)
+
+
+def score_error(s):
+    """[seqs, H, 1]: how far a head's scores may be off, from its own largest |q|:
+    fp32 sums of D products (2^-24 of each per step) and, over an fp8 cache, E4M3
+    terms of the query that cut it at 2^-17 of the head's largest component."""
+    q = s.query.double().view(s.lens.numel(), s.H, s.D).abs().amax(2, keepdim=True)
+    k = 448 * SCALE8 if s.fp8 else s.cache[0].double().nan_to_num(0.0, 0.0, 0.0).abs().max().item()
+    per = s.D * 2.0 ** -24 + (2.0 ** -17 if s.fp8 else 0.0)
+    return s.op.scale * s.D * q * k * per + 64.0 * 2.0 ** -22
+
+
+def near(s, got, want, spread, rows, what):
+    """Half a step of the output, the weights' rounding (half a step of 16 bits at
+    most) and a weight's 2 d for scores that are off by d, at the heads `rows`
+    [seqs, H]."""
+    half = torch.finfo(s.dtype).eps / 2
+    weights = torch.finfo(FP).eps / 2 if s.fp8 else half
+    tol = 1.01 * (half * want.abs() + (weights + 2 * score_error(s)) * spread) + 1e-7
+    seen = torch.zeros_like(rows)
+    seen[[*range(min(4, len(rows))), -1]] = True      # those that `expected` gives
+    bad = ~((got - want).abs() <= tol) & (rows & seen)[:, :, None]
+    assert not bad.any(), f"{what}: heads {sorted(set(bad.nonzero()[:, 1].tolist()))}"
+
+
+# (heads, KV heads, head size, type, 8-bit cache): 1 .. 17 query heads to a KV head
+SHAPES = [(4, 1, 128, BF, True), (8, 2, 64, FP, True), (7, 1, 64, BF, True), (16, 2, 128, FP, True),
+          (12, 1, 128, BF, True), (17, 1, 64, FP, True), (4, 1, 128, BF, False), (8, 1, 64, FP, False),
+          (12, 1, 64, BF, False), (17, 1, 128, FP, False)]
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,D,dtype,fp8", [
+    (8, 2, 128, BF, True), (8, 2, 64, FP, False), (24, 2, 64, BF, True), (24, 2, 128, FP, False)])
+def test_visible_keys_and_values_that_are_nan(heads, kv_heads, D, dtype, fp8, many):
+    # a NaN in a key: every head of that KV head is NaN; in a value: one channel
+    # is; KV head 1 has neither
+    lens = [100, 100, 800, 40] + ([16] * 90 if many else [])
+    s = Scene(lens, heads, kv_heads, D, 16, dtype, fp8)
+    sel = s.selection(7)
+    want, spread = expected(s, sel)
+    nan = 0x7f if fp8 else NAN
+    flat = s.cache.view(2, s.blocks, 16, kv_heads, D)
+    place = lambda b, k: int(s.tables[b, int(sel[b, 0, k])])  # noqa: E731
+    flat[0, place(0, 2), 3, 0, 1] = nan        # a key
+    flat[1, place(1, 4), 9, 0, 5] = nan        # a value
+    for k in range(7):
+        flat[0, place(2, k), :, 0, 7] = nan    # every key
+    flat[0, place(3, 2), 40 % 16:, 0] = nan   # keys and values past the end are not seen
+    flat[1, place(3, 2), 40 % 16:, 0] = nan
+    assert int(sel[3, 0, 2]) == 2
+    got = decode(s, sel)
+    group = heads // kv_heads
+    rows = torch.ones(len(lens), heads, dtype=torch.bool)
+    rows[:3, :group] = False
+    near(s, got, want, spread, rows, "the rest")
+    assert torch.isnan(got[[0, 2], :group]).all()
+    channels = torch.isnan(got[1, :group])
+    assert channels[:, 5].all() and channels.sum() == group
+    got[1, :group, 5] = want[1, :group, 5]
+    rows[1] = True
+    near(s, got, want, spread, rows, "the other channels")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("heads,D,dtype", [(4, 64, BF), (12, 128, FP)])
+def test_visible_keys_that_are_infinite(heads, D, dtype, many):
+    # scores of minus infinity weigh nothing; a row that has no other is NaN, as
+    # is one with a score of plus infinity
+    lens = [160, 160, 700] + ([16] * 170 if many else [])
+    s = Scene(lens, heads, 1, D, 16, dtype)
+    s.query.view(-1, heads, D)[:, :, 2] = 1.5
+    sel = s.selection(10)
+    flat = s.cache.view(2, s.blocks, 16, 1, D)
+    flat[0, s.tables[0, 4].long(), :, 0, 2] = -INF
+    flat[0, s.tables[1, 6].long(), 2, 0, 2] = INF
+    flat[0, s.tables[2].long(), :, 0, 2] = -INF
+    got = decode(s, sel)
+    want, spread = expected(s, sel)            # its softmax of -infinities alone is NaN too
+    assert torch.isnan(got[1:3]).all() and torch.isnan(want[1:3]).all()
+    rows = torch.ones(len(lens), heads, dtype=torch.bool)
+    rows[1:3] = False
+    near(s, got, want, spread, rows, "the rest")
