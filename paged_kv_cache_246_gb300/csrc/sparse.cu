@@ -25,10 +25,10 @@
 // blocks of 16 for each of 8 KV heads of 128, 538 MB in 89 us (6.1 TB/s).
 //
 // Over an fp8 cache the boxes carry the codes.  q.k runs on them as they are:
-// each query row scaled by a power of two and split into two E4M3 terms for
-// bf16, three for fp16 (4 bits each: the 8 and 11 bits of a component, exact
-// within 2^10 of the tile's largest and off by 2^-17 of it below); with four
-// rows or fewer the first two in one product, the low ones as rows 4 .. 7.  The
+// each query row scaled by a power of two of its own and split into two E4M3
+// terms for bf16, three for fp16 (4 bits each: the 8 and 11 bits of a component,
+// exact within 2^9 and 2^6 of the row's largest and off by 2^-17 of it below); with
+// four rows or fewer the first two in one product, the low ones as rows 4 .. 7.  The
 // channels are taken in an order in which a lane's 16-byte chunk of a key is its
 // own fragment.  p.V runs transposed on fp16 operands: the weights' fragments
 // are the B operand, V^T is built from the codes by byte permutes.
@@ -246,7 +246,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   }
   const uint16_t *qb = a.query + static_cast<int64_t>(b) * a.H * D;
   uint32_t qa[KS][4], qc[kThird ? KS8 : 1][4];
-  float sl2 = a.scale_log2;
+  float sl2[2] = {a.scale_log2, a.scale_log2};  // of rows g, g + 8
   const bool fold = KV8 && HALF && a.QPK - rg * kRows <= 4;
   if constexpr (KV8) {
     // qa[s] = high, qa[KS8 + s] = low terms of k-step s: this lane's channels
@@ -260,23 +260,29 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       const uint4 *p = reinterpret_cast<const uint4 *>(qb + h * D + tq * (D / 4));
       return v ? __ldg(p + s) : make_uint4(0u, 0u, 0u, 0u);
     };
-    uint32_t am = 0;  // largest |q| of the tile, as bits
+    // each row by its own power of two: largest finite |q| * 2^-e in [2^7, 2^8)
+    float mul[NR];
 #pragma unroll
-    for (int x = 0; x < NR; ++x)
+    for (int x = 0; x < NR; ++x) {
+      uint32_t am = 0;  // its largest finite |q|, as bits
 #pragma unroll
       for (int s = 0; s < KS8; ++s) {
         const uint4 u = chunk(x, s);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          am = max(am, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+          const uint32_t b0 = __float_as_uint(fabsf(f.x)), b1 = __float_as_uint(fabsf(f.y));
+          am = max(am, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
         }
       }
-    am = __reduce_max_sync(0xffffffffu, am);
-    const int E = static_cast<int>(am >> 23);
-    const int e = E == 0 ? 0 : min(64, max(-64, E - 134));  // largest * 2^-e in [2^7, 2^8)
-    const float mul = __int_as_float((127 - e) << 23);
-    sl2 *= __int_as_float((127 + e) << 23);
+      // (the row's other channels are in the quad's other lanes)
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int E = static_cast<int>(am >> 23);
+      const int e = E == 0 ? 0 : min(64, max(-64, E - 134));
+      mul[x] = __int_as_float((127 - e) << 23);
+      sl2[x] *= __int_as_float((127 + e) << 23);
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -295,8 +301,9 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          v[2 * k] = f.x * mul;
-          v[2 * k + 1] = f.y * mul;
+          // an infinity becomes NaN, as its scores make the row
+          v[2 * k] = fmaf(f.x, 0.f, f.x * mul[x]);
+          v[2 * k + 1] = fmaf(f.y, 0.f, f.y * mul[x]);
         }
         split_e4m3x4(v[0], v[1], v[2], v[3], qa[s][x], qa[KS8 + s][x]);
         split_e4m3x4(v[4], v[5], v[6], v[7], qa[s][2 + x], qa[KS8 + s][2 + x]);
@@ -419,7 +426,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int j = j0 + 8 * n + 2 * tq + c;
-          float v = sc[n][2 * r + c] * sl2;
+          float v = sc[n][2 * r + c] * sl2[r];
           if (has_alibi) v = fmaf(slope[r], static_cast<float>(j - i_pos), v);
           if (!interior && (j < lo || j >= L)) v = -INFINITY;
           x[r][2 * n + c] = v;

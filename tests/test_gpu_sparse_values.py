@@ -67,6 +67,55 @@ SHAPES = [(4, 1, 128, BF, True), (8, 2, 64, FP, True), (7, 1, 64, BF, True), (16
 
 
 @pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("heads,kv_heads,D,dtype,fp8", SHAPES)
+def test_a_head_that_is_not_finite_stays_alone(heads, kv_heads, D, dtype, fp8, bad, many):
+    # many: more (sequence, KV head) pairs than SMs; else parts of a cluster
+    lens = [90, 0, 400, 33] + ([16] * 170 if many else [])
+    s = Scene(lens, heads, kv_heads, D, 16, dtype, fp8)
+    sel = s.selection(9)
+    sel[3] = -1                                # nothing selected: zeros, whatever the query holds
+    q = s.query.view(len(lens), heads, D)
+    group = heads // kv_heads
+    at = [0, group - 1] if group > 1 else [0]
+    clean = s.query.clone()
+    want, spread = expected(s, sel)
+    hit = torch.zeros(len(lens), heads, dtype=torch.bool)
+    for b in range(4):
+        h = at[b % len(at)]
+        q[b, h, (17 * b + 5) % D] = bad
+        hit[b, h] = True
+    got = decode(s, sel)
+    s.query = clean
+    near(s, got, want, spread, ~hit, "the other heads")
+    for b, h in hit.nonzero().tolist():
+        assert torch.isnan(got[b, h]).all() if b in (0, 2) else (got[b, h] == 0).all(), (b, h)
+
+
+@pytest.mark.parametrize("ratio", [-6, -12, -20])
+@pytest.mark.parametrize("heads,kv_heads,D,dtype,fp8", [x for x in SHAPES if x[4]])
+def test_a_head_is_as_exact_beside_a_larger_one(heads, kv_heads, D, dtype, fp8, ratio):
+    # the largest head of the group is 2^-ratio of the others, whose scores have
+    # an ordinary size
+    s = Scene([90, 500, 16], heads, kv_heads, D, 16, dtype, fp8)
+    group = heads // kv_heads
+    if dtype is FP:
+        s.query /= 16                          # 2^20 times 4 does not fit
+    up = 2.0 ** (-ratio if dtype is BF else min(-ratio, 16))
+    s.op = dataclasses.replace(s.op, scale=D ** -0.5 * (16 if dtype is FP else 1))
+    q = s.query.view(3, heads, D)
+    big = torch.zeros(3, heads, dtype=torch.bool)
+    big[:, group // 2::group] = True
+    q[big] = (q[big].double() * up).to(dtype)
+    assert torch.isfinite(q).all()
+    sel = s.selection(20)
+    got = decode(s, sel)
+    want, spread = expected(s, sel)
+    assert torch.isfinite(got).all()
+    near(s, got, want, spread, ~big if group > 1 else big, "the smaller heads")
+
+
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("heads,kv_heads,D,dtype,fp8", [
     (8, 2, 128, BF, True), (8, 2, 64, FP, False), (24, 2, 64, BF, True), (24, 2, 128, FP, False)])
 def test_visible_keys_and_values_that_are_nan(heads, kv_heads, D, dtype, fp8, many):
