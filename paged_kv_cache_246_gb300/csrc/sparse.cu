@@ -279,7 +279,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
       const int E = static_cast<int>(am >> 23);
-      const int e = E == 0 ? 0 : min(64, max(-64, E - 134));
+      const int e = E == 0 ? 0 : max(-126, E - 134);  // 2^-e and 2^e are normal: e <= 120
       mul[x] = __int_as_float((127 - e) << 23);
       sl2[x] *= __int_as_float((127 + e) << 23);
     }

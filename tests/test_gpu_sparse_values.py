@@ -115,6 +115,18 @@ def test_a_head_is_as_exact_beside_a_larger_one(heads, kv_heads, D, dtype, fp8, 
     near(s, got, want, spread, ~big if group > 1 else big, "the smaller heads")
 
 
+@pytest.mark.parametrize("power", [100, 70, -100, -60])
+@pytest.mark.parametrize("heads,D,fp8", [(4, 128, True), (8, 64, True), (16, 64, True), (4, 64, False)])
+def test_huge_and_tiny_queries(heads, D, fp8, power):
+    s = Scene([90, 300], heads, 1, D, 16, BF, fp8)
+    s.query = (s.query.double() * 2.0 ** power).to(BF)
+    s.op = dataclasses.replace(s.op, scale=D ** -0.5 * 2.0 ** -power)
+    sel = s.selection(20)
+    got = decode(s, sel)
+    want, spread = expected(s, sel)
+    near(s, got, want, spread, torch.ones(2, heads, dtype=torch.bool), "all heads")
+
+
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("heads,kv_heads,D,dtype,fp8", [
     (8, 2, 128, BF, True), (8, 2, 64, FP, False), (24, 2, 64, BF, True), (24, 2, 128, FP, False)])
