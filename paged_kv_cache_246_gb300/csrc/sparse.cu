@@ -116,17 +116,26 @@ __device__ __forceinline__ uint32_t rest_e4m3x4(const float *v, uint32_t hi, uin
   return c;
 }
 
-// CTAs per SM that registers are kept for (shared memory allows as many).
-template <int D, bool KV8, bool HALF, int W>
-constexpr int kCtasPerSm = W == kFew ? 1 : D == 64 ? (HALF ? 5 : 4) : KV8 && !HALF ? 3 : 4;
+// CTAs per SM that registers are kept for (shared memory allows as many).  One
+// fewer for 8 rows of bf16 over an fp8 cache, which would spill (256 sequences,
+// 8 KV heads of 128: 149 / 157 us; of 64: 90 / 93; fp16, whose third query term
+// spills either way, 182 / 171).
+template <class T, int D, bool KV8, int ROWS, int W>
+constexpr int kCtasPerSm =
+    W == kFew ? 1
+              : (D == 64 ? (ROWS > 8 ? 4 : 5) : KV8 && ROWS > 8 ? 3 : 4) -
+                    (KV8 && ROWS == 8 && std::is_same<T, BF16>::value ? 1 : 0);
 
-// HALF: 8 rows or fewer, rows 8 .. 15 of the tile are not kept.
-template <class T, int D, bool KV8, bool HALF, int W>
-__global__ void __launch_bounds__(32 * W, kCtasPerSm<D, KV8, HALF, W>)
+// ROWS: 16, or 8 for groups of no more query heads (rows 8 .. 15 of the tile are
+// not kept), or over an fp8 cache 4 (rows 4 .. 7 are the low terms of 0 .. 3).
+template <class T, int D, bool KV8, int ROWS, int W>
+__global__ void __launch_bounds__(32 * W, kCtasPerSm<T, D, KV8, ROWS, W>)
 sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   constexpr int kWarps = W, kThreads = 32 * W;
   using L_ = Lay<D, KV8, W>;
   using MT = std::conditional_t<KV8, FP16, T>;  // type of the weights and of V
+  constexpr bool HALF = ROWS <= 8, fold = ROWS == 4;
+  static_assert(KV8 || !fold, "a 16-bit tile's low terms are in rows 8 .. 15");
   constexpr int NR = HALF ? 1 : 2;              // row halves a lane keeps (g, g + 8)
   constexpr int KS = D / 16, NT = D / 8, KS8 = D / 32;
   constexpr bool kThird = KV8 && std::is_same<T, FP16>::value;  // a third query term
@@ -243,11 +252,14 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     valid[x] = x < NR && r < a.QPK;
     head[x] = kvh * a.QPK + (valid[x] ? r : 0);
     slope[x] = a.alibi && valid[x] ? __ldg(a.alibi + head[x]) * kLog2e : 0.f;
+    if (x == 0 && fold && a.alibi) {  // rows 4 .. 7 weigh as rows 0 .. 3 do
+      const int rs = min(g & 3, a.QPK - 1);
+      slope[0] = __ldg(a.alibi + kvh * a.QPK + rs) * kLog2e;
+    }
   }
   const uint16_t *qb = a.query + static_cast<int64_t>(b) * a.H * D;
   uint32_t qa[KS][4], qc[kThird ? KS8 : 1][4];
   float sl2[2] = {a.scale_log2, a.scale_log2};  // of rows g, g + 8
-  const bool fold = KV8 && HALF && a.QPK - rg * kRows <= 4;
   if constexpr (KV8) {
     // qa[s] = high, qa[KS8 + s] = low terms of k-step s: this lane's channels
     // tq * D / 4 + 8 s .. + 7
@@ -379,7 +391,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
             mma_16832_e4m3(c, q[0], HALF ? 0u : q[1], q[2], HALF ? 0u : q[3], b0, b1, c[0], c[1],
                            HALF ? 0.f : c[2], HALF ? 0.f : c[3]);
           };
-          if (HALF && fold) {
+          if constexpr (fold) {
             mul((s & 1) ? sd[n] : sc[n], qa[s]);
           } else {
             mul(sc[n], qa[s]);
@@ -405,13 +417,11 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int c = 0; c < 2 * NR; ++c) sc[n][c] += sd[n][c];
-    if constexpr (KV8 && HALF) {
-      if (fold) {  // row g + 4 holds row g's low terms
+    if constexpr (fold) {  // row g + 4 holds row g's low terms
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) sc[n][c] += __shfl_xor_sync(0xffffffffu, sc[n][c], 16);
-      }
+        for (int c = 0; c < 2; ++c) sc[n][c] += __shfl_xor_sync(0xffffffffu, sc[n][c], 16);
     }
     // ---- scores in the log2 domain, masked -------------------------------------------
     // sc[n][2 r + c]: row g + 8 r, key j0 + 8 n + 2 tq + c
@@ -469,8 +479,13 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         }
       }
     }
-    // ---- weights: rounded to the product's type; their sum l is of the unrounded -----
-    uint32_t pa[4] = {0u, 0u, 0u, 0u};
+    // ---- weights: as two terms of the product's type, p = hi + lo within 2^-18 of it
+    // (bf16; fp16 2^-23); their sum l is of the unrounded.  A tile of 8 rows or
+    // fewer has the low terms in its other 8 rows (16-bit cache) or, of 4 rows, in
+    // rows 4 .. 7 (fp8): no product more.  (One rounded term put 2^-9 of a bf16
+    // weight into the output; the second costs 0 to 1% there, and where it is a
+    // product of its own 2% of 16 rows over 16 bits and 6 to 9% over fp8.)
+    uint32_t pa[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const float mr = m[r] == -INFINITY ? 0.f : m[r];
@@ -480,6 +495,18 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       l[r] += (p[0] + p[1]) + (p[2] + p[3]);
       pa[r] = MT::from_f2(p[0], p[1]);
       pa[2 + r] = MT::from_f2(p[2], p[3]);
+      const float2 h01 = MT::to_f2(pa[r]), h23 = MT::to_f2(pa[2 + r]);
+      pl[r] = MT::from_f2(p[0] - h01.x, p[1] - h01.y);
+      pl[2 + r] = MT::from_f2(p[2] - h23.x, p[3] - h23.y);
+    }
+    if constexpr (HALF) {
+      if constexpr (!KV8) {
+        pa[1] = pl[0];
+        pa[3] = pl[2];
+      } else if (fold && g >= 4) {
+        pa[0] = pl[0];
+        pa[2] = pl[2];
+      }
     }
     // ---- O += P V.  A masked key's V may hold anything, NaN too, and 0 * NaN is
     // NaN: its row is read as zeros.
@@ -516,6 +543,9 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
           float(&c)[4] = ot[mt][nt];
           mma_16816<FP16>(c, h01.x, h01.y, h89.x, h89.y, pa[nt], pa[2 + nt], c[0], c[1], c[2],
                           c[3]);
+          if constexpr (!fold)
+            mma_16816<FP16>(c, h01.x, h01.y, h89.x, h89.y, pl[nt], pl[2 + nt], c[0], c[1], c[2],
+                            c[3]);
         }
       }
     } else {
@@ -532,13 +562,16 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
             c[2] = o[2 * n2 + i][2];
             c[3] = o[2 * n2 + i][3];
           }
-          mma_16816<MT>(c, pa[0], HALF ? 0u : pa[1], pa[2], HALF ? 0u : pa[3], vb[2 * i],
-                        vb[2 * i + 1], c[0], c[1], c[2], c[3]);
-          o[2 * n2 + i][0] = c[0];
-          o[2 * n2 + i][1] = c[1];
-          if constexpr (!HALF) {
-            o[2 * n2 + i][2] = c[2];
-            o[2 * n2 + i][3] = c[3];
+          mma_16816<MT>(c, pa[0], pa[1], pa[2], pa[3], vb[2 * i], vb[2 * i + 1], c[0], c[1], c[2],
+                        c[3]);
+          if constexpr (HALF) {
+            o[2 * n2 + i][0] = c[0] + c[2];
+            o[2 * n2 + i][1] = c[1] + c[3];
+          } else {
+            mma_16816<MT>(c, pl[0], pl[1], pl[2], pl[3], vb[2 * i], vb[2 * i + 1], c[0], c[1], c[2],
+                          c[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[2 * n2 + i][x] = c[x];
           }
         }
       }
@@ -560,6 +593,12 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     if (seen && m[r] == -INFINITY) m[r] = kLowest;
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
+  if constexpr (fold) {  // columns 2 tq + 4, + 5 of O^T hold the low terms' share of 2 tq, + 1
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ot[mt][0][c] += __shfl_xor_sync(0xffffffffu, ot[mt][0][c], 2);
   }
   __syncthreads();  // all copies have landed: the rings are free
   float *sm = reinterpret_cast<float *>(smem);   // [kWarps + 1][row]: the warps', the CTA's
@@ -649,10 +688,10 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   cluster_sync();  // no CTA leaves while its shared memory is read
 }
 
-template <class T, int D, bool KV8, bool HALF, int W>
+template <class T, int D, bool KV8, int ROWS, int W>
 static cudaError_t launch_w(const Args &a, const CUtensorMap &tmap, int num_seqs,
                             cudaStream_t stream) {
-  auto kern = sparse_kernel<T, D, KV8, HALF, W>;
+  auto kern = sparse_kernel<T, D, KV8, ROWS, W>;
   constexpr int smem = Lay<D, KV8, W>::SMEM;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_shared_memory(kern, allowed, 1024);
@@ -661,15 +700,20 @@ static cudaError_t launch_w(const Args &a, const CUtensorMap &tmap, int num_seqs
   return cudaLaunchKernelEx(&cfg.c, kern, a, tmap);
 }
 
+template <class T, int D, bool KV8, int W>
+static cudaError_t launch_rows(const Args &a, const CUtensorMap &tmap, int num_seqs,
+                               cudaStream_t stream) {
+  if constexpr (KV8)
+    if (a.QPK <= 4) return launch_w<T, D, KV8, 4, W>(a, tmap, num_seqs, stream);
+  return a.QPK <= 8 ? launch_w<T, D, KV8, 8, W>(a, tmap, num_seqs, stream)
+                    : launch_w<T, D, KV8, 16, W>(a, tmap, num_seqs, stream);
+}
+
 template <class T, int D, bool KV8>
 static cudaError_t launch_typed(const Args &a, const CUtensorMap &tmap, int num_seqs, bool few,
                                 cudaStream_t stream) {
-  if (few)
-    return a.QPK <= kRows / 2 ? launch_w<T, D, KV8, true, kFew>(a, tmap, num_seqs, stream)
-                              : launch_w<T, D, KV8, false, kFew>(a, tmap, num_seqs, stream);
-  constexpr int W = kMany<D, KV8>;
-  return a.QPK <= kRows / 2 ? launch_w<T, D, KV8, true, W>(a, tmap, num_seqs, stream)
-                            : launch_w<T, D, KV8, false, W>(a, tmap, num_seqs, stream);
+  return few ? launch_rows<T, D, KV8, kFew>(a, tmap, num_seqs, stream)
+             : launch_rows<T, D, KV8, kMany<D, KV8>>(a, tmap, num_seqs, stream);
 }
 
 }  // namespace sparse

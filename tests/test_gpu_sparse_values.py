@@ -179,3 +179,49 @@ def test_visible_keys_that_are_infinite(heads, D, dtype, many):
     rows = torch.ones(len(lens), heads, dtype=torch.bool)
     rows[1:3] = False
     near(s, got, want, spread, rows, "the rest")
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("heads,D,dtype,fp8", [
+    (1, 64, BF, False), (8, 128, BF, False), (16, 128, BF, False), (8, 64, FP, False), (12, 64, FP, False),
+    (4, 128, BF, True), (8, 64, FP, True), (16, 128, FP, True), (3, 64, FP, True), (6, 64, BF, True)])
+def test_every_bit_of_a_weight_counts(heads, D, dtype, fp8, many):
+    # One block: eight keys of weight 1 and value v, eight of weight w = e^q and
+    # value 1.  With v = -w rounded to 16 bits the output (v + w) / (1 + w) is what
+    # w has beyond those bits.  Over an fp8 cache v = -0.8125, and q such that w is
+    # close to it and about half way between two 16-bit values.
+    lens = [16] * (174 if many else 1)
+    s = Scene(lens, heads, 1, D, 16, dtype, fp8)
+    if fp8:
+        grid = (-torch.linspace(0.19, 0.23, 2000)).to(dtype).unique().double()
+        part = torch.exp(grid) * 2 ** 11 % 1    # of fp16's step of 2^-11
+        q0 = grid[(part - 0.5).abs() < 0.15][:heads]
+    else:
+        q0 = (-torch.linspace(0.3, 1.9, heads)).to(dtype).double()
+    assert q0.numel() == heads
+    w = torch.exp(q0)
+    s.query.zero_()
+    s.query.view(-1, heads, D)[0, :, 0] = q0.to(dtype)
+    at = s.tables[0, 0].long()
+    k, v = s.cache.view(2, s.blocks, 16, D)[:, at]
+    k[:], v[:] = 0, 0
+    if fp8:
+        code = lambda x: torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+        k[8:, 0], v[:8], v[8:] = code(1.0), code(-13.0), code(16.0)
+        s.op = dataclasses.replace(s.op, scale=1 / SCALE8)
+        v0, v1 = torch.full_like(w, -13.0 * SCALE8), 16.0 * SCALE8
+    else:
+        k[8:, 0], v[8:] = 1.0, 1.0
+        v0, v1 = -w.to(dtype).double(), 1.0
+        v[:8, :heads] = v0.to(dtype)           # channel h: head h's
+        s.op = dataclasses.replace(s.op, scale=1.0)
+    got = decode(s, s.selection(1))[0].diagonal()[:heads] if not fp8 else decode(s, s.selection(1))[0, :, 0]
+    want, spread = (v0 + w * v1) / (1 + w), (v0.abs() + w * v1) / (1 + w)
+    # half a step of the output; of the weights 2^-17 (two terms of 9 bits and
+    # more, or the fp32 exponential's few 2^-22), once more for the quotient
+    half = torch.finfo(dtype).eps / 2
+    tol = 1.01 * (half * want.abs() + 2.0 ** -16 * spread) + 2.0 ** -26
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+    # (what rounded weights would give is told apart)
+    rounded = w.to(FP if fp8 else dtype).double()
+    assert (((v0 + rounded * v1) / (1 + w) - want).abs() > 2 * tol).any()
