@@ -950,12 +950,13 @@ cudaError_t launch_block_bounds(void *bounds, const void *kv_cache, const int32_
   a.BS = g.BS;
   a.D = g.D;
   // new positions may start anywhere in a block
-  const int touched = std::min(max_blocks_per_seq, (max_new_tokens - 1 + g.BS - 1) / g.BS + 1);
+  const int64_t touched =
+      std::min<int64_t>(max_blocks_per_seq, (int64_t{max_new_tokens} + g.BS - 2) / g.BS + 1);
   const int64_t items = touched * (g.row_bytes / 16);
   PdlLaunch cfg(dim3(static_cast<unsigned>((items + sel::kBoundsThreads - 1) / sel::kBoundsThreads),
                      num_seqs),
                 sel::kBoundsThreads, 0, stream);
-  const bool bulk = static_cast<int64_t>(num_seqs) * touched * g.block_bytes > 64 << 20;
+  const bool bulk = num_seqs * touched * g.block_bytes > 64 << 20;
 #define PKV_BOUNDS(PP, KK)                                                              \
   return bulk ? cudaLaunchKernelEx(&cfg.c, sel::bounds_kernel<sel::PP, KK, true>, a)    \
               : cudaLaunchKernelEx(&cfg.c, sel::bounds_kernel<sel::PP, KK, false>, a)
