@@ -174,7 +174,10 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   const int32_t *sel = a.selected + sel0;
   const int32_t *table = a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq;
   const int upb = a.BS / kUnit;
-  const int units = a.max_selected * upb;
+  // a valid selection is no longer than the sequence has blocks; behind that only
+  // negative numbers may stand, which are looked at below and not shared out
+  const int n_places = min(a.max_selected, nblk + 1);
+  const int units = n_places * upb;
   const int per = (units + a.parts - 1) / a.parts;
   const int u_begin = min(part * per, units), nu = min(per, units - u_begin);
   const int places = nu > warp ? (nu - warp + kWarps - 1) / kWarps : 0;
@@ -240,6 +243,10 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
     }
   };
   for (int st = 0; st < kStages; ++st) issue();
+  if (L > 0)
+    for (int e = n_places + part * kThreads + threadIdx.x; e < a.max_selected;
+         e += a.parts * kThreads)
+      if (__ldg(sel + e) >= 0) record_error(PKV_ERR_BOUNDS, sel0 + e);
 
   // ---- query fragments -----------------------------------------------------------
   const int g = lane >> 2, tq = lane & 3;

@@ -20,6 +20,42 @@ def clean(where):
     assert st == B.PKV_OK, f"{where}: {B.status_string(st)} at {d}"
 
 
+# ---- selections wider than the sequences -------------------------------------------
+
+
+@pytest.mark.parametrize("heads,D,fp8", [(4, 128, False), (8, 64, True)])
+def test_selection_wider_than_the_sequences(heads, D, fp8):
+    # tables of 32 blocks under a selection of 4096 places: the same output, and
+    # the same bits, as from one of 32 places
+    s = Scene([500, 512, 17, 0], heads, 2, D, 16, fp8=fp8)
+    narrow = s.selection(32, short=True)
+    wide = torch.full((4, 2, 4096), -1, dtype=torch.int32)
+    wide[:, :, :32] = narrow
+    p, q = s.params(), s.query.to(DEV)
+    args = [s.cache.to(DEV), s.tables.to(DEV), s.lens.to(DEV)]
+    out = []
+    for sel in (narrow, wide):
+        out.append(torch.full_like(q, float("nan")))
+        B.paged_attn_decode_sparse(out[-1], q, *args, sel.to(DEV), p)
+        clean("sparse")
+    assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("places", [40, 4096])
+@pytest.mark.parametrize("at", [33, 34, 39])
+def test_numbers_behind_the_end_are_reported(places, at):
+    # behind the first negative number only negative ones may stand, however far
+    s = Scene([512, 512], 4, 2, 64, 16)
+    sel = torch.full((2, 2, places), -1, dtype=torch.int32)
+    sel[:, :, :32] = torch.arange(32)
+    sel[1, 0, at if places == 40 else 100 * at] = 5
+    p, q = s.params(), s.query.to(DEV)
+    out = torch.zeros_like(q)
+    B.paged_attn_decode_sparse(out, q, s.cache.to(DEV), s.tables.to(DEV), s.lens.to(DEV), sel.to(DEV), p)
+    torch.cuda.synchronize()
+    assert B.device_error() == (B.PKV_ERR_BOUNDS, 2 * places + (at if places == 40 else 100 * at))
+
+
 # ---- host bounds far above the lengths ----------------------------------------------
 
 
