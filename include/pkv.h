@@ -504,9 +504,9 @@ pkv_status kv_block_bounds(void *bounds, const void *kv_cache, int64_t num_block
  *                  own position)
  * A table entry out of range records PKV_ERR_BOUNDS; its block is taken last.
  * ALiBi slopes are PKV_ERR_UNSUPPORTED (the scores are unbiased), as are
- * sequences of more than PKV_SELECT_MAX_BLOCKS blocks and KV heads with more
- * than 16384 / head_size query heads.  scale, k_scale and
- * non_causal do not matter.
+ * KV heads with more than 16384 / head_size query heads, and a max_seq_len (or,
+ * if smaller, sliding_window + block_size) of more than PKV_SELECT_MAX_BLOCKS
+ * blocks.  scale, k_scale and non_causal do not matter.
  */
 #define PKV_SELECT_MAX_BLOCKS 32768
 pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, const void *query,

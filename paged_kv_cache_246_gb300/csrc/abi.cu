@@ -511,7 +511,7 @@ pkv_status paged_attn_select_blocks(int32_t *selected, int32_t max_selected, con
       max_selected < static_cast<int64_t>(num_sink) + num_recent)
     return PKV_ERR_INVALID;
   if (g.alibi || g.KVH > 65535 || g.QPK * g.D > kMaxSelectQuery ||
-      (static_cast<int64_t>(max_seq_len) + g.BS - 1) / g.BS > PKV_SELECT_MAX_BLOCKS)
+      scored_blocks(max_seq_len, g) > PKV_SELECT_MAX_BLOCKS)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   if (!selected || !query || !bounds || !block_tables || !seq_lens) return PKV_ERR_INVALID;

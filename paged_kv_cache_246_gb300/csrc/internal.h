@@ -121,6 +121,13 @@ struct SelectCall {
   const int32_t *seq_lens;
   int max_seq_len, num_sink, num_recent;
 };
+// Blocks of a sequence of max_seq_len tokens that a selection may score: those
+// that the sliding window can reach.
+inline int64_t scored_blocks(int64_t max_seq_len, const Geometry &g) {
+  const int64_t window = static_cast<int64_t>(g.window) + g.BS;
+  const int64_t span = g.window > 0 && window < max_seq_len ? window : max_seq_len;
+  return (span + g.BS - 1) / g.BS;
+}
 cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t stream);
 cudaError_t read_device_error_select(unsigned long long *out);
 

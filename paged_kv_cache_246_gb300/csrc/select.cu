@@ -987,10 +987,11 @@ cudaError_t launch_select(const SelectCall &s, const Geometry &g, cudaStream_t s
   a.QPK = g.QPK;
   a.BS = g.BS;
   a.window = g.window;
-  // blocks a sequence can have candidates in
-  int64_t span = s.max_seq_len;
-  if (g.window > 0) span = std::min<int64_t>(span, static_cast<int64_t>(g.window) + g.BS);
-  const int blocks = static_cast<int>((span + g.BS - 1) / g.BS);
+  // blocks a sequence can have candidates in: max_seq_len may be a captured step's
+  // bound, far above what the table's width allows (64 sequences of 2k .. 4k under a
+  // bound of 512k: 17 us, 42 sized by the bound)
+  const int blocks = static_cast<int>(
+      std::min<int64_t>(scored_blocks(s.max_seq_len, g), s.max_blocks_per_seq));
   const int64_t items = static_cast<int64_t>(s.num_seqs) * g.KVH;
   const size_t heads8 = (g.QPK + 7) / 8;
   const size_t fixed = (heads8 - 1) * (8 * 4 + (g.D / 8) * 32 * 8);

@@ -69,3 +69,32 @@ def test_bounds_with_any_bound_on_the_new_tokens(BS, fp8, new):
     want = torch.zeros(got.shape, dtype=torch.float64)
     O.kv_block_bounds(want, s.cache, s.tables, s.lens, s.op)
     assert torch.equal(values(got.cpu(), fp8), want)
+
+
+@pytest.mark.parametrize("max_len", [0x7fffffff, 20_000_000, 16 * B.PKV_SELECT_MAX_BLOCKS + 1])
+def test_select_under_a_window_takes_any_length(max_len):
+    # only the blocks inside the window are scored: the bound on the lengths does
+    # not limit them
+    s = Scene([1777, 900, 16], 4, 2, 64, 16, window=700)
+    b = s.random_bounds()
+    got = torch.full((3, 2, 12), 99, dtype=torch.int32, device=DEV)
+    B.paged_attn_select_blocks(got, s.query.to(DEV), b.to(DEV), s.tables.to(DEV), s.lens.to(DEV), max_len, s.params(),
+                               num_sink=1, num_recent=2)
+    clean("select")
+    want = O.paged_attn_select_blocks(s.query, values(b, False), s.tables, s.lens, 12, 1, 2, s.op)
+    assert torch.equal(got.cpu(), want)
+
+
+def test_select_far_into_a_sequence_under_a_window():
+    # 640,000 tokens, 40,000 blocks: more than are scored without a window
+    s = Scene([640], 4, 2, 64, 16, window=600)
+    L = 640_000
+    tables = torch.full((1, L // 16), -1, dtype=torch.int32)
+    tables[:, -40:] = s.tables
+    b = s.random_bounds()
+    got = torch.full((1, 2, 9), 99, dtype=torch.int32, device=DEV)
+    B.paged_attn_select_blocks(got, s.query.to(DEV), b.to(DEV), tables.to(DEV), torch.tensor([L], dtype=torch.int32, device=DEV),
+                               L, s.params(), num_recent=2)
+    clean("select")
+    want = O.paged_attn_select_blocks(s.query, values(b, False), s.tables, s.lens, 9, 0, 2, s.op)
+    assert torch.equal(got.cpu(), torch.where(want >= 0, want + L // 16 - 40, -1))
