@@ -467,6 +467,14 @@ def _is(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> tuple:
                      f"{'contiguous' if t.is_contiguous() else 'strided'}, {t.dtype}, {list(t.shape)}")
 
 
+def _int32(value, name: str) -> int:
+    """ctypes would cut it to 32 bits."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{name} must fit in 32 bits, got {value}")
+    return value
+
+
 def _is_cache(t: torch.Tensor, dtype: torch.dtype, block: int) -> int:
     two, blocks, elems = _is(t, "kv_cache", dtype, 3)
     if two != 2 or elems != block:
@@ -561,8 +569,8 @@ def kv_block_bounds(bounds: torch.Tensor, kv_cache: torch.Tensor, block_tables: 
             raise ValueError("context_lens and seq_lens sizes disagree")
         tensors, ctx = tensors + (context_lens,), context_lens.data_ptr()
     _call_on("kv_block_bounds", stream, tensors, bounds.data_ptr(), kv_cache.data_ptr(), nb,
-             block_tables.data_ptr(), wide, ctx, seq_lens.data_ptr(), n, int(max_new_tokens),
-             ctypes.byref(params))
+             block_tables.data_ptr(), wide, ctx, seq_lens.data_ptr(), n,
+             _int32(max_new_tokens, "max_new_tokens"), ctypes.byref(params))
 
 
 def _is_selected(selected: torch.Tensor, n: int, kv_heads: int) -> int:
@@ -592,8 +600,8 @@ def paged_attn_select_blocks(selected: torch.Tensor, query: torch.Tensor, bounds
     _is_rows(query, "query", dtype, n, q_row)
     _call_on("paged_attn_select_blocks", stream, (bounds, selected, query, block_tables, seq_lens),
              selected.data_ptr(), k, query.data_ptr(), n, bounds.data_ptr(), nb,
-             block_tables.data_ptr(), wide, seq_lens.data_ptr(), int(max_seq_len), int(num_sink),
-             int(num_recent), ctypes.byref(params))
+             block_tables.data_ptr(), wide, seq_lens.data_ptr(), _int32(max_seq_len, "max_seq_len"),
+             _int32(num_sink, "num_sink"), _int32(num_recent, "num_recent"), ctypes.byref(params))
 
 
 def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor,

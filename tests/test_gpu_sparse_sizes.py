@@ -98,3 +98,20 @@ def test_select_far_into_a_sequence_under_a_window():
     clean("select")
     want = O.paged_attn_select_blocks(s.query, values(b, False), s.tables, s.lens, 9, 0, 2, s.op)
     assert torch.equal(got.cpu(), torch.where(want >= 0, want + L // 16 - 40, -1))
+
+
+@pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 32) + 40, -(1 << 31) - 1])
+def test_numbers_beyond_32_bits_are_refused(value):
+    # not cut to 32 bits on their way into the library
+    s = Scene([40, 40], 4, 2, 64, 16)
+    p, t, lens = s.params(), s.tables.to(DEV), s.lens.to(DEV)
+    bounds, sel = s.random_bounds().to(DEV), s.selection(2).to(DEV)
+    with pytest.raises(ValueError):
+        B.kv_block_bounds(bounds, s.cache.to(DEV), t, lens, value, p)
+    with pytest.raises(ValueError):
+        B.paged_attn_select_blocks(sel, s.query.to(DEV), bounds, t, lens, value, p)
+    with pytest.raises(ValueError):
+        B.paged_attn_select_blocks(sel, s.query.to(DEV), bounds, t, lens, 40, p, num_sink=value)
+    with pytest.raises(ValueError):
+        B.paged_attn_select_blocks(sel, s.query.to(DEV), bounds, t, lens, 40, p, num_recent=value)
+    clean("refusals")
