@@ -636,6 +636,7 @@ pkv_status pkv_device_error(int64_t *detail) {
   cudaError_t (*readers[kUnits])(unsigned long long *) = {
       read_device_error_kv_ops, read_device_error_decode, read_device_error_prefill,
       read_device_error_rope,   read_device_error_select, read_device_error_sparse};
+  if (cudaDeviceSynchronize() != cudaSuccess) return PKV_ERR_CUDA;
   for (int k = 0; k < kUnits; ++k)
     if (readers[k](&words[k]) != cudaSuccess) return PKV_ERR_CUDA;
   for (int k = 0; k < kUnits; ++k) {

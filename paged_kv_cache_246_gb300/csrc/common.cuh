@@ -26,12 +26,11 @@ __device__ __forceinline__ void record_error(pkv_status code, int64_t detail) {
   atomicCAS(&g_dev_error, 0ull, v);
 }
 
-// Host side: read and clear this unit's word (synchronises the device).
+// Host side, after the caller synchronised the device: read this unit's word and
+// clear it if it is set.
 static inline cudaError_t read_and_clear_unit_error(unsigned long long *out) {
-  cudaError_t e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyFromSymbol(out, g_dev_error, sizeof(*out));
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_dev_error, sizeof(*out));
+  if (e != cudaSuccess || *out == 0) return e;
   const unsigned long long zero = 0ull;
   return cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero));
 }

@@ -115,3 +115,21 @@ def test_numbers_beyond_32_bits_are_refused(value):
     with pytest.raises(ValueError):
         B.paged_attn_select_blocks(sel, s.query.to(DEV), bounds, t, lens, 40, p, num_recent=value)
     clean("refusals")
+
+
+# ---- errors ---------------------------------------------------------------------------
+
+
+def test_one_poll_reports_and_clears_the_errors_of_all_calls():
+    s = Scene([40, 40], 4, 2, 64, 16)
+    p, q, t = s.params(), s.query.to(DEV), s.tables.to(DEV)
+    bounds, sel = s.random_bounds().to(DEV), s.selection(2).to(DEV)
+    bad = torch.tensor([40, 4000], dtype=torch.int32, device=DEV)
+    cache = s.cache.to(DEV)
+    kv = torch.zeros(1, 128, dtype=BF, device=DEV)
+    B.paged_attn_decode_sparse(torch.zeros_like(q), q, cache, t, bad, sel, p)
+    B.kv_cache_write(kv, kv, cache, torch.full((1,), s.blocks * 16, device=DEV), p)
+    B.paged_attn_select_blocks(sel, q, bounds, t, bad, 40, p)
+    torch.cuda.synchronize()
+    assert B.device_error() == (B.PKV_ERR_BOUNDS, 0)      # the write's token
+    assert B.device_error() == (B.PKV_OK, 0)
