@@ -20,6 +20,48 @@ def clean(where):
     assert st == B.PKV_OK, f"{where}: {B.status_string(st)} at {d}"
 
 
+# ---- every place of a long selection is read, and once ----------------------------
+
+
+@pytest.mark.parametrize("seqs,kv_heads,K", [(160, 2, 300), (80, 2, 230), (100, 1, 600), (40, 1, 900), (3, 1, 1100)])
+@pytest.mark.parametrize("heads,D,BS,dtype,fp8", [
+    (1, 128, 16, BF, False), (2, 64, 32, FP, False), (8, 128, 16, FP, True), (12, 64, 16, BF, True)])
+def test_each_place_counts_once(seqs, kv_heads, K, heads, D, BS, dtype, fp8):
+    # Zero queries give every key of the n selected blocks the weight 1 / n.  The
+    # values of place e are 1 in channel e mod D: a place that is lost or read
+    # twice moves its channel by an eighteenth or more.  The sequences' selections end
+    # at every place around a warp's 32nd and 64th unit (of 3, 4 or 8 warps, one or
+    # two units per block) and where the parts of a cluster meet.
+    L = K * BS - 3
+    s = Scene([L], heads * kv_heads, kv_heads, D, BS, dtype, fp8)
+    place = torch.zeros(K, D)
+    place[torch.arange(K), torch.arange(K) % D] = 1.0
+    v = place.view(K, 1, 1, D).expand(K, BS, kv_heads, D).reshape(K, -1)
+    s.cache[1, s.tables[0].long()] = codes(v * SCALE8) if fp8 else v.to(dtype)
+    s.cache[1, s.tables[0, -1].long()].view(BS, -1)[BS - 3:] = 0x7f if fp8 else float("nan")
+    marks = sorted({n for m in (32, 64, 96) for w in (1, 3, 4, 8) for x in (-1, 0, 1)
+                    if 0 < (n := m * w // (BS // 16) + x) <= K} | {1, K // 2, K - 1, K})
+    ends = torch.tensor([marks[-1 - i % len(marks)] for i in range(seqs)])
+    sel = torch.arange(K).view(1, 1, K).expand(seqs, kv_heads, K).clone().int()
+    sel[sel >= ends.view(-1, 1, 1)] = -1
+    p = B.make_params(s.H, kv_heads, D, BS, dtype, 1.0, **s._k)
+    q = torch.zeros(seqs, s.H * D, dtype=dtype, device=DEV)
+    out = torch.full_like(q, float("nan"))
+    tables = s.tables.expand(seqs, -1).contiguous().to(DEV)
+    lens = torch.full((seqs,), L, dtype=torch.int32, device=DEV)
+    B.paged_attn_decode_sparse(out, q, s.cache.to(DEV), tables, lens, sel.to(DEV), p)
+    clean("sparse")
+    keys = torch.full((K,), float(BS))
+    keys[-1] = BS - 3
+    cum = torch.cumsum(keys.view(-1, 1) * place, 0).double()
+    want = (cum / cum.sum(1, keepdim=True))[ends - 1] * (SCALE8 if fp8 else 1.0)
+    got = out.cpu().double().view(seqs, s.H, D)
+    # weights are exactly 1; fp32 sums, one rounding out (fp16 below its normal
+    # range by half of 2^-24)
+    tol = 1.01 * (torch.finfo(dtype).eps / 2 + 2.0 ** -20) * want.abs() + 2.0 ** -25
+    assert ((got - want[:, None]).abs() <= tol[:, None]).all()
+
+
 # ---- selections wider than the sequences -------------------------------------------
 
 
