@@ -165,7 +165,7 @@ static pkv_status make_geometry(const pkv_attn_params *p, int64_t num_blocks, Ge
 
 static pkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
-constexpr int32_t kMaxSelectQuery = 16384;  // query elements of one KV head's group (64 KB as fp32)
+constexpr int32_t kMaxSelectQuery = 16384;  // query elements of one KV head's group (64 KB as fragments)
 constexpr int32_t kMaxMultiQueryLen = 64;  // tokens per sequence of a multi-token decode
 
 }  // namespace pkv

@@ -54,7 +54,7 @@ __device__ __forceinline__ void mma_16832_e4m3(float (&d)[4], uint32_t a0, uint3
 }
 
 // Thread-block clusters: the CTA's rank, the barrier (arrive and wait apart or
-// together), the word or words at `p` of CTA `rank`'s shared memory.
+// together), the word at `p` of CTA `rank`'s shared memory.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -79,17 +79,6 @@ __device__ __forceinline__ uint32_t cluster_load(const void *p, uint32_t rank) {
       "mapa.shared::cluster.u32 a, %1, %2;\n\t"
       "ld.shared::cluster.u32 %0, [a];\n\t}"
       : "=r"(v)
-      : "r"(smem_u32(p)), "r"(rank)
-      : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 cluster_load4(const void *p, uint32_t rank) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-      "ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [a];\n\t}"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
       : "r"(smem_u32(p)), "r"(rank)
       : "memory");
   return v;
