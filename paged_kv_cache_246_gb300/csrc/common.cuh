@@ -199,6 +199,17 @@ __device__ __forceinline__ void split_e4m3x4(float v0, float v1, float v2, float
   lo = pack(v0 - f01.x, v1 - f01.y, v2 - f23.x, v3 - f23.y);
 }
 
+// |x| as bits, 0 for infinities and NaN: the largest of these scales a group of
+// queries, so that one that is not finite leaves the others their bits.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(fabsf(x));
+  return b < 0x7f800000u ? b : 0u;
+}
+// x * mul, and NaN for an infinite x: its E4M3 code would saturate to a finite one.
+__device__ __forceinline__ float scaled_query(float x, float mul) {
+  return fmaf(x, 0.f, x * mul);
+}
+
 // Packed fp32 pairs (Blackwell f32x2 FMA/ADD/MUL) and the 3-input max: the
 // attention inner loops are instruction-bound, and the packed forms halve
 // their per-element arithmetic.

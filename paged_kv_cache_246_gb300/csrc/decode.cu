@@ -415,7 +415,7 @@ decode_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       const uint4 *qp = reinterpret_cast<const uint4 *>(a.query) + (r * D + tq * (D / 4)) / 8;
       return v ? __ldg(qp + s) : make_uint4(0u, 0u, 0u, 0u);
     };
-    uint32_t am = 0;  // largest |q| bit pattern (fp32)
+    uint32_t am = 0;  // largest finite |q|, as bits
 #pragma unroll
     for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -424,7 +424,7 @@ decode_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          am = max(am, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+          am = max(am, max(finite_bits(f.x), finite_bits(f.y)));
         }
       }
     // every warp holds the whole row group, so a warp's max is the group's
@@ -447,8 +447,8 @@ decode_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          v[2 * k] = f.x * mul;
-          v[2 * k + 1] = f.y * mul;
+          v[2 * k] = scaled_query(f.x, mul);
+          v[2 * k + 1] = scaled_query(f.y, mul);
         }
         split_e4m3x4(v[0], v[1], v[2], v[3], qa[s][x], qa[KS8 + s][x]);
         split_e4m3x4(v[4], v[5], v[6], v[7], qa[s][2 + x], qa[KS8 + s][2 + x]);

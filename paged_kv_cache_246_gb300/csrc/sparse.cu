@@ -290,8 +290,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          const uint32_t b0 = __float_as_uint(fabsf(f.x)), b1 = __float_as_uint(fabsf(f.y));
-          am = max(am, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
+          am = max(am, max(finite_bits(f.x), finite_bits(f.y)));
         }
       }
       // (the row's other channels are in the quad's other lanes)
@@ -320,9 +319,8 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = T::to_f2(word_of(u, k));
-          // an infinity becomes NaN, as its scores make the row
-          v[2 * k] = fmaf(f.x, 0.f, f.x * mul[x]);
-          v[2 * k + 1] = fmaf(f.y, 0.f, f.y * mul[x]);
+          v[2 * k] = scaled_query(f.x, mul[x]);
+          v[2 * k + 1] = scaled_query(f.y, mul[x]);
         }
         split_e4m3x4(v[0], v[1], v[2], v[3], qa[s][x], qa[KS8 + s][x]);
         split_e4m3x4(v[4], v[5], v[6], v[7], qa[s][2 + x], qa[KS8 + s][2 + x]);
