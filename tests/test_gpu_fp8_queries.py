@@ -38,3 +38,12 @@ def test_decode_rows_beside_one_that_is_not_finite(H, KVH, D, dtype, multi, bad)
     w = fp8(small(201, dtype=dtype, H=H, KVH=KVH, D=D, multi=multi, seq_lens=[9, 40, 77, 200]))
     hurt = poison(w, lambda r: r.decode_multi() if multi else r.decode(), bad)
     assert (hurt == 0).all()                   # a sum that is NaN
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("H,KVH,D,dtype,alibi", [
+    (4, 2, 128, torch.bfloat16, False), (2, 1, 64, torch.float16, False), (4, 1, 64, torch.bfloat16, True)])
+def test_prefill_rows_beside_one_that_is_not_finite(H, KVH, D, dtype, alibi, bad):
+    w = fp8(chunked(202, [0, 31], [100, 70], dtype=dtype, H=H, KVH=KVH, D=D, alibi=alibi))
+    hurt = poison(w, lambda r: r.prefill(), bad)
+    assert (torch.isnan(hurt) | (hurt == 0)).all()
