@@ -484,11 +484,11 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         }
       }
     }
-    // ---- weights: as two terms of the product's type, p = hi + lo within 2^-18 of it
+    // ---- weights: as two terms of the product's type, p = hi + lo within 2^-17 of it
     // (bf16; fp16 2^-23); their sum l is of the unrounded.  A tile of 8 rows or
     // fewer has the low terms in its other 8 rows (16-bit cache) or, of 4 rows, in
-    // rows 4 .. 7 (fp8): no product more.  (One rounded term put 2^-9 of a bf16
-    // weight into the output; the second costs 0 to 1% there, and where it is a
+    // rows 4 .. 7 (fp8): no product more.  (One rounded term put up to 2^-8 of a
+    // bf16 weight into the output; the second costs 0 to 1% there, and where it is a
     // product of its own 2% of 16 rows over 16 bits and 6 to 9% over fp8.)
     uint32_t pa[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll

@@ -225,3 +225,53 @@ def test_every_bit_of_a_weight_counts(heads, D, dtype, fp8, many):
     # (what rounded weights would give is told apart)
     rounded = w.to(FP if fp8 else dtype).double()
     assert (((v0 + rounded * v1) / (1 + w) - want).abs() > 2 * tol).any()
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,D,fp8", [(4, 1, 128, True), (3, 1, 64, True), (2, 2, 64, True), (8, 4, 128, True),
+                                                  (7, 1, 64, True), (12, 1, 64, True), (4, 1, 64, False), (12, 1, 128, False)])
+def test_every_bit_of_a_weight_counts_under_alibi(heads, kv_heads, D, fp8, many):
+    # Zero queries: the weights are those of the distances alone, another for
+    # every head.  The last keys' values nearly cancel the others' sum, so that
+    # the output is small beside what the weights carry.
+    lens = [32] * (174 if many else 2)
+    s = Scene(lens, heads, kv_heads, D, 16, FP, fp8)
+    slopes = [0.3 * 0.7 ** (h % 5) for h in range(heads)]
+    s.op = dataclasses.replace(s.op, alibi_slopes=torch.tensor(slopes).tolist())
+    s.query.zero_()
+    group = heads // kv_heads
+    v = torch.randn(32, kv_heads, D, generator=s.gen, dtype=torch.float64)
+    dist = torch.arange(32, dtype=torch.float64) - 31
+    w = torch.softmax(torch.tensor(s.op.alibi_slopes, dtype=torch.float64)[:, None] * dist, 1)   # [heads, 32]
+    typed = lambda x: ((x / SCALE8).to(torch.float8_e4m3fn) if fp8 else x.to(FP))  # noqa: E731
+    plain = lambda x: typed(x).double() * (SCALE8 if fp8 else 1.0)  # noqa: E731
+    lead = w.view(kv_heads, group, 32)[:, 0]                  # each group's first head cancels
+    for k in (29, 30, 31):
+        v = plain(v)
+        v[k] = 0
+        v[k] = (-torch.einsum("hk,khd->hd", lead, v) / lead[:, k, None]).clamp(-8, 8)   # E4M3 ends at 8.96
+    v = plain(v)
+    flat = s.cache.view(2, s.blocks, 16, kv_heads, D)
+    for j in range(2):
+        t = typed(v[16 * j:16 * j + 16] + 0.0)
+        flat[1, s.tables[0, j].long()] = t.view(torch.uint8) if fp8 else t
+    s.slopes = s.op.alibi_slopes
+    dev = torch.tensor(s.slopes, device=DEV)
+    p = B.make_params(heads, kv_heads, D, 16, FP, s.op.scale, dev, 0, **s._k)
+    q = s.query.to(DEV)
+    out = torch.full_like(q, 7.0)
+    B.paged_attn_decode_sparse(out, q, s.cache.to(DEV), s.tables.to(DEV), s.lens.to(DEV), s.selection(2).to(DEV), p)
+    torch.cuda.synchronize()
+    assert B.device_error()[0] == B.PKV_OK
+    got = out.cpu().double().view(-1, kv_heads, group, D)[0]
+    wg = w.view(kv_heads, group, 32)
+    want = torch.einsum("hgk,khd->hgd", wg, v)
+    spread = torch.einsum("hgk,khd->hgd", wg, v.abs())
+    # half a step of fp16 (2^-25 below its normal range); the weights' two terms,
+    # the exponential and distances of up to 31 slopes in fp32: 2^-17 in all
+    tol = 1.01 * (2.0 ** -11 * want.abs() + 2.0 ** -17 * spread) + 2.0 ** -25
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).amax((0, 2))
+    if heads == group:                                        # (rounded weights are told apart)
+        rounded = (w / w.amax(1, keepdim=True)).to(FP).double() * w.amax(1, keepdim=True)
+        off = (torch.einsum("hgk,khd->hgd", rounded.view(kv_heads, group, 32), v) - want).abs()
+        assert (off[:, 0] > 2 * tol[:, 0]).any()
