@@ -40,6 +40,7 @@ static inline cudaError_t read_and_clear_unit_error(unsigned long long *out) {
 // ---------------------------------------------------------------------------
 struct BF16 {
   using storage = __nv_bfloat16;
+  static constexpr uint32_t kInf = 0x7f80u;  // bits of infinity
   using pair = __nv_bfloat162;
   // exact widening of a packed pair (low half = first element)
   static __device__ __forceinline__ float2 to_f2(uint32_t w) {
@@ -56,6 +57,7 @@ struct BF16 {
 
 struct FP16 {
   using storage = __half;
+  static constexpr uint32_t kInf = 0x7c00u;
   using pair = __half2;
   static __device__ __forceinline__ float2 to_f2(uint32_t w) {
     __half2 h = *reinterpret_cast<__half2 *>(&w);
@@ -208,6 +210,13 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 // x * mul, and NaN for an infinite x: its E4M3 code would saturate to a finite one.
 __device__ __forceinline__ float scaled_query(float x, float mul) {
   return fmaf(x, 0.f, x * mul);
+}
+// A packed 16-bit pair with its infinities made NaN.
+template <class T>
+__device__ __forceinline__ uint32_t without_infinities(uint32_t w) {
+  if ((w & 0x7fffu) == T::kInf) w |= 1u;
+  if ((w & 0x7fff0000u) == T::kInf << 16) w |= 0x10000u;
+  return w;
 }
 
 // Packed fp32 pairs (Blackwell f32x2 FMA/ADD/MUL) and the 3-input max: the
