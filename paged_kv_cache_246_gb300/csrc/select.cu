@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const BoundsArgs
 // Exactness.  Products of 16-bit values are exact.  A product step sums 16 of
 // them; how the tensor core rounds that is not documented, and it is taken to err
 // by no more than 1.5 * 2^-19 of the largest (as if each term were cut at 2^-23 of it
-// and the sum at 2^-24; the most measured over random terms was 2^-19.6).  It
-// starts from zero, so that errors scale with the step's terms, not the sum so far;
+// and the sum at 2^-24; the most measured, over random terms and those that a climb
+// from them found, was half of that).  It starts from zero, so that errors scale with the step's terms, not the sum so far;
 // the steps' sums are added in fp32, 8 at most in a row and the two rows' sums.
 // With m_h the sum of the steps' largest |q| a score is within
 //     E = max_h (1.5 * 2^-19 m_h + 9 * 2^-24 |q_h|_1) * max |bound|
