@@ -116,6 +116,30 @@ __device__ __forceinline__ uint32_t rest_e4m3x4(const float *v, uint32_t hi, uin
   return c;
 }
 
+// The leading 8 or 11 bits of x: a bf16 value, an fp16 value in its normal range.
+__device__ __forceinline__ float leading(float x, BF16) {
+  return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+__device__ __forceinline__ float leading(float x, FP16) {
+  return __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+}
+// A pair of values >= 0 with zeros replaced: by bf16's 2^-126, by fp16's 2^-24.
+__device__ __forceinline__ uint32_t above_zero(uint32_t w, BF16) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0x00800080u));
+  return d;
+}
+__device__ __forceinline__ uint32_t above_zero(uint32_t w, FP16) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0x00010001u));
+  return d;
+}
+
+// A row's output: zero where no key was visible, NaN where all scores were -infinity.
+__device__ __forceinline__ float joined(float m, float num, float den) {
+  return m == -INFINITY ? 0.f : den == 0.f ? NAN : num / den;
+}
+
 // CTAs per SM that registers are kept for (shared memory allows as many).  One
 // fewer for 8 rows of bf16 over an fp8 cache, which would spill (256 sequences,
 // 8 KV heads of 128: 149 / 157 us; of 64: 90 / 93; fp16, whose third query term
@@ -138,6 +162,9 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   static_assert(KV8 || !fold, "a 16-bit tile's low terms are in rows 8 .. 15");
   constexpr int NR = HALF ? 1 : 2;              // row halves a lane keeps (g, g + 8)
   constexpr int KS = D / 16, NT = D / 8, KS8 = D / 32;
+  // fp16 weights of a 16-bit cache are 2^6 times e^(s - m), 2^14 at most: what takes
+  // the place of a zero low term is 2^-30 of the largest
+  constexpr float kLift = !KV8 && std::is_same<T, FP16>::value ? 6.f : 0.f;
   constexpr bool kThird = KV8 && std::is_same<T, FP16>::value;  // a third query term
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -484,25 +511,37 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         }
       }
     }
-    // ---- weights: as two terms of the product's type, p = hi + lo within 2^-17 of it
-    // (bf16; fp16 2^-23); their sum l is of the unrounded.  A tile of 8 rows or
+    // ---- weights: as two terms of the product's type, p = hi + lo within 2^-16 of it
+    // (bf16; fp16 2^-22); their sum l is of the unrounded.  A tile of 8 rows or
     // fewer has the low terms in its other 8 rows (16-bit cache) or, of 4 rows, in
     // rows 4 .. 7 (fp8): no product more.  (One rounded term put up to 2^-8 of a
     // bf16 weight into the output; the second costs 0 to 1% there, and where it is a
-    // product of its own 2% of 16 rows over 16 bits and 6 to 9% over fp8.)
+    // product of its own 2% of 16 rows over 16 bits and 6 to 9% over fp8.)  Over a
+    // 16-bit cache lo is above zero, so that an infinite value stays one: hi is p's
+    // leading bits, lo what is left or next to nothing.
     uint32_t pa[4] = {0u, 0u, 0u, 0u}, pl[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      const float mr = m[r] == -INFINITY ? 0.f : m[r];
+      const float mr = (m[r] == -INFINITY ? 0.f : m[r]) - kLift;
       float p[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) p[c] = fast_exp2(x[r][c] - mr);
       l[r] += (p[0] + p[1]) + (p[2] + p[3]);
-      pa[r] = MT::from_f2(p[0], p[1]);
-      pa[2 + r] = MT::from_f2(p[2], p[3]);
-      const float2 h01 = MT::to_f2(pa[r]), h23 = MT::to_f2(pa[2 + r]);
-      pl[r] = MT::from_f2(p[0] - h01.x, p[1] - h01.y);
-      pl[2 + r] = MT::from_f2(p[2] - h23.x, p[3] - h23.y);
+      if constexpr (KV8) {
+        pa[r] = MT::from_f2(p[0], p[1]);
+        pa[2 + r] = MT::from_f2(p[2], p[3]);
+        const float2 h01 = MT::to_f2(pa[r]), h23 = MT::to_f2(pa[2 + r]);
+        pl[r] = MT::from_f2(p[0] - h01.x, p[1] - h01.y);
+        pl[2 + r] = MT::from_f2(p[2] - h23.x, p[3] - h23.y);
+      } else {
+        float hi[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) hi[c] = leading(p[c], T{});
+        pa[r] = MT::from_f2(hi[0], hi[1]);
+        pa[2 + r] = MT::from_f2(hi[2], hi[3]);
+        pl[r] = above_zero(MT::from_f2(p[0] - hi[0], p[1] - hi[1]), T{});
+        pl[2 + r] = above_zero(MT::from_f2(p[2] - hi[2], p[3] - hi[3]), T{});
+      }
     }
     if constexpr (HALF) {
       if constexpr (!KV8) {
@@ -590,9 +629,9 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
 
   // ---- the warps' (m, l, O) joined, then the cluster's --------------------------------
   // m is -infinity still where no key was visible, and where every score was NaN
-  // (l and O are NaN) or -infinity (they are 0): these rows take the lowest finite
-  // m, so that they weigh nothing beside a finite score, NaN stays, and 0 / 0 is NaN
-  // where a row had no other
+  // (l and O are NaN) or -infinity (l is 0): these rows take the lowest finite m, so
+  // that they weigh nothing beside a finite score, NaN stays, and a row that had no
+  // other has a sum of 0 and is NaN
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (seen && m[r] == -INFINITY) m[r] = kLowest;
@@ -654,7 +693,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
       }
     }
     if (a.parts == 1) {
-      const float v = M == -INFINITY ? 0.f : num / den * a.v_scale;
+      const float v = joined(M, num, den) * a.v_scale;
       out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
     } else {
       so[(kWarps * kRows + r) * L_::PAD + d] = num;
@@ -687,7 +726,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
         den = fmaf(e, pl[c], den);
       }
     }
-    const float v = M == -INFINITY ? 0.f : num / den * a.v_scale;
+    const float v = joined(M, num, den) * a.v_scale;
     out[i] = static_cast<uint16_t>(T::from_f2(v, 0.f) & 0xffffu);
   }
   cluster_sync();  // no CTA leaves while its shared memory is read

@@ -182,6 +182,33 @@ def test_visible_keys_that_are_infinite(heads, D, dtype, many):
 
 
 @pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("heads,D,dtype", [(4, 64, BF), (8, 128, FP), (12, 128, FP), (17, 64, BF)])
+def test_visible_values_that_are_infinite(heads, D, dtype, zero, many):
+    # an infinite value makes its channel infinite, two of either sign NaN, for
+    # weights of 1 (zero queries) as for any other; the other channels stay
+    lens = [160, 90, 16, 33] + ([16] * 170 if many else [])
+    s = Scene(lens, heads, 1, D, 16, dtype)
+    if zero:
+        s.query.zero_()
+    sel = s.selection(10)
+    want, spread = expected(s, sel)
+    flat = s.cache.view(2, s.blocks, 16, D)
+    flat[1, s.tables[0, 4].long(), 3, 1] = INF
+    flat[1, s.tables[0, 9].long(), 15, 2] = -INF
+    flat[1, s.tables[0, 0].long(), 0, 5] = INF
+    flat[1, s.tables[0, 7].long(), 7, 5] = -INF
+    flat[1, s.tables[2, 0].long(), 15, 9] = -INF
+    flat[1, s.tables[1, 5].long(), 10:, 3] = INF     # past the end: not seen
+    got = decode(s, sel)
+    assert (got[0, :, 1] == INF).all() and (got[0, :, 2] == -INF).all() and (got[2, :, 9] == -INF).all()
+    assert torch.isnan(got[0, :, 5]).all()
+    for b, d in ((0, 1), (0, 2), (0, 5), (2, 9)):
+        got[b, :, d] = want[b, :, d]
+    near(s, got, want, spread, torch.ones(len(lens), heads, dtype=torch.bool), "the other channels")
+
+
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("heads,D,dtype,fp8", [
     (1, 64, BF, False), (8, 128, BF, False), (16, 128, BF, False), (8, 64, FP, False), (12, 64, FP, False),
     (4, 128, BF, True), (8, 64, FP, True), (16, 128, FP, True), (3, 64, FP, True), (6, 64, BF, True)])
