@@ -203,7 +203,7 @@ sparse_kernel(const Args a, const __grid_constant__ CUtensorMap tmap) {
   const int upb = a.BS / kUnit;
   // a valid selection is no longer than the sequence has blocks; behind that only
   // negative numbers may stand, which are looked at below and not shared out
-  const int n_places = min(a.max_selected, nblk + 1);
+  const int n_places = min(a.max_selected, nblk);
   const int units = n_places * upb;
   const int per = (units + a.parts - 1) / a.parts;
   const int u_begin = min(part * per, units), nu = min(per, units - u_begin);

@@ -244,10 +244,11 @@ def test_every_bit_of_a_weight_counts(heads, D, dtype, fp8, many):
         s.op = dataclasses.replace(s.op, scale=1.0)
     got = decode(s, s.selection(1))[0].diagonal()[:heads] if not fp8 else decode(s, s.selection(1))[0, :, 0]
     want, spread = (v0 + w * v1) / (1 + w), (v0.abs() + w * v1) / (1 + w)
-    # half a step of the output; of the weights 2^-17 (two terms of 9 bits and
-    # more, or the fp32 exponential's few 2^-22), once more for the quotient
+    # half a step of the output; of the weights 2^-16 at most (bf16: the leading 8
+    # bits, which leave less than 2^-7, and 8 bits of the rest to half a step) and
+    # 2^-20 for the fp32 exponential, sums and quotient
     half = torch.finfo(dtype).eps / 2
-    tol = 1.01 * (half * want.abs() + 2.0 ** -16 * spread) + 2.0 ** -26
+    tol = 1.01 * half * want.abs() + (2.0 ** -16 + 2.0 ** -20) * spread + 2.0 ** -26
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
     # (what rounded weights would give is told apart)
     rounded = w.to(FP if fp8 else dtype).double()
