@@ -550,6 +550,140 @@ pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_se
                                     int32_t max_selected, const pkv_attn_params *params,
                                     pkv_stream_t stream);
 
+/*
+ * Speculative decoding over trees of drafted tokens.  Where
+ * paged_attn_decode_multi verifies one run of drafted tokens per sequence,
+ * these calls verify a tree of them, over the same cache, block tables and
+ * params.  The attention-backend pages have no counterpart.  A step makes
+ * them in this order:
+ *   kv_cache_write_rope_axes (or another cache write)  store the nodes
+ *   paged_attn_decode_tree                             in every layer
+ *   paged_attn_tree_accept                             once, on the sampled tokens
+ *   kv_commit_tree                                     all layers at once
+ * Sequence b's tree has the rows cu_nodes[b] .. cu_nodes[b + 1] - 1 of the
+ * step's tokens: n_b nodes, node t in row cu_nodes[b] + t.  Node t is stored at
+ * position seq_lens[b] - n_b + t of the sequence (seq_lens counts context and
+ * nodes), whatever its depth; for the rotary embedding, the window and ALiBi
+ * its position is seq_lens[b] - n_b + its depth.
+ *   cu_nodes   int32[num_seqs + 1], ascending, in 0 .. num_tokens; a
+ *              sequence may have no nodes
+ *   parents    int32[num_tokens]: the parent's number within the tree, below
+ *              the node's own; -1: none (depth 0, a child of the context)
+ *   max_nodes  host upper bound on n_b, 1 .. PKV_TREE_MAX_NODES
+ * A sequence whose cu_nodes, n_b or length breaks this, or whose n_b is above
+ * its length, records PKV_ERR_BOUNDS and is skipped; so does a bad parent,
+ * whose node then counts as having none.  Rows behind the last tree stay as
+ * they were.  Like the decode calls they are launched as programmatic
+ * dependents and read and write nothing before the kernel before them has
+ * completed.
+ */
+#define PKV_TREE_MAX_NODES 256
+
+/*
+ * kv_cache_write_rope_axes -- kv_cache_write_rope with positions of several
+ * axes (time, height and width of an image's or a video's patches): pair i of
+ * a head turns by the table's entry i in the row of its own axis,
+ *   c, s = cos_sin[positions[pair_axes[i]][token]][i], [rot_dim / 2 + i].
+ * With all axes' positions equal (text) it does what kv_cache_write_rope does.
+ * The table's columns may hold any frequencies.
+ *
+ *   positions        int64[num_axes][num_tokens]; one outside [0,
+ *                    max_position), of an axis that some pair turns by, is
+ *                    recorded as a bounds error and the token skipped
+ *   positions_stride elements from one axis to the next, >= num_tokens
+ *   num_axes         1 .. 4
+ *   pair_axes        HOST uint8[rot_dim / 2]: each pair's axis, below num_axes
+ *                    (read during the call)
+ * Everything else as kv_cache_write_rope.
+ */
+pkv_status kv_cache_write_rope_axes(void *query_out, int64_t query_out_stride, const void *query,
+                                    int64_t query_stride, const void *key, int64_t key_stride,
+                                    const void *value, int64_t value_stride, int64_t num_tokens,
+                                    const int64_t *positions, int64_t positions_stride,
+                                    int32_t num_axes, const uint8_t *pair_axes,
+                                    const float *cos_sin, int64_t max_position, int32_t rot_dim,
+                                    int32_t interleaved, void *kv_cache, int64_t num_blocks,
+                                    const int64_t *slot_mapping, const pkv_attn_params *params,
+                                    pkv_stream_t stream);
+
+/*
+ * paged_attn_decode_tree -- every node attends to its sequence's context, to
+ * its ancestors and to itself (inside the sliding window, with ALiBi, by the
+ * positions above):
+ *   s_j = scale q.k_j + slope_h (pos_j - pos_i),  out = softmax(s) . V.
+ * A tree whose parents are -1, 0, 1, ... is the run of tokens that
+ * paged_attn_decode_multi takes.
+ *
+ *   out, query   [num_tokens][num_heads * head_size] elements
+ *   seq_lens     int32[num_seqs], at most max_seq_len and max_blocks_per_seq *
+ *                block_size
+ *   workspace    >= paged_attn_decode_tree_workspace_size(...) bytes of device
+ *                scratch, 256-byte aligned.  Contents on entry do not matter;
+ *                calls sharing a workspace must not overlap on the GPU.
+ * Values that are not finite go the way of the formula (a row whose scores hold
+ * a NaN or +infinity, or nothing but -infinity, is NaN), and what a row does
+ * not see does not touch it.  non_causal and more than 128 query heads per KV
+ * head are PKV_ERR_UNSUPPORTED.
+ */
+pkv_status paged_attn_decode_tree(void *out, const void *query, int64_t num_tokens,
+                                  int32_t num_seqs, const int32_t *cu_nodes,
+                                  const int32_t *parents, int32_t max_nodes, const void *kv_cache,
+                                  int64_t num_blocks, const int32_t *block_tables,
+                                  int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, const pkv_attn_params *params,
+                                  void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* Bytes of workspace paged_attn_decode_tree needs (host only; 0 when none is
+ * needed or the arguments are not supported). */
+size_t paged_attn_decode_tree_workspace_size(int32_t num_seqs, int32_t max_nodes,
+                                             int32_t max_seq_len, const pkv_attn_params *params);
+
+/*
+ * paged_attn_tree_accept -- the drafted tokens that the model would have
+ * taken.  From node 0, which is the sequence's last sampled token, the path
+ * goes on to the child whose drafted token equals the token that the model
+ * sampled at the path's node (the lowest of several such children), until
+ * there is none or the path has max_accepted nodes.  The tokens sampled at the
+ * path's nodes are those that decoding one by one would sample.
+ *
+ *   accepted       int32[num_seqs][max_accepted]: the path, ascending node
+ *                  numbers from 0 on, -1 behind the last one
+ *   num_accepted   int32[num_seqs]: its nodes
+ *   next_token     int64[num_seqs]: the token sampled at its last node
+ *   draft_tokens   int64[num_tokens]: each node's own token
+ *   target_tokens  int64[num_tokens]: the token sampled from the model's
+ *                  output at each node
+ *   max_accepted   >= 1
+ * A sequence without nodes, or skipped, has -1s, 0 and token -1.
+ */
+pkv_status paged_attn_tree_accept(int32_t *accepted, int32_t max_accepted, int32_t *num_accepted,
+                                  int64_t *next_token, const int64_t *draft_tokens,
+                                  const int64_t *target_tokens, const int32_t *parents,
+                                  const int32_t *cu_nodes, int32_t num_seqs, int64_t num_tokens,
+                                  int32_t max_nodes, pkv_stream_t stream);
+
+/*
+ * kv_commit_tree -- the accepted nodes' keys and values move behind the
+ * context, in every layer: the rows at position seq_lens[b] - n_b +
+ * accepted[b][i] go to position seq_lens[b] - n_b + i, exactly and as if all
+ * were read before any is written.  The sequence then has seq_lens[b] - n_b +
+ * num_accepted[b] tokens; what lies behind them is left as it was.
+ *
+ *   kv_caches    host array of num_layers device pointers, as kv_copy_blocks;
+ *                num_layers <= 256
+ *   accepted     int32[num_seqs][max_accepted]: ascending node numbers below
+ *                n_b, then negative numbers.  A path that breaks this, or a
+ *                table entry out of range on its way, records PKV_ERR_BOUNDS
+ *                and nothing of the sequence is moved.
+ *   max_accepted 1 .. PKV_TREE_MAX_NODES
+ * Positions of different sequences must not share cache slots.
+ */
+pkv_status kv_commit_tree(void *const *kv_caches, int32_t num_layers, int64_t num_blocks,
+                          const int32_t *accepted, int32_t max_accepted,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *seq_lens, const int32_t *cu_nodes, int32_t num_seqs,
+                          const pkv_attn_params *params, pkv_stream_t stream);
+
 /* Static, never-NULL description of a status code. */
 const char *pkv_status_string(pkv_status status);
 

@@ -7,3 +7,4 @@ nothing from the library: the two share no code.
 """
 from .paged_attention import *  # noqa: F401,F403
 from .sparse_decode import *  # noqa: F401,F403
+from .tree_decode import *  # noqa: F401,F403

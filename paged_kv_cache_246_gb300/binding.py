@@ -22,6 +22,7 @@ PKV_OK, PKV_ERR_INVALID, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_BOUNDS, PKV_
 PKV_FP16, PKV_BF16 = 0, 1
 PKV_CACHE_AUTO, PKV_CACHE_FP8_E4M3 = 0, 1
 PKV_DECODE_STATIC_SCRATCH_BYTES = 64 << 20   # include/pkv.h: paged_attn_decode_noalloc's limit
+PKV_TREE_MAX_NODES = 256        # include/pkv.h: nodes of a sequence's tree of drafted tokens
 PKV_SELECT_MAX_BLOCKS = 32768   # include/pkv.h: blocks per sequence of paged_attn_select_blocks
 _DTYPES = {torch.float16: PKV_FP16, torch.bfloat16: PKV_BF16}
 
@@ -32,7 +33,8 @@ EXPORTS = ("kv_cache_write", "paged_attn_decode", "paged_attn_decode_workspace_s
            "paged_attn_decode_dcp_workspace_size", "paged_attn_dcp_combine",
            "paged_attn_prefill_varlen", "kv_copy_blocks", "kv_swap_blocks",
            "kv_cache_write_rope", "kv_block_bounds", "paged_attn_select_blocks",
-           "paged_attn_decode_sparse",
+           "paged_attn_decode_sparse", "kv_cache_write_rope_axes", "paged_attn_decode_tree",
+           "paged_attn_decode_tree_workspace_size", "paged_attn_tree_accept", "kv_commit_tree",
            "pkv_status_string", "pkv_device_error", "pkv_abi_version",
            "pkv_check_wait_timeout")
 
@@ -88,6 +90,13 @@ def lib() -> ctypes.CDLL:
             "paged_attn_select_blocks": (i32, [vp, i32, vp, i32, vp, i64, vp, i32, vp, i32, i32,
                                                i32, P, vp]),
             "paged_attn_decode_sparse": (i32, [vp, vp, i32, vp, i64, vp, i32, vp, vp, i32, P, vp]),
+            "kv_cache_write_rope_axes": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i32,
+                                               vp, vp, i64, i32, i32, vp, i64, vp, P, vp]),
+            "paged_attn_decode_tree": (i32, [vp, vp, i64, i32, vp, vp, i32, vp, i64, vp, i32, vp,
+                                             i32, P, vp, sz, vp]),
+            "paged_attn_decode_tree_workspace_size": (sz, [i32, i32, i32, P]),
+            "paged_attn_tree_accept": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, i32, i64, i32, vp]),
+            "kv_commit_tree": (i32, [vp, i32, i64, vp, i32, vp, i32, vp, vp, i32, P, vp]),
             "pkv_status_string": (ctypes.c_char_p, [i32]),
             "pkv_device_error": (i32, [ctypes.POINTER(ctypes.c_int64)]),
             "pkv_abi_version": (i32, []),
@@ -619,6 +628,151 @@ def paged_attn_decode_sparse(out: torch.Tensor, query: torch.Tensor, kv_cache: t
              (kv_cache, out, query, block_tables, seq_lens, selected), out.data_ptr(),
              query.data_ptr(), n, kv_cache.data_ptr(), nb, block_tables.data_ptr(), wide,
              seq_lens.data_ptr(), selected.data_ptr(), k, ctypes.byref(params))
+
+
+# ---------------------------------------------------------------------------
+# Speculative decoding over trees of drafted tokens: cache write with positions
+# of several axes, attention, acceptance, commit of the accepted path.  As the
+# calls above they run on the device that holds their tensors.
+# ---------------------------------------------------------------------------
+def rope_pair_axes(sections: Sequence[int], woven: bool = False) -> tuple:
+    """The pair_axes of kv_cache_write_rope_axes for sections[a] pairs of axis
+    a: behind one another, or woven, where axis 0 has all pairs but i = a,
+    a + n, a + 2n, ... (n axes), of which axis a > 0 has the first sections[a]."""
+    sections = [int(x) for x in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 0:
+        raise ValueError("sections must be 1 to 4 counts of pairs")
+    if not woven:
+        return tuple(a for a, n in enumerate(sections) for _ in range(n))
+    n = len(sections)
+    return tuple(i % n if i < n * sections[i % n] else 0 for i in range(sum(sections)))
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axes(axes: tuple) -> tuple:
+    """(array for the call, axes that it names)"""
+    if not axes or not all(isinstance(a, int) and 0 <= a < 4 for a in axes):
+        raise ValueError("pair_axes must name an axis 0 .. 3 for every pair of channels")
+    return (ctypes.c_uint8 * len(axes))(*axes), max(axes) + 1
+
+
+def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                             value: torch.Tensor, kv_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                             positions: torch.Tensor, cos_sin: torch.Tensor,
+                             pair_axes: Sequence[int], params: AttnParams,
+                             interleaved: bool = False, stream=None) -> None:
+    """kv_cache_write_rope with positions [num_axes, T]: pair i of a head turns
+    by the position on axis pair_axes[i] (rope_pair_axes makes the list)."""
+    dtype, cache_dtype, _, _, q_row, kv_row, block = _facts(params)
+    nb = _is_cache(kv_cache, cache_dtype, block)
+    T = _is(slot_mapping, "slot_mapping", torch.int64, 1)[0]
+    axes, n = _is(positions, "positions", torch.int64, 2)
+    if n != T:
+        raise ValueError("positions and slot_mapping sizes disagree")
+    max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
+    array, named = _pair_axes(tuple(pair_axes))
+    if len(array) != rot_dim // 2 or named > axes:
+        raise ValueError(f"pair_axes must name one of the {axes} axes for each of the "
+                         f"{rot_dim // 2} pairs")
+    so = _row_stride(query_out, "query_out", T, q_row, dtype)
+    sq = _row_stride(query, "query", T, q_row, dtype)
+    sk = _row_stride(key, "key", T, kv_row, dtype)
+    sv = _row_stride(value, "value", T, kv_row, dtype)
+    _call_on("kv_cache_write_rope_axes", stream,
+             (kv_cache, query_out, query, key, value, slot_mapping, positions, cos_sin),
+             query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(),
+             sv, T, positions.data_ptr(), T, axes, array, cos_sin.data_ptr(), max_position, rot_dim,
+             1 if interleaved else 0, kv_cache.data_ptr(), nb, slot_mapping.data_ptr(),
+             ctypes.byref(params))
+
+
+def paged_attn_decode_tree_workspace_size(num_seqs: int, max_nodes: int, max_seq_len: int,
+                                          params: AttnParams) -> int:
+    return int(lib().paged_attn_decode_tree_workspace_size(
+        _int32(num_seqs, "num_seqs"), _int32(max_nodes, "max_nodes"),
+        _int32(max_seq_len, "max_seq_len"), ctypes.byref(params)))
+
+
+def _is_trees(cu_nodes: torch.Tensor, n: int) -> None:
+    if _is(cu_nodes, "cu_nodes", torch.int32, 1)[0] != n + 1:
+        raise ValueError("cu_nodes must be [num_seqs + 1]")
+
+
+def paged_attn_decode_tree(out: torch.Tensor, query: torch.Tensor, kv_cache: torch.Tensor,
+                           block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           cu_nodes: torch.Tensor, parents: torch.Tensor, max_nodes: int,
+                           max_seq_len: int, params: AttnParams,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Every node of each sequence's tree of drafted tokens attends to the
+    context, its ancestors and itself.  Node t of sequence b has row cu_nodes[b]
+    + t of query and out, stands in the cache at position seq_lens[b] - nodes +
+    t, and parents (numbers within the tree, -1: none) may be longer than the
+    trees, as the rows may."""
+    dtype, cache_dtype, _, _, q_row, _, block = _facts(params)
+    nb = _is_cache(kv_cache, cache_dtype, block)
+    n, wide = _is_batch(block_tables, seq_lens)
+    _is_trees(cu_nodes, n)
+    T = _is(query, "query", dtype, 2)[0]
+    _is_rows(out, "out", dtype, T, q_row)
+    _is_rows(query, "query", dtype, T, q_row)
+    # rows behind the last tree have no parents
+    T = min(T, _is(parents, "parents", torch.int32, 1)[0])
+    tensors, ws_ptr, ws_bytes = (kv_cache, out, query, block_tables, seq_lens, cu_nodes, parents), None, 0
+    if workspace is not None:
+        _need(workspace, "workspace")
+        tensors = tensors + (workspace,)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call_on("paged_attn_decode_tree", stream, tensors, out.data_ptr(), query.data_ptr(), T, n,
+             cu_nodes.data_ptr(), parents.data_ptr(), _int32(max_nodes, "max_nodes"),
+             kv_cache.data_ptr(), nb, block_tables.data_ptr(), wide, seq_lens.data_ptr(),
+             _int32(max_seq_len, "max_seq_len"), ctypes.byref(params), ws_ptr, ws_bytes)
+
+
+def paged_attn_tree_accept(accepted: torch.Tensor, num_accepted: torch.Tensor,
+                           next_token: torch.Tensor, draft_tokens: torch.Tensor,
+                           target_tokens: torch.Tensor, parents: torch.Tensor,
+                           cu_nodes: torch.Tensor, max_nodes: int, stream=None) -> None:
+    """accepted [num_seqs, K]: the path from node 0 along the children whose
+    drafted token is the one sampled at their parent, -1 behind it; num_accepted
+    [num_seqs] its nodes, next_token [num_seqs] the token sampled at its end."""
+    n, most = _is(accepted, "accepted", torch.int32, 2)
+    if (_is(num_accepted, "num_accepted", torch.int32, 1)[0] != n or
+            _is(next_token, "next_token", torch.int64, 1)[0] != n):
+        raise ValueError("accepted, num_accepted and next_token sizes disagree")
+    _is_trees(cu_nodes, n)
+    T = _is(draft_tokens, "draft_tokens", torch.int64, 1)[0]
+    if (_is(target_tokens, "target_tokens", torch.int64, 1)[0] != T or
+            _is(parents, "parents", torch.int32, 1)[0] != T):
+        raise ValueError("draft_tokens, target_tokens and parents sizes disagree")
+    _call_on("paged_attn_tree_accept", stream,
+             (accepted, num_accepted, next_token, draft_tokens, target_tokens, parents, cu_nodes),
+             accepted.data_ptr(), most, num_accepted.data_ptr(), next_token.data_ptr(),
+             draft_tokens.data_ptr(), target_tokens.data_ptr(), parents.data_ptr(),
+             cu_nodes.data_ptr(), n, T, _int32(max_nodes, "max_nodes"))
+
+
+def kv_commit_tree(kv_caches: Sequence[torch.Tensor], accepted: torch.Tensor,
+                   block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_nodes: torch.Tensor,
+                   params: AttnParams, stream=None) -> None:
+    """In every layer's cache, each sequence's rows of the nodes accepted [num_seqs,
+    K] (as paged_attn_tree_accept gives them) move behind its context."""
+    if len(kv_caches) == 0:
+        return
+    _, cache_dtype, _, _, _, _, block = _facts(params)
+    nb = _is_cache(kv_caches[0], cache_dtype, block)
+    shape = kv_caches[0].shape
+    for k, c in enumerate(kv_caches):
+        if _is(c, "kv_caches", cache_dtype, 3) != shape:
+            raise ValueError("all caches must have the same number of blocks")
+    n, wide = _is_batch(block_tables, seq_lens)
+    seqs, most = _is(accepted, "accepted", torch.int32, 2)
+    if seqs != n:
+        raise ValueError("accepted must be [num_seqs, max_accepted]")
+    _is_trees(cu_nodes, n)
+    array = (ctypes.c_void_p * len(kv_caches))(*[c.data_ptr() for c in kv_caches])
+    _call_on("kv_commit_tree", stream, (*kv_caches, accepted, block_tables, seq_lens, cu_nodes),
+             array, len(kv_caches), nb, accepted.data_ptr(), most, block_tables.data_ptr(), wide,
+             seq_lens.data_ptr(), cu_nodes.data_ptr(), n, ctypes.byref(params))
 
 
 def check_wait_timeout(tag: int, stream=None) -> None:

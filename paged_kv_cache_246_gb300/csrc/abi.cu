@@ -1,6 +1,6 @@
 // extern "C" front end of libpkv.so: argument validation, device selection
 // and dispatch to the kernels of kv_ops.cu, decode.cu, prefill.cu, rope.cu,
-// select.cu and sparse.cu.
+// select.cu, sparse.cu, tree.cu and tree_ops.cu.
 // Everything here runs on the host; nothing reads device memory.
 #include <cudaTypedefs.h>
 
@@ -434,6 +434,33 @@ pkv_status paged_attn_prefill_varlen(void *out, const void *query, int64_t num_q
 
 static bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; }
 
+// The checks that both rotating writes share; PKV_OK with *empty set: nothing to do.
+static pkv_status check_rope(const RopeCall &r, int64_t num_blocks, const pkv_attn_params *params,
+                             Geometry *g, bool *empty) {
+  *empty = false;
+  pkv_status st = make_geometry(params, num_blocks, g);
+  if (st != PKV_OK) return st;
+  if (r.num_tokens < 0 || r.max_position <= 0 || (r.interleaved != 0 && r.interleaved != 1))
+    return PKV_ERR_INVALID;
+  if (r.rot_dim <= 0 || r.rot_dim > g->D) return PKV_ERR_INVALID;
+  if (r.rot_dim % 16 != 0 || r.num_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  const int64_t q_row = static_cast<int64_t>(g->H) * g->D;
+  if (!row_stride_ok(r.query_out_stride, q_row) || !row_stride_ok(r.query_stride, q_row) ||
+      !row_stride_ok(r.key_stride, g->row_elems) || !row_stride_ok(r.value_stride, g->row_elems))
+    return PKV_ERR_INVALID;
+  *empty = r.num_tokens == 0;
+  if (*empty) return PKV_OK;
+  if (!r.query_out || !r.query || !r.key || !r.value || !r.positions || !r.cos_sin ||
+      !r.kv_cache || !r.slot_mapping)
+    return PKV_ERR_INVALID;
+  if (!aligned(r.query_out, 16) || !aligned(r.query, 16) || !aligned(r.key, 16) ||
+      !aligned(r.value, 16) || !aligned(r.positions, 8) || !aligned(r.cos_sin, 16) ||
+      !aligned(r.kv_cache, 16) || !aligned(r.slot_mapping, 8))
+    return PKV_ERR_INVALID;
+  if (r.query_out == r.query && r.query_out_stride != r.query_stride) return PKV_ERR_INVALID;
+  return PKV_OK;
+}
+
 pkv_status kv_cache_write_rope(void *query_out, int64_t query_out_stride, const void *query,
                                int64_t query_stride, const void *key, int64_t key_stride,
                                const void *value, int64_t value_stride, int64_t num_tokens,
@@ -441,33 +468,45 @@ pkv_status kv_cache_write_rope(void *query_out, int64_t query_out_stride, const 
                                int64_t max_position, int32_t rot_dim, int32_t interleaved,
                                void *kv_cache, int64_t num_blocks, const int64_t *slot_mapping,
                                const pkv_attn_params *params, pkv_stream_t stream) {
-  Geometry g;
-  pkv_status st = make_geometry(params, num_blocks, &g);
-  if (st != PKV_OK) return st;
-  if (num_tokens < 0 || max_position <= 0 || (interleaved != 0 && interleaved != 1))
-    return PKV_ERR_INVALID;
-  if (rot_dim <= 0 || rot_dim > g.D) return PKV_ERR_INVALID;
-  if (rot_dim % 16 != 0 || num_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  const int64_t q_row = static_cast<int64_t>(g.H) * g.D;
-  if (!row_stride_ok(query_out_stride, q_row) || !row_stride_ok(query_stride, q_row) ||
-      !row_stride_ok(key_stride, g.row_elems) || !row_stride_ok(value_stride, g.row_elems))
-    return PKV_ERR_INVALID;
-  if (num_tokens == 0) return PKV_OK;
-  if (!query_out || !query || !key || !value || !positions || !cos_sin || !kv_cache ||
-      !slot_mapping)
-    return PKV_ERR_INVALID;
-  if (!aligned(query_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
-      !aligned(positions, 8) || !aligned(cos_sin, 16) || !aligned(kv_cache, 16) ||
-      !aligned(slot_mapping, 8))
-    return PKV_ERR_INVALID;
-  if (query_out == query && query_out_stride != query_stride) return PKV_ERR_INVALID;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  DeviceScope scope;
-  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
   const RopeCall r = {query_out,    query_out_stride, query,     query_stride, key,
                       key_stride,   value,            value_stride, num_tokens, positions,
                       cos_sin,      max_position,     rot_dim,   interleaved,  kv_cache,
                       slot_mapping};
+  Geometry g;
+  bool empty;
+  pkv_status st = check_rope(r, num_blocks, params, &g, &empty);
+  if (st != PKV_OK || empty) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  return from_cuda(launch_rope_write(r, g, s));
+}
+
+pkv_status kv_cache_write_rope_axes(void *query_out, int64_t query_out_stride, const void *query,
+                                    int64_t query_stride, const void *key, int64_t key_stride,
+                                    const void *value, int64_t value_stride, int64_t num_tokens,
+                                    const int64_t *positions, int64_t positions_stride,
+                                    int32_t num_axes, const uint8_t *pair_axes,
+                                    const float *cos_sin, int64_t max_position, int32_t rot_dim,
+                                    int32_t interleaved, void *kv_cache, int64_t num_blocks,
+                                    const int64_t *slot_mapping, const pkv_attn_params *params,
+                                    pkv_stream_t stream) {
+  const RopeCall r = {query_out,    query_out_stride, query,     query_stride, key,
+                      key_stride,   value,            value_stride, num_tokens, positions,
+                      cos_sin,      max_position,     rot_dim,   interleaved,  kv_cache,
+                      slot_mapping, pair_axes,        positions_stride};
+  Geometry g;
+  bool empty;
+  pkv_status st = check_rope(r, num_blocks, params, &g, &empty);
+  if (st != PKV_OK) return st;
+  if (num_axes < 1 || positions_stride < num_tokens || !pair_axes) return PKV_ERR_INVALID;
+  if (num_axes > 4) return PKV_ERR_UNSUPPORTED;
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (pair_axes[i] >= num_axes) return PKV_ERR_INVALID;
+  if (empty) return PKV_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
   return from_cuda(launch_rope_write(r, g, s));
 }
 
@@ -555,6 +594,111 @@ pkv_status paged_attn_decode_sparse(void *out, const void *query, int32_t num_se
                                         s));
 }
 
+static bool tree_batch_ok(int64_t num_tokens, int32_t num_seqs) {
+  return num_seqs >= 0 && num_seqs <= 65535 && num_tokens >= 0;
+}
+
+// Whether paged_attn_decode_tree takes these params.
+static bool tree_supported(const Geometry &g, int64_t num_tokens) {
+  return !g.non_causal && g.QPK <= 128 && g.KVH <= 65535 && num_tokens <= 0x7fffffffLL / g.H;
+}
+
+size_t paged_attn_decode_tree_workspace_size(int32_t num_seqs, int32_t max_nodes,
+                                             int32_t max_seq_len, const pkv_attn_params *params) {
+  Geometry g;
+  if (make_geometry(params, 1, &g) != PKV_OK || num_seqs <= 0 || num_seqs > 65535 ||
+      max_nodes <= 0 || max_nodes > PKV_TREE_MAX_NODES || max_seq_len < 0 || !tree_supported(g, 0))
+    return 0;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) dev.sms = 152;
+  return tree_workspace_bytes(num_seqs, max_nodes, max_seq_len, g, dev.sms);
+}
+
+pkv_status paged_attn_decode_tree(void *out, const void *query, int64_t num_tokens,
+                                  int32_t num_seqs, const int32_t *cu_nodes,
+                                  const int32_t *parents, int32_t max_nodes, const void *kv_cache,
+                                  int64_t num_blocks, const int32_t *block_tables,
+                                  int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, const pkv_attn_params *params,
+                                  void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (!tree_batch_ok(num_tokens, num_seqs) || max_nodes < 1 || max_seq_len < 0 ||
+      max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID;
+  if (max_nodes > PKV_TREE_MAX_NODES || !tree_supported(g, num_tokens)) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!out || !query || !cu_nodes || !parents || !kv_cache || !block_tables || !seq_lens)
+    return PKV_ERR_INVALID;
+  if (!aligned(out, 16) || !aligned(query, 16) || !aligned(kv_cache, 16) ||
+      !aligned(cu_nodes, 4) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4))
+    return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  DeviceInfo dev;
+  if (current_device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  const size_t need = tree_workspace_bytes(num_seqs, max_nodes, max_seq_len, g, dev.sms);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_INVALID;
+  const TreeBatch t = {cu_nodes, parents, num_tokens, num_seqs, max_nodes};
+  return from_cuda(launch_tree_decode(out, query, t, kv_cache, block_tables, max_blocks_per_seq,
+                                      seq_lens, max_seq_len, g, workspace, s));
+}
+
+pkv_status paged_attn_tree_accept(int32_t *accepted, int32_t max_accepted, int32_t *num_accepted,
+                                  int64_t *next_token, const int64_t *draft_tokens,
+                                  const int64_t *target_tokens, const int32_t *parents,
+                                  const int32_t *cu_nodes, int32_t num_seqs, int64_t num_tokens,
+                                  int32_t max_nodes, pkv_stream_t stream) {
+  if (!tree_batch_ok(num_tokens, num_seqs) || max_nodes < 1 || max_accepted < 1)
+    return PKV_ERR_INVALID;
+  if (max_nodes > PKV_TREE_MAX_NODES || num_tokens > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  if (!accepted || !num_accepted || !next_token || !cu_nodes) return PKV_ERR_INVALID;
+  if (num_tokens > 0 && (!draft_tokens || !target_tokens || !parents)) return PKV_ERR_INVALID;
+  if (!aligned(accepted, 4) || !aligned(num_accepted, 4) || !aligned(next_token, 8) ||
+      !aligned(draft_tokens, 8) || !aligned(target_tokens, 8) || !aligned(parents, 4) ||
+      !aligned(cu_nodes, 4))
+    return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  const TreeBatch t = {cu_nodes, parents, num_tokens, num_seqs, max_nodes};
+  return from_cuda(launch_tree_accept(accepted, max_accepted, num_accepted, next_token,
+                                      draft_tokens, target_tokens, t, s));
+}
+
+pkv_status kv_commit_tree(void *const *kv_caches, int32_t num_layers, int64_t num_blocks,
+                          const int32_t *accepted, int32_t max_accepted,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *seq_lens, const int32_t *cu_nodes, int32_t num_seqs,
+                          const pkv_attn_params *params, pkv_stream_t stream) {
+  Geometry g;
+  pkv_status st = make_geometry(params, num_blocks, &g);
+  if (st != PKV_OK) return st;
+  if (!tree_batch_ok(0, num_seqs) || num_layers < 0 || num_layers > 256 ||
+      max_accepted < 1 || max_blocks_per_seq <= 0)
+    return PKV_ERR_INVALID;
+  if (max_accepted > PKV_TREE_MAX_NODES || g.row_bytes / 16 > 0x3fffffffLL)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || num_layers == 0) return PKV_OK;
+  if (!kv_caches || !accepted || !block_tables || !seq_lens || !cu_nodes) return PKV_ERR_INVALID;
+  if (!aligned(accepted, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_nodes, 4))
+    return PKV_ERR_INVALID;
+  for (int l = 0; l < num_layers; ++l)
+    if (!kv_caches[l] || !aligned(kv_caches[l], 16)) return PKV_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  DeviceScope scope;
+  if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;
+  const TreeBatch t = {cu_nodes, nullptr, 0x7fffffffLL, num_seqs, PKV_TREE_MAX_NODES};
+  return from_cuda(launch_commit_tree(kv_caches, num_layers, accepted, max_accepted, block_tables,
+                                      max_blocks_per_seq, seq_lens, t, g, s));
+}
+
 pkv_status kv_copy_blocks(void *const *kv_caches, int32_t num_layers, int64_t num_blocks,
                           const int64_t *pairs, int64_t num_pairs, const pkv_attn_params *params,
                           pkv_stream_t stream) {
@@ -631,11 +775,12 @@ pkv_status pkv_check_wait_timeout(int64_t tag, pkv_stream_t stream) {
 }
 
 pkv_status pkv_device_error(int64_t *detail) {
-  constexpr int kUnits = 6;
+  constexpr int kUnits = 8;
   unsigned long long words[kUnits] = {};
   cudaError_t (*readers[kUnits])(unsigned long long *) = {
       read_device_error_kv_ops, read_device_error_decode, read_device_error_prefill,
-      read_device_error_rope,   read_device_error_select, read_device_error_sparse};
+      read_device_error_rope,   read_device_error_select, read_device_error_sparse,
+      read_device_error_tree,   read_device_error_tree_ops};
   if (cudaDeviceSynchronize() != cudaSuccess) return PKV_ERR_CUDA;
   for (int k = 0; k < kUnits; ++k)
     if (readers[k](&words[k]) != cudaSuccess) return PKV_ERR_CUDA;

@@ -101,6 +101,9 @@ struct RopeCall {
   int32_t rot_dim, interleaved;
   void *kv_cache;
   const int64_t *slot_mapping;
+  // positions of several axes: each pair's (host array), elements between them; null: one
+  const uint8_t *pair_axes = nullptr;
+  int64_t positions_stride = 0;
 };
 cudaError_t launch_rope_write(const RopeCall &r, const Geometry &g, cudaStream_t stream);
 cudaError_t read_device_error_rope(unsigned long long *out);
@@ -137,6 +140,29 @@ cudaError_t launch_sparse_decode(void *out, const void *query, int num_seqs, con
                                  const int32_t *seq_lens, const int32_t *selected,
                                  int max_selected, const Geometry &g, cudaStream_t stream);
 cudaError_t read_device_error_sparse(unsigned long long *out);
+
+// tree.cu, tree_ops.cu (speculative decoding over trees)
+struct TreeBatch {
+  const int32_t *cu_nodes, *parents;
+  int64_t num_tokens;
+  int num_seqs, max_nodes;
+};
+cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
+                               const void *kv_cache, const int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *seq_lens, int max_seq_len,
+                               const Geometry &g, void *workspace, cudaStream_t stream);
+size_t tree_workspace_bytes(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g,
+                            int sms);
+cudaError_t read_device_error_tree(unsigned long long *out);
+cudaError_t launch_tree_accept(int32_t *accepted, int max_accepted, int32_t *num_accepted,
+                               int64_t *next_token, const int64_t *draft_tokens,
+                               const int64_t *target_tokens, const TreeBatch &t,
+                               cudaStream_t stream);
+cudaError_t launch_commit_tree(void *const *caches, int num_layers, const int32_t *accepted,
+                               int max_accepted, const int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *seq_lens, const TreeBatch &t,
+                               const Geometry &g, cudaStream_t stream);
+cudaError_t read_device_error_tree_ops(unsigned long long *out);
 
 // Lets a kernel take as much dynamic shared memory as the device grants beside
 // its static `reserved` bytes; asked once per kernel and device (`done`: a bit

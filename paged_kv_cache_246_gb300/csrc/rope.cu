@@ -1,5 +1,5 @@
-// kv_cache_write_rope: the cache write with the rotary position embedding on
-// the way.  Per pair (x1, x2) of channels and the position's cos c, sin s:
+// kv_cache_write_rope, kv_cache_write_rope_axes: the cache write with the rotary
+// position embedding on the way.  Per pair (x1, x2) of channels and the position's cos c, sin s:
 //     y1 = x1 c - x2 s,   y2 = x2 c + x1 s      (fp32, one rounding out)
 // Queries go to query_out, keys (rotated) and values to their cache slots.
 //
@@ -29,6 +29,13 @@ struct Args {
   int64_t row_bytes;  // of the cache
   int H, KVH, rot;
   float k_scale, v_scale, k_inv, v_inv;  // and their reciprocals (0: divide)
+};
+
+// Positions of several axes: elements from one axis to the next, and the axis
+// of each of up to 64 pairs, 2 bits apiece.
+struct Axes {
+  int64_t stride;
+  uint32_t bits[4];
 };
 
 __device__ __forceinline__ void widen(float (&f)[8], const uint4 &u, BF16) {
@@ -89,6 +96,115 @@ __device__ __forceinline__ void rotate(float &x1, float &x2, float c, float s) {
   x2 = y2;
 }
 
+// Item i of a token: two 16-byte chunks, c0 and c1, of one of its H + 2 KVH
+// heads, and which of the two turn.
+template <int D, bool INTER>
+struct Item {
+  static constexpr int LPH = D / 16;  // lanes per head
+  int j, c0, c1, hh;
+  bool rot0, rot1, is_q, is_v;
+  __device__ __forceinline__ Item(const Args &a, int i) {
+    const int head = i / LPH;
+    j = i % LPH;
+    if constexpr (INTER) {
+      c0 = 2 * j;
+      c1 = c0 + 1;
+      rot0 = c0 * 8 < a.rot;
+      rot1 = c1 * 8 < a.rot;
+    } else {
+      const int half = a.rot / 16;
+      rot0 = rot1 = j < half;
+      c0 = rot0 ? j : 2 * j;
+      c1 = rot0 ? j + half : 2 * j + 1;
+    }
+    is_q = head < a.H;
+    is_v = head >= a.H + a.KVH;
+    hh = is_q ? head : is_v ? head - a.H - a.KVH : head - a.H;
+  }
+  template <bool BULK>
+  __device__ __forceinline__ void load(const Args &a, int64_t t, uint4 &u0, uint4 &u1) const {
+    const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+    const uint4 *s4 =
+        reinterpret_cast<const uint4 *>((is_q ? a.q : is_v ? a.v : a.k) + t * stride + hh * D);
+    u0 = BULK ? __ldcs(s4 + c0) : s4[c0];
+    u1 = BULK ? __ldcs(s4 + c1) : s4[c1];
+  }
+};
+
+// Four cosines or sines of a row in global or in shared memory.
+template <bool SHARED>
+__device__ __forceinline__ float4 row4(const float *p) {
+  return SHARED ? *reinterpret_cast<const float4 *>(p) : __ldg(reinterpret_cast<const float4 *>(p));
+}
+
+// The item's chunks turned by the row `cs` (rot / 2 cosines, then sines), and stored.
+template <class T, int D, bool KV8, bool INTER, bool BULK, bool SHARED>
+__device__ __forceinline__ void finish(const Args &a, const Item<D, INTER> &it, int64_t t,
+                                       int64_t slot, const float *cs, uint4 u0, uint4 u1) {
+  const int c0 = it.c0, c1 = it.c1;
+  const bool turn = !it.is_v && (it.rot0 || it.rot1);
+  if (turn || (KV8 && !it.is_q)) {
+    float x0[8], x1[8];
+    widen(x0, u0, T{});
+    widen(x1, u1, T{});
+    if (turn) {
+      const int half = a.rot / 2;
+      if constexpr (INTER) {
+        // chunk c holds pairs 4c .. 4c + 3
+        const float4 ca = row4<SHARED>(cs + 4 * c0), sa = row4<SHARED>(cs + half + 4 * c0);
+        rotate(x0[0], x0[1], ca.x, sa.x);
+        rotate(x0[2], x0[3], ca.y, sa.y);
+        rotate(x0[4], x0[5], ca.z, sa.z);
+        rotate(x0[6], x0[7], ca.w, sa.w);
+        if (it.rot1) {
+          const float4 cb = row4<SHARED>(cs + 4 * c1), sb = row4<SHARED>(cs + half + 4 * c1);
+          rotate(x1[0], x1[1], cb.x, sb.x);
+          rotate(x1[2], x1[3], cb.y, sb.y);
+          rotate(x1[4], x1[5], cb.z, sb.z);
+          rotate(x1[6], x1[7], cb.w, sb.w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 cc = row4<SHARED>(cs + 8 * it.j + e);
+          const float4 ss = row4<SHARED>(cs + half + 8 * it.j + e);
+          rotate(x0[e], x1[e], cc.x, ss.x);
+          rotate(x0[e + 1], x1[e + 1], cc.y, ss.y);
+          rotate(x0[e + 2], x1[e + 2], cc.z, ss.z);
+          rotate(x0[e + 3], x1[e + 3], cc.w, ss.w);
+        }
+      }
+    }
+    if (KV8 && !it.is_q) {
+      const float scale = it.is_v ? a.v_scale : a.k_scale;
+      uint2 *d2 = reinterpret_cast<uint2 *>((it.is_v ? a.v_half : a.k_half) + slot * a.row_bytes +
+                                            it.hh * D);
+      const float inv = it.is_v ? a.v_inv : a.k_inv;
+      const uint2 w0 = codes8(x0, scale, inv), w1 = codes8(x1, scale, inv);
+      if constexpr (BULK) {
+        __stcs(d2 + c0, w0);
+        __stcs(d2 + c1, w1);
+      } else {
+        d2[c0] = w0;
+        d2[c1] = w1;
+      }
+      return;
+    }
+    if (it.rot0) u0 = narrow<T>(x0);
+    if (it.rot1) u1 = narrow<T>(x1);
+  }
+  uint4 *d4 = it.is_q ? reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + it.hh * D)
+                      : reinterpret_cast<uint4 *>((it.is_v ? a.v_half : a.k_half) +
+                                                  slot * a.row_bytes + it.hh * D * 2);
+  if constexpr (BULK) {
+    __stcs(d4 + c0, u0);
+    __stcs(d4 + c1, u1);
+  } else {
+    d4[c0] = u0;
+    d4[c1] = u1;
+  }
+}
+
 // CTA = one token; thread i takes the lane slots i, i + blockDim, ... of the
 // token's (H + 2 KVH) heads.  The row is loaded before slot and position are
 // looked at (that of a token to be skipped is only read), so one memory latency
@@ -103,108 +219,68 @@ __device__ __forceinline__ void rotate(float &x1, float &x2, float c, float s) {
 template <class T, int D, bool KV8, bool INTER, bool BULK>
 __global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? 8 : 1)
 rope_write_kernel(const Args a) {
-  constexpr int LPH = D / 16;  // lanes per head
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t t = blockIdx.x;
-  const int items = (a.H + 2 * a.KVH) * LPH;
+  const int items = (a.H + 2 * a.KVH) * (D / 16);
   for (int i = threadIdx.x; i < items; i += blockDim.x) {
-    const int head = i / LPH, j = i % LPH;
-    // this lane's two chunks of the head
-    int c0, c1;
-    bool rot0, rot1;
-    if constexpr (INTER) {
-      c0 = 2 * j;
-      c1 = c0 + 1;
-      rot0 = c0 * 8 < a.rot;
-      rot1 = c1 * 8 < a.rot;
-    } else {
-      const int half = a.rot / 16;
-      rot0 = rot1 = j < half;
-      c0 = rot0 ? j : 2 * j;
-      c1 = rot0 ? j + half : 2 * j + 1;
-    }
-    const bool is_q = head < a.H, is_v = head >= a.H + a.KVH;
-    const int hh = is_q ? head : is_v ? head - a.H - a.KVH : head - a.H;
-    const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-    const uint16_t *src = (is_q ? a.q : is_v ? a.v : a.k) + t * stride + hh * D;
-    const uint4 *s4 = reinterpret_cast<const uint4 *>(src);
-    uint4 u0 = BULK ? __ldcs(s4 + c0) : s4[c0], u1 = BULK ? __ldcs(s4 + c1) : s4[c1];
+    const Item<D, INTER> it(a, i);
+    uint4 u0, u1;
+    it.template load<BULK>(a, t, u0, u1);
     const int64_t slot = __ldg(a.slots + t), pos = __ldg(a.positions + t);
     if (slot < 0) return;  // padding token
     if (slot >= a.num_slots || pos < 0 || pos >= a.max_position) {
       if (i == 0) record_error(PKV_ERR_BOUNDS, t);
       return;
     }
-    const bool turn = !is_v && (rot0 || rot1);
-    if (turn || (KV8 && !is_q)) {
-      float x0[8], x1[8];
-      widen(x0, u0, T{});
-      widen(x1, u1, T{});
-      if (turn) {
-        const float *cs = a.cos_sin + pos * a.rot;
-        const int half = a.rot / 2;
-        if constexpr (INTER) {
-          // chunk c holds pairs 4c .. 4c + 3
-          const float4 ca = __ldg(reinterpret_cast<const float4 *>(cs + 4 * c0));
-          const float4 sa = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * c0));
-          rotate(x0[0], x0[1], ca.x, sa.x);
-          rotate(x0[2], x0[3], ca.y, sa.y);
-          rotate(x0[4], x0[5], ca.z, sa.z);
-          rotate(x0[6], x0[7], ca.w, sa.w);
-          if (rot1) {
-            const float4 cb = __ldg(reinterpret_cast<const float4 *>(cs + 4 * c1));
-            const float4 sb = __ldg(reinterpret_cast<const float4 *>(cs + half + 4 * c1));
-            rotate(x1[0], x1[1], cb.x, sb.x);
-            rotate(x1[2], x1[3], cb.y, sb.y);
-            rotate(x1[4], x1[5], cb.z, sb.z);
-            rotate(x1[6], x1[7], cb.w, sb.w);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 cc = __ldg(reinterpret_cast<const float4 *>(cs + 8 * j + e));
-            const float4 ss = __ldg(reinterpret_cast<const float4 *>(cs + half + 8 * j + e));
-            rotate(x0[e], x1[e], cc.x, ss.x);
-            rotate(x0[e + 1], x1[e + 1], cc.y, ss.y);
-            rotate(x0[e + 2], x1[e + 2], cc.z, ss.z);
-            rotate(x0[e + 3], x1[e + 3], cc.w, ss.w);
-          }
-        }
-      }
-      if (KV8 && !is_q) {
-        const float scale = is_v ? a.v_scale : a.k_scale;
-        uint2 *d2 = reinterpret_cast<uint2 *>((is_v ? a.v_half : a.k_half) +
-                                              slot * a.row_bytes + hh * D);
-        const float inv = is_v ? a.v_inv : a.k_inv;
-        const uint2 w0 = codes8(x0, scale, inv), w1 = codes8(x1, scale, inv);
-        if constexpr (BULK) {
-          __stcs(d2 + c0, w0);
-          __stcs(d2 + c1, w1);
-        } else {
-          d2[c0] = w0;
-          d2[c1] = w1;
-        }
-        continue;
-      }
-      if (rot0) u0 = narrow<T>(x0);
-      if (rot1) u1 = narrow<T>(x1);
-    }
-    uint4 *d4 = is_q ? reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + hh * D)
-                     : reinterpret_cast<uint4 *>((is_v ? a.v_half : a.k_half) +
-                                                 slot * a.row_bytes + hh * D * 2);
-    if constexpr (BULK) {
-      __stcs(d4 + c0, u0);
-      __stcs(d4 + c1, u1);
-    } else {
-      d4[c0] = u0;
-      d4[c1] = u1;
-    }
+    finish<T, D, KV8, INTER, BULK, false>(a, it, t, slot, a.cos_sin + pos * a.rot, u0, u1);
+  }
+}
+
+// Positions of several axes: the CTA first gathers its token's cosines and
+// sines, each from its pair's own row of the table, into shared memory (the
+// first items' rows are on their way meanwhile); from there the heads' lanes
+// read them as the kernel above reads a table row.  The pairs' axes, 2 bits
+// each, are launch arguments.
+template <class T, int D, bool KV8, bool INTER, bool BULK>
+__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? 8 : 1)
+rope_axes_write_kernel(const Args a, const Axes x) {
+  __shared__ __align__(16) float row[128];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int items = (a.H + 2 * a.KVH) * (D / 16);
+  int i = threadIdx.x;
+  uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+  if (i < items) Item<D, INTER>(a, i).template load<BULK>(a, t, u0, u1);
+  const int64_t slot = __ldg(a.slots + t);
+  bool bad = slot >= a.num_slots;
+  const int half = a.rot / 2;
+  for (int p = threadIdx.x; p < a.rot; p += blockDim.x) {
+    const int pair = p < half ? p : p - half;
+    const uint32_t axis = (x.bits[pair / 16] >> (2 * (pair % 16))) & 3u;
+    const int64_t pos = __ldg(a.positions + axis * x.stride + t);
+    if (pos < 0 || pos >= a.max_position)
+      bad = true;
+    else
+      row[p] = __ldg(a.cos_sin + pos * a.rot + p);
+  }
+  bad = __syncthreads_or(bad);
+  if (slot < 0) return;  // padding token
+  if (bad) {
+    if (threadIdx.x == 0) record_error(PKV_ERR_BOUNDS, t);
+    return;
+  }
+  while (i < items) {
+    finish<T, D, KV8, INTER, BULK, true>(a, Item<D, INTER>(a, i), t, slot, row, u0, u1);
+    i += blockDim.x;
+    if (i < items) Item<D, INTER>(a, i).template load<BULK>(a, t, u0, u1);
   }
 }
 
 template <class T, int D, bool KV8>
-static cudaError_t launch_typed(const Args &a, bool interleaved, cudaStream_t stream) {
+static cudaError_t launch_typed(const Args &a, const Axes *x, bool interleaved,
+                                cudaStream_t stream) {
   const int items = (a.H + 2 * a.KVH) * (D / 16);
   DeviceInfo dev;
   cudaError_t e = current_device_info(&dev);
@@ -212,11 +288,14 @@ static cudaError_t launch_typed(const Args &a, bool interleaved, cudaStream_t st
   const bool bulk = a.num_tokens > 6LL * dev.sms;
   PdlLaunch cfg(dim3(static_cast<unsigned>(a.num_tokens)),
                 std::min(bulk ? 192 : 512, (items + 31) / 32 * 32), 0, stream);
-  if (bulk)
-    return interleaved ? cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, true, true>, a)
-                       : cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, false, true>, a);
-  return interleaved ? cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, true, false>, a)
-                     : cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, false, false>, a);
+#define PKV_ROPE_FORM(IN, BULK)                                                             \
+  return x ? cudaLaunchKernelEx(&cfg.c, rope_axes_write_kernel<T, D, KV8, IN, BULK>, a, *x) \
+           : cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, IN, BULK>, a)
+  if (bulk && interleaved) PKV_ROPE_FORM(true, true);
+  if (bulk) PKV_ROPE_FORM(false, true);
+  if (interleaved) PKV_ROPE_FORM(true, false);
+  PKV_ROPE_FORM(false, false);
+#undef PKV_ROPE_FORM
 }
 
 }  // namespace rope
@@ -248,11 +327,16 @@ cudaError_t launch_rope_write(const RopeCall &r, const Geometry &g, cudaStream_t
   auto inverse = [](float x) { return x >= 0x1p-100f && x <= 0x1p100f ? 1.f / x : 0.f; };
   a.k_inv = inverse(g.k_scale);
   a.v_inv = inverse(g.v_scale);
+  rope::Axes x = {r.positions_stride, {0, 0, 0, 0}};
+  if (r.pair_axes)
+    for (int i = 0; i < r.rot_dim / 2; ++i)
+      x.bits[i / 16] |= static_cast<uint32_t>(r.pair_axes[i]) << (2 * (i % 16));
+  const rope::Axes *axes = r.pair_axes ? &x : nullptr;
   const bool bf = g.dtype == PKV_BF16, in = r.interleaved != 0;
 #define PKV_ROPE(TT, DD)                                                     \
   if (g.D == DD)                                                             \
-    return g.fp8 ? rope::launch_typed<TT, DD, true>(a, in, stream)           \
-                 : rope::launch_typed<TT, DD, false>(a, in, stream);
+    return g.fp8 ? rope::launch_typed<TT, DD, true>(a, axes, in, stream)     \
+                 : rope::launch_typed<TT, DD, false>(a, axes, in, stream);
   if (bf) {
     PKV_ROPE(BF16, 128) PKV_ROPE(BF16, 64)
   } else {
