@@ -1,6 +1,6 @@
 // Inline-PTX wrappers for the 5th-generation tensor core (tcgen05), tensor
 // memory (TMEM) and the 128-byte-swizzled shared-memory operand layout, as
-// used by the prefill kernel.  sm_100a-family only (built for sm_103a).
+// used by the prefill and tree kernels.  sm_100a-family only (built for sm_103a).
 #pragma once
 
 #include "common.cuh"
@@ -144,6 +144,43 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
           smem_u32(bar))
       : "memory");
 }
+
+// A bounded wait of a CTA whose roles stop together: false when it ran out
+// (PKV_ERR_TIMEOUT recorded, the abort flag raised) or another role raised the
+// flag.
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
+                                              volatile uint32_t *abort_flag, int64_t where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1u;
+      record_error(PKV_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+
+// Warp-uniform verdict of a bounded wait performed by every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
+                                          volatile uint32_t *abort_flag, int64_t where) {
+  const bool got = wait_or_abort(bar, parity, abort_flag, where);
+  return __all_sync(0xffffffffu, got);
+}
+
+// The operand type's field of an instruction descriptor.
+template <class T>
+struct AB;
+template <>
+struct AB<BF16> {
+  static constexpr int v = 1;
+};
+template <>
+struct AB<FP16> {
+  static constexpr int v = 0;
+};
 
 // 3-D tiled TMA load.
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar,

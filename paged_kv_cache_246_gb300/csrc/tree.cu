@@ -4,16 +4,71 @@
 // where a context key's position is its place in the cache and a node's is the
 // context's length plus its depth.
 //
-// The plainest form: CTA = (node, query head), four warps take the keys in
-// turn, each lane D / 32 channels, with a running maximum and sum.
-#include <algorithm>
-
+// Rows are (node, query head of the KV group) pairs, node by node, in tiles of
+// 128: 128 / QPK nodes each.  The step reads the context's K and V once per
+// KV head, so it is bound by HBM up to some 250 rows (2 flops per row and byte
+// against 281 of the card) and by the tensor core above; mma.sync tiles of 16
+// rows, as the other decodes use, would read K and V from L2 once per tile.
+//
+// CTA = one per SM, persistent.  The work is the list of (sequence, KV head,
+// 128-key tile) units in this order; every CTA takes an equal, contiguous
+// share of it, found from seq_lens and cu_nodes on the device, and walks it
+// segment by segment (a segment: its part of one sequence's KV head).  A
+// segment that is a whole (sequence, KV head) writes the output; a part writes
+// its (o, m, l) in fp32, and combine_kernel merges the parts in order.  So all
+// SMs read the same amount whatever the lengths are, and every CTA has at most
+// two partial segments (its first and its last).  Trees that need more than two
+// row tiles are cut into groups; group i runs on the CTAs i, i + groups, ...,
+// which walk the same units at the same time, so that K and V come from L2 for
+// all groups but one.
+//
+// Roles of the 12 warps:
+//   warp 0      TMA producer: query rows of each segment, K and V tiles of 128
+//               keys, one box (block_size rows x 64 channels, 128-byte swizzle)
+//               per cache block; blocks out of the visible range are loaded
+//               from an out-of-range coordinate and arrive as zeros.
+//   warp 1      MMA issuer (one thread): S = Q K^T into one of two score
+//               buffers in tensor memory, O += P V with P read from there.
+//   warps 2, 3  look through the V tiles that some row sees only in part (the
+//               tree's, and the window's edge): rows hidden from all are
+//               zeroed, values that are not finite are zeroed and the segment
+//               is marked, since 0 * NaN in the product would reach rows that
+//               do not see them (the rows that do get them back at the end).
+//               Over an 8-bit cache they also widen the V codes to fp16.
+//   warps 4-7, 8-11  softmax groups A and B: thread r owns row r.
+// With one row tile (PAIR = false) A takes the even key tiles and B the odd
+// ones, each with its own running maximum, sum and accumulator, and the two are
+// merged at the segment's end; with more (PAIR) A and B take a row tile each.
+// Either way one group's softmax runs under the other's products.
+//
+// The weights enter P V as two 16-bit terms (hi + lo): a single rounded term
+// puts up to 2^-9 of a bf16 weight into the output, as much as the output's own
+// rounding.  Over an 8-bit cache P is fp16, whose 2^-12 does not show in a bf16
+// output: one term there, two for fp16 outputs.
+// Over an 8-bit cache q.k runs on the codes as they are (kind::f8f6f4), each
+// query row scaled by a power of two to its own largest finite component and
+// split into E4M3 terms (two for the 8 bits of bf16, three for the 11 of fp16).
+//
+// Every wait is bounded; a timeout raises a CTA-wide flag, the roles stop,
+// copies and products in flight are drained, tensor memory is freed.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+#include <type_traits>
+
+#include "tcgen05.cuh"
 #include "tree.cuh"
 
 namespace pkv {
 namespace tree {
+
+using tc5::AB;
+using tc5::wait_or_abort;
+using tc5::warp_wait;
+
+constexpr int kThreads = 384;
+constexpr int BM = 128, BN = 128;
+constexpr int kMaskWords = PKV_TREE_MAX_NODES / 32;
 
 struct Args {
   TreeBatch tb;
@@ -22,130 +77,1049 @@ struct Args {
   const uint8_t *cache;
   const int32_t *block_tables, *seq_lens;
   const float *alibi;
+  float *part_o;     // [CTA][2][row tile][D / 4][128][4]
+  float2 *part_ml;   // [CTA][2][row tile][128]: maximum (log2 units), sum
+  int4 *record;      // [CTA]: sequence, KV head, further CTAs of the item that its last segment begins
   int64_t num_blocks, row_elems;
-  int max_blocks_per_seq, max_seq_len, H, QPK, BS, window;
+  int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window, groups;
   float scale_log2, v_scale;
 };
 
-constexpr int kMax = PKV_TREE_MAX_NODES;
+// ---------------------------------------------------------------------------
+// The list of work
+// ---------------------------------------------------------------------------
+struct Seq {
+  int row, nodes, ctx, L, kv_lo, kv_start, tiles;
+};
 
+// Sequence b for a CTA whose rows begin at node0; false: nothing to do, `bad`
+// where what the tensors say cannot be.
+__device__ __forceinline__ bool seq_of(const Args &a, int b, int node0, Seq &s, bool &bad) {
+  bad = !nodes_of(a.tb, b, s.row, s.nodes);
+  s.L = __ldg(a.seq_lens + b);
+  if (bad || s.nodes == 0) return false;
+  bad = s.L < s.nodes || s.L > a.max_seq_len ||
+        s.L > static_cast<int64_t>(a.max_blocks_per_seq) * a.BS;
+  if (bad || s.nodes <= node0) return false;
+  s.ctx = s.L - s.nodes;
+  // the first position that a node of depth 0 sees: deeper ones see less
+  s.kv_lo = a.window > 0 ? max(0, s.ctx - a.window + 1) : 0;
+  s.kv_start = s.kv_lo / BN * BN;
+  s.tiles = (s.L - s.kv_start + BN - 1) / BN;
+  return true;
+}
+
+struct Seg {
+  Seq s;
+  int b, g, j0, n;  // tiles j0 .. j0 + n - 1 of KV head g
+  __device__ __forceinline__ bool whole() const { return n == s.tiles; }
+};
+
+// A CTA's segments, in order: every role walks them by itself.
+struct Walk {
+  int b, node0;
+  int64_t off, left;  // units into sequence b; units to go
+  bool known = false;
+  Seq s;
+  __device__ __forceinline__ bool next(const Args &a, Seg &o) {
+    while (left > 0 && b < a.tb.num_seqs) {
+      if (!known) {
+        bool bad;
+        if (!seq_of(a, b, node0, s, bad)) {
+          ++b;
+          continue;
+        }
+        known = true;
+      }
+      o.s = s;
+      o.b = b;
+      o.g = static_cast<int>(off / s.tiles);
+      o.j0 = static_cast<int>(off - static_cast<int64_t>(o.g) * s.tiles);
+      o.n = static_cast<int>(min(static_cast<int64_t>(s.tiles - o.j0), left));
+      left -= o.n;
+      off += o.n;
+      if (off == static_cast<int64_t>(s.tiles) * a.KVH) {
+        ++b;
+        off = 0;
+        known = false;
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// Whether some row sees the tile of keys from kv0 on only in part.
+__device__ __forceinline__ bool edge_tile(const Args &a, const Seq &s, int kv0) {
+  return kv0 + BN > s.ctx || (a.window > 0 && kv0 < s.ctx + s.nodes - a.window);
+}
+
+// ---------------------------------------------------------------------------
+// Shared memory
+// ---------------------------------------------------------------------------
+template <class T, int D, bool KV8, bool PAIR>
+struct Lay {
+  static constexpr int REG = 128 * 128;  // a 64-channel region of 128 rows
+  static constexpr int NREG = D / 64;
+  static constexpr int TILE = REG * NREG;
+  static constexpr int TILE8 = BN * D;
+  static constexpr int TERMS = std::is_same_v<T, FP16> ? 3 : 2;  // E4M3 terms of a query
+  // the largest rings that fit
+  static constexpr bool TIGHT = KV8 && PAIR && TERMS == 3 && D == 128;
+  static constexpr int NK = KV8 ? 0 : (D == 128 ? 2 : 4);
+  static constexpr int NV = KV8 ? 2 : (D == 128 ? 2 : 4);
+  static constexpr int N8K = !KV8 ? 0 : TIGHT ? 2 : D == 128 ? 3 : 6;
+  static constexpr int N8V = !KV8 ? 0 : TIGHT ? 1 : D == 128 ? 2 : 4;
+  static constexpr int NQ = KV8 ? 1 : PAIR ? 1 : 2;  // query buffers (of one or two row tiles)
+  static constexpr int OFF_Q = 0;
+  static constexpr int Q_BYTES = KV8 ? (PAIR ? 2 : 1) * TERMS * TILE8 : 2 * TILE;
+  static constexpr int OFF_K = OFF_Q + Q_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * TILE;
+  static constexpr int OFF_K8 = OFF_V + NV * TILE;
+  static constexpr int OFF_V8 = OFF_K8 + N8K * TILE8;
+  static constexpr int OFF_MASK = OFF_V8 + N8V * TILE8;  // [words + 2][256 threads]
+  static constexpr int OFF_ML = OFF_MASK + (kMaskWords + 2) * 256 * 4;  // [2][128] float2
+  static constexpr int OFF_EXP = OFF_ML + 2 * 128 * 8;                  // [2][2][128] 2^e of the queries
+  static constexpr int OFF_BAR = OFF_EXP + 2 * 2 * 128 * 4;
+  // copies landed (K, V, Q), stages free again (EK, EV, EQ), V looked through
+  // (VG), V codes widened (E8V), scores ready (S), weights ready (P), product
+  // done (O), both groups' maxima written (ML), both accumulators read (EPI)
+  static constexpr int NKT = KV8 ? N8K : NK, NVT = KV8 ? N8V : NV;
+  static constexpr int B_K = 0, B_EK = B_K + NKT, B_V = B_EK + NKT, B_VG = B_V + NVT,
+                       B_EV = B_VG + NV, B_E8V = B_EV + NV, B_Q = B_E8V + N8V, B_EQ = B_Q + 2,
+                       B_S = B_EQ + 2, B_P = B_S + 2, B_O = B_P + 2, B_ML = B_O + 2,
+                       B_EPI = B_ML + 1, B_FIN = B_EPI + 1, NBAR = B_FIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 512;
+  // one CTA owns an SM and its tensor memory
+  static constexpr int ALLOC = std::max(BYTES + 1024, 118 * 1024);
+  static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+// Words of the MISC area.
+enum { kTmem = 0, kAbort = 1, kIssuedK = 2, kIssuedV = 3, kIssuedQ = 4, kStart = 6, kFlags = 16, kScan = 32 };
+constexpr int kFlagSlots = 16;  // twice as many as segments that can be under way at once
+
+// The element of a 16-bit pair that is not finite: bits of its half, else 0.
+template <class T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & T::kInf) == T::kInf ? 0xffffu : 0u) |
+         ((w & (T::kInf << 16)) == T::kInf << 16 ? 0xffff0000u : 0u);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// What the look through V took out of it goes back into the rows that see it:
+// every visible value that is not finite, in the tiles that rows see in part,
+// is added to the row's elements as they stand in memory.  Rare.
 template <class T, int D, bool KV8>
-__global__ void __launch_bounds__(128) simple_kernel(const Args a) {
-  __shared__ int depth[kMax];
-  __shared__ uint32_t seen[kMax / 32];
-  __shared__ float part[4][D + 2];
+__device__ __noinline__ void add_not_finite(const Args &a, const Seg &seg, int lo, int c0, int cols,
+                                            const uint32_t *mask, uint16_t *out, float *part) {
+  const int32_t *trow = a.block_tables + static_cast<int64_t>(seg.b) * a.max_blocks_per_seq;
+  auto key = [&](int pos) {
+    const int pb = __ldg(trow + pos / a.BS);
+    if (pb < 0 || pb >= a.num_blocks) return;
+    const int64_t at = ((a.num_blocks + pb) * a.BS + pos % a.BS) * a.row_elems + seg.g * D + c0;
+    for (int d = 0; d < cols; ++d) {
+      float v;
+      if constexpr (KV8)
+        v = (a.cache[at + d] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
+      else
+        v = T::to_f(reinterpret_cast<const uint16_t *>(a.cache)[at + d]);
+      if (fabsf(v) < INFINITY) continue;
+      if (out)
+        out[c0 + d] = static_cast<uint16_t>(T::from_f2(T::to_f(out[c0 + d]) + v, 0.f));
+      else
+        part[static_cast<int64_t>((c0 + d) / 4) * 512 + (c0 + d) % 4] += v;
+    }
+  };
+  for (int j = seg.j0; j < seg.j0 + seg.n; ++j) {
+    const int kv0 = seg.s.kv_start + j * BN;
+    if (!edge_tile(a, seg.s, kv0)) continue;
+    for (int pos = max(kv0, lo); pos < min(kv0 + BN, seg.s.ctx); ++pos) key(pos);
+    for (int c = max(0, kv0 - seg.s.ctx); c < min(seg.s.nodes, kv0 + BN - seg.s.ctx); ++c)
+      if (mask[(c / 32 + 1) * 256] >> (c % 32) & 1) key(seg.s.ctx + c);
+  }
+}
+
+template <class T, int D, bool KV8, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
+               const __grid_constant__ CUtensorMap kvmap) {
+  using L = Lay<T, D, KV8, PAIR>;
+  using OPT = std::conditional_t<KV8, FP16, T>;  // operand type of P V
+  constexpr bool TWO = !KV8 || std::is_same_v<T, FP16>;  // weights in two terms
+  constexpr int NV = L::NV, NKT = L::NKT, NVT = L::NVT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+  volatile uint32_t *abort_flag = misc + kAbort;
+  volatile uint32_t *flags = misc + kFlags;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t where = blockIdx.x;
+  const int nodes_per_tile = BM / a.QPK;
+  const int tile_rows = nodes_per_tile * a.QPK;
+  const int group = blockIdx.x % a.groups, slot = blockIdx.x / a.groups;
+  const int slots = gridDim.x / a.groups;
+  const int node0 = group * (PAIR ? 2 : 1) * nodes_per_tile;
+
+  // ---- before the kernel ahead has completed: nothing that it may write ----
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NBAR; ++i) {
+      uint32_t count = 1;
+      if (i >= L::B_VG && i < L::B_VG + NV) count = 64;
+      if (KV8 && i >= L::B_E8V && i < L::B_E8V + L::N8V) count = 64;
+      if (KV8 && (i == L::B_Q || i == L::B_Q + 1)) count = 128;
+      if (i == L::B_P || i == L::B_P + 1) count = 128;
+      if (i == L::B_ML || i == L::B_EPI) count = 256;
+      mbar_init(&bars[i], count);
+    }
+    misc[kAbort] = 0;
+    misc[kIssuedK] = misc[kIssuedV] = misc[kIssuedQ] = 0;
+    for (int i = 0; i < kFlagSlots; ++i) misc[kFlags + i] = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kvmap);
+  }
+  if (warp == 1) tc5::tmem_alloc<512>(misc + kTmem);
+  if constexpr (!KV8) {
+    // rows that no copy writes (128 is no multiple of QPK): finite once and for all
+    for (int i = threadIdx.x; i < 2 * L::NREG * (BM - tile_rows) * 8; i += kThreads) {
+      const int per = (BM - tile_rows) * 8;
+      *reinterpret_cast<uint4 *>(smem + L::OFF_Q + (i / per) * L::REG + tile_rows * 128 +
+                                 (i % per) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  const int b = blockIdx.z, t = blockIdx.y, h = blockIdx.x;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int row, n;
-  bool ok = nodes_of(a.tb, b, row, n);
-  const int L = __ldg(a.seq_lens + b);
-  ok = ok && L >= n && L <= a.max_seq_len &&
-       L <= static_cast<int64_t>(a.max_blocks_per_seq) * a.BS;
-  if (!ok) {
-    if (threadIdx.x == 0 && t == 0 && h == 0) record_error(PKV_ERR_BOUNDS, b);
-    return;
-  }
-  if (t >= n) return;
-  const int ctx = L - n;
-  auto parent = [&](int c) -> int {
-    const int p = __ldg(a.tb.parents + row + c);
-    if (p >= -1 && p < c) return p;
-    record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(row) + c);
-    return -1;
-  };
-  for (int c = threadIdx.x; c < n; c += blockDim.x) {
-    int d = -1;
-    for (int p = c; p >= 0; p = parent(p)) ++d;
-    depth[c] = d;
-  }
-  if (threadIdx.x < kMax / 32) seen[threadIdx.x] = 0;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    for (int p = t; p >= 0; p = parent(p)) seen[p / 32] |= 1u << (p % 32);
-  __syncthreads();
-  const int mine = ctx + depth[t];
-  const float slope = a.alibi ? __ldg(a.alibi + h) * kLog2e : 0.f;
-  constexpr int E = D / 32;
-  float q[E], o[E];
-  const uint16_t *qr = a.query + (static_cast<int64_t>(row + t) * a.H + h) * D + lane * E;
+
+  // ---- this CTA's share of the units ----
+  Walk walk;
+  int64_t total, u0, u1;
+  int shares;
+  {
+    int64_t *scan = reinterpret_cast<int64_t *>(misc + kScan);  // [12 warps]
+    auto units = [&](int b) -> int64_t {
+      Seq s;
+      bool bad = false;
+      int64_t u = 0;
+      if (b < a.tb.num_seqs) {
+        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(s.tiles) * a.KVH;
+        if (bad && blockIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
+      }
+      return u;
+    };
+    // inclusive sum over the CTA's threads; every thread gets the sum over all
+    auto block_scan = [&](int64_t v, int64_t &all) -> int64_t {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = T::to_f(qr[e]);
-    o[e] = 0.f;
+      for (int d = 1; d < 32; d *= 2) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+      }
+      if (lane == 31) scan[warp] = v;
+      __syncthreads();
+      int64_t before = 0;
+      all = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
+      }
+      __syncthreads();
+      return v + before;
+    };
+    const int64_t mine = units(threadIdx.x);
+    int64_t first_all;
+    const int64_t first_incl = block_scan(mine, first_all);
+    total = first_all;
+    for (int b0 = kThreads; b0 < a.tb.num_seqs; b0 += kThreads) {
+      int64_t all;
+      block_scan(units(b0 + threadIdx.x), all);
+      total += all;
+    }
+    shares = static_cast<int>(min(static_cast<int64_t>(slots), total));  // no empty ones among them
+    u0 = slot < shares ? total * slot / shares : total;
+    u1 = slot < shares ? total * (slot + 1) / shares : total;
+    // the sequence that holds unit u0
+    int64_t *start = reinterpret_cast<int64_t *>(misc + kStart);  // sequence, units into it
+    auto find = [&](int b, int64_t incl, int64_t own) {
+      if (u0 < incl && u0 >= incl - own) {
+        start[0] = b;
+        start[1] = u0 - (incl - own);
+      }
+    };
+    find(threadIdx.x, first_incl, mine);
+    int64_t base = first_all;
+    for (int b0 = kThreads; b0 < a.tb.num_seqs && base <= u0; b0 += kThreads) {
+      int64_t all;
+      const int64_t own = units(b0 + threadIdx.x), incl = base + block_scan(own, all);
+      find(b0 + threadIdx.x, incl, own);
+      base += all;
+    }
+    tc5::fence_before_sync();
+    __syncthreads();
+    tc5::fence_after_sync();
+    walk.node0 = node0;
+    walk.left = u1 - u0;
+    walk.b = walk.left > 0 ? static_cast<int>(start[0]) : 0;
+    walk.off = walk.left > 0 ? start[1] : 0;
   }
-  float m = -INFINITY, l = 0.f;
-  const int g = h / a.QPK;
-  const int lo = a.window > 0 ? max(0, mine - a.window + 1) : 0;
-  auto value = [&](int64_t elem) -> float {
-    if constexpr (KV8) {
-      const __half_raw x = __nv_cvt_fp8_to_halfraw(a.cache[elem], __NV_E4M3);
-      return __half2float(__half(x));
-    } else {
-      return T::to_f(reinterpret_cast<const uint16_t *>(a.cache)[elem]);
+  const uint32_t tmem = misc[kTmem];
+
+  auto producer = [&]() {
+    const int TB = BN / a.BS;
+    // lane l < TB: where cache block l of the segment's key tile j lies, or an
+    // out-of-range row (zeros) outside the visible range or for a bad entry
+    auto coord_of = [&](const Seg &s, int j) -> int {
+      int coord = -a.BS;
+      if (lane < TB) {
+        const int lb = (s.s.kv_start + (s.j0 + j) * BN) / a.BS + lane;
+        const int p0 = lb * a.BS;
+        if (p0 < s.s.L && p0 + a.BS > s.s.kv_lo) {
+          const int64_t e = static_cast<int64_t>(s.b) * a.max_blocks_per_seq + lb;
+          const int pb = __ldg(a.block_tables + e);
+          if (pb < 0 || pb >= a.num_blocks)
+            record_error(PKV_ERR_BOUNDS, e);
+          else
+            coord = pb * a.BS;
+        }
+      }
+      return coord;
+    };
+    Seg s, ahead;
+    bool have = walk.next(a, s);
+    int next = have ? coord_of(s, 0) : 0;
+    int it = 0;  // key tiles
+    for (int si = 0; have; ++si) {
+      const bool more = walk.next(a, ahead);
+      for (int j = 0; j < s.n; ++j, ++it) {
+        const int coord = next;
+        next = j + 1 < s.n ? coord_of(s, j + 1) : more ? coord_of(ahead, 0) : 0;
+        const int sk = it % NKT, sv = it % NVT;
+        if (it >= NKT && !warp_wait(&bars[L::B_EK + sk], ((it / NKT) - 1) & 1, abort_flag, where))
+          return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars[L::B_K + sk], KV8 ? L::TILE8 : L::TILE);
+          misc[kIssuedK] = it + 1;
+        }
+        __syncwarp();
+        if (lane < TB) {
+          if constexpr (KV8) {
+            tma_load_4d(smem + L::OFF_K8 + sk * L::TILE8 + lane * a.BS * D, &kvmap,
+                        &bars[L::B_K + sk], 0, s.g, coord, 0);
+          } else {
+            for (int r = 0; r < L::NREG; ++r)
+              tma_load_4d(smem + L::OFF_K + sk * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
+                          &bars[L::B_K + sk], 64 * r, s.g, coord, 0);
+          }
+        }
+        if (!KV8 && j == 0) {
+          const int q = si % L::NQ;
+          if (si >= L::NQ &&
+              !warp_wait(&bars[L::B_EQ + q], ((si / L::NQ) - 1) & 1, abort_flag, where))
+            return;
+          if (lane == 0) {
+            constexpr int X = PAIR ? 2 : 1;
+            mbar_arrive_expect_tx(&bars[L::B_Q + q], X * L::NREG * tile_rows * 128);
+            misc[kIssuedQ] = si + 1;
+            for (int x = 0; x < X; ++x)
+              for (int r = 0; r < L::NREG; ++r)
+                tc5::tma_load_3d(smem + L::OFF_Q + (q + x) * L::TILE + r * L::REG, &qmap,
+                                 &bars[L::B_Q + q], 64 * r, s.g * a.QPK,
+                                 s.s.row + node0 + x * nodes_per_tile);
+          }
+          __syncwarp();
+        }
+        const int ev = KV8 ? L::B_E8V : L::B_EV;
+        if (it >= NVT && !warp_wait(&bars[ev + sv], ((it / NVT) - 1) & 1, abort_flag, where))
+          return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars[L::B_V + sv], KV8 ? L::TILE8 : L::TILE);
+          misc[kIssuedV] = it + 1;
+        }
+        __syncwarp();
+        if (lane < TB) {
+          if constexpr (KV8) {
+            tma_load_4d(smem + L::OFF_V8 + sv * L::TILE8 + lane * a.BS * D, &kvmap,
+                        &bars[L::B_V + sv], 0, s.g, coord, 1);
+          } else {
+            for (int r = 0; r < L::NREG; ++r)
+              tma_load_4d(smem + L::OFF_V + sv * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
+                          &bars[L::B_V + sv], 64 * r, s.g, coord, 1);
+          }
+        }
+      }
+      have = more;
+      s = ahead;
     }
   };
-  for (int j = warp; j < L; j += 4) {
-    int pos = j;
-    if (j < ctx) {
-      if (j < lo) continue;
-    } else {
-      const int c = j - ctx;
-      pos = ctx + depth[c];
-      if (!(seen[c / 32] >> (c % 32) & 1) || pos < lo) continue;
+
+  auto issuer = [&]() {
+    constexpr uint32_t ID_QK = tc5::idesc_f16(KV8 ? 0 : AB<OPT>::v, 0, BM, BN);
+    constexpr uint32_t ID_PV = tc5::idesc_f16(AB<OPT>::v, 1, BM, D);
+    auto desc8 = [&](uint32_t off) -> uint64_t {
+      return D == 128 ? tc5::sdesc_sw128(sbase + off, 16, 1024)
+                      : tc5::sdesc_sw64(sbase + off, 16, 512);
+    };
+    const uint64_t q_desc = KV8 ? desc8(L::OFF_Q) : tc5::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
+    const uint64_t k_desc = KV8 ? desc8(L::OFF_K8) : tc5::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
+    const uint64_t v_desc = tc5::sdesc_sw128(sbase + L::OFF_V, L::REG, 1024);
+    Seg s;
+    int base = 0;           // key tiles before the segment
+    int done[2] = {0, 0};   // weight tiles consumed per group
+    for (int si = 0; walk.next(a, s); ++si) {
+      const int q = si % L::NQ;
+      if (!wait_or_abort(&bars[L::B_Q + q], (si / L::NQ) & 1, abort_flag, where)) return;
+      if (KV8 && PAIR && !wait_or_abort(&bars[L::B_Q + 1], si & 1, abort_flag, where)) return;
+      tc5::fence_after_sync();
+      const int ops = PAIR ? 2 * s.n : s.n;
+      // op i: group i & 1, key tile i (i / 2 where the groups share it)
+      auto qk = [&](int i) -> bool {
+        const int x = i & 1, t = base + (PAIR ? i >> 1 : i), sk = t % NKT;
+        if (!PAIR || x == 0) {
+          if (!wait_or_abort(&bars[L::B_K + sk], (t / NKT) & 1, abort_flag, where)) return false;
+          tc5::fence_after_sync();
+        }
+        const uint32_t sb = tmem + x * 128;
+        if constexpr (KV8) {
+          const uint64_t qb = q_desc + static_cast<uint64_t>(((PAIR ? x : 0) * L::TERMS * L::TILE8) >> 4);
+          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE8) >> 4);
+#pragma unroll
+          for (int e = 0; e < L::TERMS; ++e)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              tc5::mma_ss_f8(sb, qb + static_cast<uint64_t>((e * L::TILE8 + k * 32) >> 4),
+                             kb + static_cast<uint64_t>(k * 2), ID_QK, (e | k) ? 1u : 0u);
+        } else {
+          const uint64_t qb = q_desc + static_cast<uint64_t>(((q + (PAIR ? x : 0)) * L::TILE) >> 4);
+          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE) >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = static_cast<uint64_t>(((k / 4) * L::REG + (k % 4) * 32) >> 4);
+            tc5::mma_ss(sb, qb + off, kb + off, ID_QK, k > 0 ? 1u : 0u);
+          }
+        }
+        tc5::commit(&bars[L::B_S + x]);
+        if (!PAIR || x == 1) tc5::commit(&bars[L::B_EK + sk]);
+        if (i == ops - 1) tc5::commit(&bars[L::B_EQ + q]);
+        return true;
+      };
+      if (!qk(0)) return;
+      if (ops > 1 && !qk(1)) return;
+      for (int i = 0; i < ops; ++i) {
+        const int x = i & 1, t = base + (PAIR ? i >> 1 : i), sv = t % NV;
+        if (!PAIR || x == 0) {
+          if (!KV8 && !wait_or_abort(&bars[L::B_V + sv], (t / NV) & 1, abort_flag, where)) return;
+          if (!wait_or_abort(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
+        }
+        if (!wait_or_abort(&bars[L::B_P + x], done[x] & 1, abort_flag, where)) return;
+        tc5::fence_after_sync();
+        const uint32_t pb = tmem + x * 128, ob = tmem + 256 + x * 128;
+        const uint64_t vb = v_desc + static_cast<uint64_t>((sv * L::TILE) >> 4);
+        const uint32_t acc0 = i >= 2 ? 1u : 0u;
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          tc5::mma_ts(ob, pb + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, k > 0 ? 1u : acc0);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            tc5::mma_ts(ob, pb + 64 + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, 1u);
+        }
+        tc5::commit(&bars[L::B_O + x]);
+        if (!PAIR || x == 1) tc5::commit(&bars[L::B_EV + sv]);
+        ++done[x];
+        if (i + 2 < ops && !qk(i + 2)) return;
+      }
+      base += s.n;
     }
-    const int pb = __ldg(a.block_tables + static_cast<int64_t>(b) * a.max_blocks_per_seq + j / a.BS);
-    if (pb < 0 || pb >= a.num_blocks) {
-      if (lane == 0) record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(b) * a.max_blocks_per_seq + j / a.BS);
-      continue;
+  };
+
+  // Warps 2 and 3 take half a V tile's rows each.
+  auto guard = [&]() {
+    const int rows0 = (warp - 2) * (BN / 2);
+    Seg s;
+    int it = 0;
+    for (int si = 0; walk.next(a, s); ++si) {
+      // a mark that no segment under way uses: the other warp is at most NV tiles
+      // ahead, and segments more than NV + 1 tiles ago have ended
+      if (warp == 2 && lane == 0) flags[(si + kFlagSlots / 2) % kFlagSlots] = 0;
+      for (int j = 0; j < s.n; ++j, ++it) {
+        const int kv0 = s.s.kv_start + (s.j0 + j) * BN;
+        const bool edge = edge_tile(a, s.s, kv0);
+        const int lo = s.s.kv_lo - kv0, hi = s.s.L - kv0;  // rows outside [lo, hi) are hidden from all
+        const int sv = it % NV;
+        bool found = false;
+        if constexpr (!KV8) {
+          if (!warp_wait(&bars[L::B_V + sv], (it / NV) & 1, abort_flag, where)) return;
+          if (edge) {
+            for (int i = lane; i < L::NREG * (BN / 2) * 8; i += 32) {
+              const int r = rows0 + (i / 8) % (BN / 2);
+              uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_V + sv * L::TILE +
+                                                   (i / (BN / 2 * 8)) * L::REG + r * 128) + i % 8;
+              const uint4 u = *p;
+              if (r < lo || r >= hi) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 m = make_uint4(not_finite<T>(u.x), not_finite<T>(u.y),
+                                           not_finite<T>(u.z), not_finite<T>(u.w));
+                if (m.x | m.y | m.z | m.w) {
+                  *p = make_uint4(u.x & ~m.x, u.y & ~m.y, u.z & ~m.z, u.w & ~m.w);
+                  found = true;
+                }
+              }
+            }
+            if (found) flags[si % kFlagSlots] = 1;
+            fence_proxy_async_smem();
+          }
+        } else {
+          // Lane (row r0, 16-channel group cc) widens 16 codes of a swizzled
+          // row into two 16-byte chunks of the swizzled fp16 tile; lanes of
+          // the upper half store them in the opposite order, so that the 8
+          // lanes of a row never meet in a bank group.
+          constexpr int LPR = D / 16, RPI = 32 / LPR;
+          const int cc = lane % LPR, r0 = lane / LPR;
+          const bool swap = cc >= LPR / 2;
+          const int s8 = it % L::N8V;
+          if (!warp_wait(&bars[L::B_V + s8], (it / L::N8V) & 1, abort_flag, where)) return;
+          if (it >= NV && !warp_wait(&bars[L::B_EV + sv], ((it / NV) - 1) & 1, abort_flag, where))
+            return;
+          const uint8_t *src = smem + L::OFF_V8 + s8 * L::TILE8;
+          uint8_t *dst = smem + L::OFF_V + sv * L::TILE + (cc / 4) * L::REG;
+          const int k0 = (2 * cc) % 8;
+#pragma unroll 8
+          for (int i = 0; i < BN / 2 / RPI; ++i) {
+            const int r = rows0 + RPI * i + r0;
+            const int chunk = D == 128 ? (cc ^ (r & 7)) : (cc ^ ((r >> 1) & 3));
+            uint4 u = *reinterpret_cast<const uint4 *>(src + r * D + chunk * 16);
+            if (edge) {
+              if (r < lo || r >= hi) u = make_uint4(0, 0, 0, 0);
+              // bytes whose low 7 bits are all set: NaN
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              uint32_t m[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t t = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                m[e] = (t >> 7) * 0xffu;
+                found |= t != 0;
+              }
+              u = make_uint4(u.x & ~m[0], u.y & ~m[1], u.z & ~m[2], u.w & ~m[3]);
+            }
+            const uint2 h0 = e4m3x4_to_h4(u.x), h1 = e4m3x4_to_h4(u.y);
+            const uint2 h2 = e4m3x4_to_h4(u.z), h3 = e4m3x4_to_h4(u.w);
+            const uint4 c0 = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            const uint4 c1 = make_uint4(h2.x, h2.y, h3.x, h3.y);
+            uint8_t *row = dst + r * 128;
+            uint4 *p0 = reinterpret_cast<uint4 *>(row + ((k0 ^ (r & 7)) * 16));
+            uint4 *p1 = reinterpret_cast<uint4 *>(row + (((k0 + 1) ^ (r & 7)) * 16));
+            *(swap ? p1 : p0) = swap ? c1 : c0;
+            *(swap ? p0 : p1) = swap ? c0 : c1;
+          }
+          if (found) flags[si % kFlagSlots] = 1;
+          fence_proxy_async_smem();
+          mbar_arrive(&bars[L::B_E8V + s8]);
+        }
+        mbar_arrive(&bars[L::B_VG + sv]);
+      }
     }
-    const int64_t at = (static_cast<int64_t>(pb) * a.BS + j % a.BS) * a.row_elems + g * D + lane * E;
-    float s = 0.f;
+  };
+
+  auto softmax = [&]() {
+    const int x = warp >= 8 ? 1 : 0;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sb = tmem + lane_base + x * 128;
+    const int node = node0 + (PAIR ? x * nodes_per_tile : 0) + r / a.QPK;
+    const bool row_ok = r < tile_rows;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::OFF_MASK) + x * 128 + r;  // word w: [(w + 1) * 256]
+    float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
+    float *q_exp = reinterpret_cast<float *>(smem + L::OFF_EXP);
+    constexpr int X = PAIR ? 2 : 1;
+    const bool rec = threadIdx.x == 128;
+    if (rec) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    // the row's query as E4M3 terms of q * 2^-e, for segment number si
+    auto queries = [&](const Seg &s, int si) -> bool {
+      if (si > 0 && !warp_wait(&bars[L::B_EQ], (si - 1) & 1, abort_flag, where)) return false;
+      uint4 v[D / 8];
+      const bool valid = row_ok && node < s.s.nodes;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * value(at + e);
+      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+      if (valid) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.query + (static_cast<int64_t>(s.s.row + node) * a.H + s.g * a.QPK + r % a.QPK) * D);
 #pragma unroll
-    for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s = s * a.scale_log2 + slope * static_cast<float>(pos - mine);
-    const float top = fmaxf(m, s);
-    const float up = m == -INFINITY ? 0.f : exp2f(m - top);
-    const float p = s == -INFINITY ? 0.f : exp2f(s - top);
-    m = top;
-    l = l * up + p;
+        for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
+      }
+      uint32_t top = 0;  // the largest finite |q|, as bits
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * up + p * value(at + e + a.num_blocks * a.BS * a.row_elems);
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = T::to_f2(word_of(v[i], k));
+          top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
+        }
+      // largest |q| 2^-e in [2^7, 2^8); queries below 2^-57 stay below that
+      const int e = max(static_cast<int>(top >> 23) - 134, -64);
+      const float mul = __int_as_float((127 - e) << 23);
+      uint8_t *dst = smem + L::OFF_Q + (PAIR ? x : 0) * L::TERMS * L::TILE8;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t w[L::TERMS][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 &u = v[2 * c + k / 2];
+          const float2 f0 = T::to_f2(word_of(u, 2 * (k % 2)));
+          const float2 f1 = T::to_f2(word_of(u, 2 * (k % 2) + 1));
+          float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul), scaled_query(f1.x, mul),
+                        scaled_query(f1.y, mul)};
+#pragma unroll
+          for (int t = 0; t < L::TERMS; t += 2) {
+            uint32_t lo;
+            split_e4m3x4(y[0], y[1], y[2], y[3], w[t][k], lo);
+            if (t + 1 < L::TERMS) w[t + 1][k] = lo;
+            if (t + 2 < L::TERMS) {
+              // what both terms leave over
+              const uint2 h = e4m3x4_to_h4(w[t][k]), g = e4m3x4_to_h4(lo);
+              const float2 ha = FP16::to_f2(h.x), hb = FP16::to_f2(h.y);
+              const float2 ga = FP16::to_f2(g.x), gb = FP16::to_f2(g.y);
+              y[0] = y[0] - ha.x - ga.x;
+              y[1] = y[1] - ha.y - ga.y;
+              y[2] = y[2] - hb.x - gb.x;
+              y[3] = y[3] - hb.y - gb.y;
+            }
+          }
+        }
+        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+#pragma unroll
+        for (int t = 0; t < L::TERMS; ++t)
+          *reinterpret_cast<uint4 *>(dst + t * L::TILE8 + off) =
+              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+      }
+      q_exp[((si & 1) * 2 + x) * 128 + r] = __int_as_float((127 + e) << 23);
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[L::B_Q + x]);
+      return true;
+    };
+
+    Seg s, ahead;
+    bool have = walk.next(a, s);
+    if (KV8 && have && (PAIR || x == 0) && !queries(s, 0)) return;
+    int last_b = -1, here = 0;
+    int used[2] = {0, 0};  // products per group before the segment
+    for (int si = 0; have; ++si) {
+      const bool more = walk.next(a, ahead);
+      if (s.b != last_b) {
+        // the node's ancestors, those inside the window: a bit each
+        last_b = s.b;
+#pragma unroll
+        for (int w = 0; w < kMaskWords + 2; ++w) mask[w * 256] = 0;
+        int depth = -1;
+        if (row_ok && node < s.s.nodes) {
+          for (int c = node; c >= 0;) {
+            ++depth;
+            if (a.window <= 0 || depth < a.window) mask[(c / 32 + 1) * 256] |= 1u << (c % 32);
+            int p = __ldg(a.tb.parents + s.s.row + c);
+            if (p < -1 || p >= c) {
+              record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(s.s.row) + c);
+              p = -1;
+            }
+            c = p;
+          }
+        }
+        here = s.s.ctx + max(depth, 0);
+      }
+      const bool valid = row_ok && node < s.s.nodes;
+      const bool busy = __any_sync(0xffffffffu, valid);
+      const int lo = a.window > 0 ? max(0, here - a.window + 1) : 0;
+      const int head = s.g * a.QPK + r % a.QPK;
+      float sl2 = a.scale_log2;
+      const float slope = a.alibi && row_ok ? __ldg(a.alibi + head) * kLog2e : 0.f;
+      const bool biased = a.alibi != nullptr;
+      // log2 units of a score and of the maximum: the scale is folded into the
+      // exponent's FMA, with ALiBi into the scores
+      float unit = biased ? 1.f : sl2;
+      float m = -INFINITY, l = 0.f;
+      const int n = PAIR ? s.n : (s.n + 1 - x) / 2;
+      for (int k = 0; k < n; ++k) {
+        if (!warp_wait(&bars[L::B_S + x], (used[x] + k) & 1, abort_flag, where)) return;
+        tc5::fence_after_sync();
+        if (KV8 && k == 0) {
+          // scores are there, so the queries' scale is: written by this thread, or by group A's
+          sl2 *= q_exp[((si & 1) * 2 + (PAIR ? x : 0)) * 128 + r];
+          unit = biased ? 1.f : sl2;
+        }
+        if (busy) {
+          uint32_t raw[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c)
+            tc5::tmem_ld32(sb + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * c));
+          tc5::tmem_ld_wait();
+          const int kv0 = s.s.kv_start + (s.j0 + (PAIR ? k : 2 * k + x)) * BN;
+          if (biased) {
+            const float b0 = slope * static_cast<float>(kv0 - here);
+#pragma unroll
+            for (int e = 0; e < BN; ++e)
+              raw[e] = __float_as_uint(fmaf(__uint_as_float(raw[e]), sl2,
+                                            fmaf(slope, static_cast<float>(e), b0)));
+          }
+          const bool full = !valid || (kv0 + BN <= s.s.ctx && kv0 >= lo);
+          if (__any_sync(0xffffffffu, !full)) {
+            const int off = kv0 - s.s.ctx;  // the node that stands at kv0
+            // nodes of the row's path behind the tile: each puts a step of depth
+            // between a key of the tile and the row
+            int behind = 0;
+            if (biased)
+              for (int w = 0; w < kMaskWords; ++w) {
+                const int z = off + BN - 32 * w;  // first bit behind the tile
+                const uint32_t b = mask[(w + 1) * 256];
+                behind += __popc(z <= 0 ? b : z >= 32 ? 0u : b >> z);
+              }
+#pragma unroll
+            for (int c = BN / 32 - 1; c >= 0; --c) {
+              const int p0 = kv0 + 32 * c, o = off + 32 * c;
+              // the row's visible context positions and path nodes among these 32 keys
+              const int from = max(lo - p0, 0), to = min(s.s.ctx - p0, 32);
+              uint32_t in_ctx = 0, in_tree = 0;
+              if (to > from) in_ctx = (to >= 32 ? ~0u : (1u << to) - 1u) & (~0u << from);
+              if (o > -32 && o < 32 * kMaskWords) {
+                const int w = (o + 32) / 32;  // one word of padding at each end
+                in_tree = __funnelshift_r(mask[w * 256], w <= kMaskWords ? mask[(w + 1) * 256] : 0u, o & 31);
+              }
+              if (biased && __any_sync(0xffffffffu, in_tree != 0)) {
+#pragma unroll
+                for (int e = 31; e >= 0; --e)
+                  if (in_tree >> e & 1) {
+                    // the key stands `behind` steps above the row, not at its place in the cache
+                    const float place = static_cast<float>(p0 + e - here);
+                    raw[32 * c + e] = __float_as_uint(__uint_as_float(raw[32 * c + e]) -
+                                                      slope * (place + static_cast<float>(behind)));
+                    ++behind;
+                  }
+              }
+              const uint32_t seen = in_ctx | in_tree;
+              if (__any_sync(0xffffffffu, seen != ~0u)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!(seen >> e & 1)) raw[32 * c + e] = __float_as_uint(-INFINITY);
+              }
+            }
+          }
+          // p = 2^(score - mu), written over the scores as one or two terms; returns the sum
+          auto exps = [&](float mu) -> float {
+            const float mul = biased ? 1.f : sl2;
+            const unsigned long long mul2 = f2pack(mul, mul), negmu2 = f2pack(-mu, -mu);
+            unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t hi[16], low[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x0, x1;
+                f2unpack(ffma2(f2pack(__uint_as_float(raw[32 * c + e]),
+                                      __uint_as_float(raw[32 * c + e + 1])),
+                               mul2, negmu2),
+                         x0, x1);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                ps2[(e / 2) & 3] = fadd2(ps2[(e / 2) & 3], f2pack(p0, p1));
+                hi[e / 2] = OPT::from_f2(p0, p1);
+                if constexpr (TWO) {
+                  const float2 h = OPT::to_f2(hi[e / 2]);
+                  low[e / 2] = OPT::from_f2(p0 - h.x, p1 - h.y);
+                }
+              }
+              tc5::tmem_st16(sb + 16 * c, hi);
+              if constexpr (TWO) tc5::tmem_st16(sb + 64 + 16 * c, low);
+            }
+            float s0, s1;
+            f2unpack(fadd2(fadd2(ps2[0], ps2[1]), fadd2(ps2[2], ps2[3])), s0, s1);
+            return s0 + s1;
+          };
+          // The reference moves lazily: exponents are taken against m as it
+          // stands; only where a row's sum is out of range (or m not set) is
+          // the maximum looked for and the pass repeated.
+          float alpha = 1.f, ps = 0.f;
+          bool moved = false, slow = valid && m == -INFINITY;
+          if (!__any_sync(0xffffffffu, slow)) {
+            ps = exps(m == -INFINITY ? 0.f : m * unit);
+            slow = valid && !(ps <= 32768.f);
+          }
+          if (__any_sync(0xffffffffu, slow)) {
+            float pm[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) pm[q] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < BN; e += 2)
+              pm[(e / 2) & 7] =
+                  fmax3(pm[(e / 2) & 7], __uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
+            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]),
+                                   fmaxf(pm[6], pm[7]));
+            if (m == -INFINITY) {
+              m = mx;
+            } else if ((mx - m) * unit > 8.f) {
+              alpha = fast_exp2((m - mx) * unit);
+              m = mx;
+              moved = valid;
+            }
+            tc5::tmem_st_wait();  // a first pass's weights are written before they are replaced
+            ps = exps(m == -INFINITY ? 0.f : m * unit);
+          }
+          l = l * alpha + ps;
+          if (__any_sync(0xffffffffu, moved)) {
+            // the accumulator holds the product before this one once that has completed
+            if (!warp_wait(&bars[L::B_O + x], (used[x] + k - 1) & 1, abort_flag, where)) return;
+            tc5::fence_after_sync();
+            const uint32_t ob = tmem + lane_base + 256 + x * 128;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc5::tmem_ld32(ob + 32 * c, o);
+              tc5::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc5::tmem_st32(ob + 32 * c, o);
+            }
+          }
+          tc5::tmem_st_wait();
+        }
+        // the other group has read this accumulator's last segment
+        if (!PAIR && k == 0 && si > 0 &&
+            !warp_wait(&bars[L::B_EPI], (si - 1) & 1, abort_flag, where))
+          return;
+        tc5::fence_before_sync();
+        mbar_arrive(&bars[L::B_P + x]);
+      }
+      // the next segment's queries, while this one's last products run
+      if (KV8 && more && (PAIR || x == 0) && !queries(ahead, si + 1)) return;
+
+      // ---- the segment's end ----
+      // f0, f1: what the two accumulators (PAIR: this group's own) are multiplied by
+      float f0 = 1.f, f1 = 0.f, top = m * unit;
+      used[0] += PAIR ? s.n : (s.n + 1) / 2;
+      used[1] += PAIR ? s.n : s.n / 2;
+      if constexpr (!PAIR) {
+        ml[x * 128 + r] = make_float2(top, l);
+        mbar_arrive(&bars[L::B_ML]);
+        if (!warp_wait(&bars[L::B_ML], si & 1, abort_flag, where)) return;
+        const float2 p = ml[r], q = ml[128 + r];
+        top = fmaxf(p.x, q.x);
+        f0 = p.x == -INFINITY ? 0.f : fast_exp2(p.x - top);
+        f1 = q.x == -INFINITY ? 0.f : fast_exp2(q.x - top);
+        l = f0 * p.y + f1 * q.y;
+        if (!warp_wait(&bars[L::B_O], (used[0] - 1) & 1, abort_flag, where)) return;
+        if (s.n > 1 && !warp_wait(&bars[L::B_O + 1], (used[1] - 1) & 1, abort_flag, where)) return;
+      } else {
+        if (!warp_wait(&bars[L::B_O + x], (used[x] - 1) & 1, abort_flag, where)) return;
+      }
+      tc5::fence_after_sync();
+      const bool whole = s.whole();
+      if (whole) {
+        const float inv = a.v_scale / l;  // l = 0: nothing but -infinity, NaN
+        f0 *= inv;
+        f1 *= inv;
+      }
+      const int at = (blockIdx.x * 2 + (s.j0 > 0 ? 0 : 1)) * X + (PAIR ? x : 0);
+      uint16_t *out = a.out + (static_cast<int64_t>(s.s.row + node) * a.H + head) * D;
+      float *part = a.part_o + (static_cast<int64_t>(at) * (D / 4) * BM + r) * 4;
+      constexpr int COLS = PAIR ? D : D / 2;  // each group stores its half of the row
+      const int col0 = PAIR ? 0 : x * COLS;
+      if (busy) {
+        const uint32_t ob = tmem + lane_base + 256 + (PAIR ? x * 128 : 0) + col0;
+#pragma unroll
+        for (int c = 0; c < COLS / 32; ++c) {
+          uint32_t o[32];
+          tc5::tmem_ld32(ob + 32 * c, o);
+          tc5::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+          if (!PAIR && s.n > 1) {
+            uint32_t o1[32];
+            tc5::tmem_ld32(ob + 128 + 32 * c, o1);
+            tc5::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+          }
+          if (valid && whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(out + col0 + 32 * c);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = T::from_f2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          } else if (valid) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<uint4 *>(part + static_cast<int64_t>((col0 + 32 * c) / 4 + q) * BM * 4) =
+                  make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+        if (!whole && (PAIR || x == 0) && valid)
+          a.part_ml[static_cast<int64_t>(at) * BM + r] = make_float2(top, l);
+        if (flags[si % kFlagSlots] && valid)
+          add_not_finite<T, D, KV8>(a, s, lo, col0, COLS, mask, whole ? out : nullptr, part);
+      }
+      if constexpr (!PAIR) {
+        tc5::fence_before_sync();
+        mbar_arrive(&bars[L::B_EPI]);
+      }
+      if (rec && s.j0 == 0 && !whole) {
+        // how many of the following CTAs the rest of the item goes to
+        const int64_t end = u1 - s.n + s.s.tiles;
+        int parts = 0;
+        while (slot + 1 + parts < shares && total * (slot + 1 + parts) / shares < end) ++parts;
+        a.record[blockIdx.x] = make_int4(s.b, s.g, parts, 0);
+      }
+      have = more;
+      s = ahead;
+    }
+    tc5::fence_before_sync();
+  };
+
+  if (warp == 0) {
+    producer();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      issuer();
+      // every product that was issued has completed before tensor memory is released
+      tc5::commit(&bars[L::B_FIN]);
+      mbar_wait_bounded(&bars[L::B_FIN], 0, where);
+    }
+  } else if (warp < 4) {
+    guard();
+  } else {
+    softmax();
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    part[warp][D] = m;
-    part[warp][D + 1] = l;
+  __syncwarp();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // copies in flight land before the CTA's memory goes away
+    auto drain = [&](int bar, int stages, int issued) {
+      for (int t = max(0, issued - stages); t < issued; ++t)
+        mbar_wait_bounded(&bars[bar + t % stages], (t / stages) & 1, where);
+    };
+    drain(L::B_K, NKT, misc[kIssuedK]);
+    drain(L::B_V, NVT, misc[kIssuedV]);
+    if (!KV8) drain(L::B_Q, L::NQ, misc[kIssuedQ]);
   }
   __syncthreads();
-  if (threadIdx.x < D) {
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
-    for (int w = 0; w < 4; ++w) {
-      if (part[w][D + 1] == 0.f) continue;
-      const float f = exp2f(part[w][D] - top);
-      sum += f * part[w][D + 1];
-      acc += f * part[w][threadIdx.x];
-    }
-    const float r = acc / sum * a.v_scale;
-    a.out[(static_cast<int64_t>(row + t) * a.H + h) * D + threadIdx.x] =
-        static_cast<uint16_t>(T::from_f2(r, 0.f));
+  if (warp == 1) {
+    tc5::fence_after_sync();
+    tc5::tmem_dealloc<512>(tmem);
   }
+}
+
+// ---------------------------------------------------------------------------
+// The parts of the items that were cut: block (CTA, row tile x 8 rows) merges
+// those of the item that the CTA's last segment begins, if it begins one: the
+// CTA's own second partial segment, then the first one of every following CTA.
+// Thread = (row, four channels).
+// ---------------------------------------------------------------------------
+template <class T, int D, bool PAIR>
+__global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
+  constexpr int X = PAIR ? 2 : 1;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int cta = blockIdx.x;
+  const int4 rec = a.record[cta];
+  if (rec.z <= 0) return;
+  const int x = blockIdx.y / (BM / 8), r = (blockIdx.y % (BM / 8)) * 8 + threadIdx.x % 8;
+  const int d4 = threadIdx.x / 8;
+  const int nodes_per_tile = BM / a.QPK;
+  const int node = ((cta % a.groups) * X + x) * nodes_per_tile + r / a.QPK;
+  Seq s;
+  bool bad;
+  if (r >= nodes_per_tile * a.QPK || !seq_of(a, rec.x, 0, s, bad) || node >= s.nodes) return;
+  auto place = [&](int i) -> int64_t {
+    return static_cast<int64_t>((cta + i * a.groups) * 2 + (i == 0 ? 1 : 0)) * X + x;
+  };
+  float top = -INFINITY;
+  for (int i = 0; i <= rec.z; ++i) top = fmaxf(top, a.part_ml[place(i) * BM + r].x);
+  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i <= rec.z; ++i) {
+    const float2 ml = a.part_ml[place(i) * BM + r];
+    const float4 p =
+        *reinterpret_cast<const float4 *>(a.part_o + ((place(i) * (D / 4) + d4) * BM + r) * 4);
+    const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+    l += w * ml.y;
+    // an infinite value stays what it is where its part's weight vanishes
+    o[0] += fabsf(p.x) < INFINITY ? w * p.x : p.x;
+    o[1] += fabsf(p.y) < INFINITY ? w * p.y : p.y;
+    o[2] += fabsf(p.z) < INFINITY ? w * p.z : p.z;
+    o[3] += fabsf(p.w) < INFINITY ? w * p.w : p.w;
+  }
+  const float inv = a.v_scale / l;
+  const int64_t row = static_cast<int64_t>(s.row + node) * a.H + rec.y * a.QPK + r % a.QPK;
+  *reinterpret_cast<uint2 *>(a.out + row * D + d4 * 4) =
+      make_uint2(T::from_f2(o[0] * inv, o[1] * inv), T::from_f2(o[2] * inv, o[3] * inv));
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+struct Plan {
+  bool pair;
+  int groups, ctas;
+  size_t part_o, part_ml, bytes;  // offsets behind the records, and the whole
+};
+
+static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g, int sms) {
+  Plan p;
+  const int per_tile = BM / g.QPK;
+  p.pair = max_nodes > per_tile;
+  const int per_group = (p.pair ? 2 : 1) * per_tile;
+  p.groups = (max_nodes + per_group - 1) / per_group;
+  int64_t keys = max_seq_len;
+  if (g.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(g.window) + max_nodes + BN);
+  const int64_t units = static_cast<int64_t>(num_seqs) * g.KVH * std::max<int64_t>(1, (keys + BN - 1) / BN);
+  const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units));
+  p.ctas = static_cast<int>(slots) * p.groups;
+  const size_t parts = static_cast<size_t>(p.ctas) * 2 * (p.pair ? 2 : 1) * BM;
+  p.part_ml = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
+  p.part_o = p.part_ml + parts * sizeof(float2);
+  p.bytes = p.part_o + parts * g.D * sizeof(float);
+  return p;
+}
+
+template <class T, int D, bool KV8, bool PAIR>
+static cudaError_t launch(const Args &a, const Plan &p, const CUtensorMap &qmap,
+                          const CUtensorMap &kvmap, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kern = tree_tc_kernel<T, D, KV8, PAIR>;
+  cudaError_t e = allow_shared_memory(kern, done, 0);
+  if (e != cudaSuccess) return e;
+  {
+    PdlLaunch cfg(dim3(p.ctas), kThreads, Lay<T, D, KV8, PAIR>::ALLOC, stream);
+    e = cudaLaunchKernelEx(&cfg.c, kern, a, qmap, kvmap);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.ctas == p.groups) return cudaSuccess;  // one CTA has all of a group's work: no parts
+  PdlLaunch cfg(dim3(p.ctas, (PAIR ? 2 : 1) * (BM / 8)), 8 * D / 4, 0, stream);
+  return cudaLaunchKernelEx(&cfg.c, combine_kernel<T, D, PAIR>, a);
 }
 
 }  // namespace tree
 
-size_t tree_workspace_bytes(int, int, int, const Geometry &, int) { return 0; }
+size_t tree_workspace_bytes(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g,
+                            int sms) {
+  return tree::plan(num_seqs, max_nodes, max_seq_len, g, sms).bytes;
+}
 
 cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
                                const void *kv_cache, const int32_t *block_tables,
                                int max_blocks_per_seq, const int32_t *seq_lens, int max_seq_len,
-                               const Geometry &g, void *, cudaStream_t stream) {
+                               const Geometry &g, void *workspace, cudaStream_t stream) {
+  DeviceInfo dev;
+  cudaError_t e = current_device_info(&dev);
+  if (e != cudaSuccess) return e;
+  const tree::Plan p = tree::plan(t.num_seqs, t.max_nodes, max_seq_len, g, dev.sms);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
   tree::Args a{};
   a.tb = t;
   a.out = static_cast<uint16_t *>(out);
@@ -154,22 +1128,61 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
   a.alibi = g.alibi;
+  a.record = reinterpret_cast<int4 *>(ws);
+  a.part_ml = reinterpret_cast<float2 *>(ws + p.part_ml);
+  a.part_o = reinterpret_cast<float *>(ws + p.part_o);
   a.num_blocks = g.num_blocks;
   a.row_elems = g.row_elems;
   a.max_blocks_per_seq = max_blocks_per_seq;
-  a.max_seq_len = max_seq_len;
+  a.max_seq_len = std::min(max_seq_len, 0x7fff0000);  // tiles' ends stay within 32 bits
   a.H = g.H;
+  a.KVH = g.KVH;
   a.QPK = g.QPK;
   a.BS = g.BS;
   a.window = g.window;
+  a.groups = p.groups;
   a.scale_log2 = g.scale * kLog2e * g.k_scale;
   a.v_scale = g.v_scale;
-  PdlLaunch cfg(dim3(g.H, t.max_nodes, t.num_seqs), 128, 0, stream);
-#define PKV_TREE(TT, DD)                                                                  \
-  if (g.D == DD)                                                                          \
-    return g.fp8 ? cudaLaunchKernelEx(&cfg.c, tree::simple_kernel<TT, DD, true>, a)       \
-                 : cudaLaunchKernelEx(&cfg.c, tree::simple_kernel<TT, DD, false>, a);
-  if (g.dtype == PKV_BF16) {
+  const bool bf = g.dtype == PKV_BF16;
+  const CUtensorMapDataType dt =
+      bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap qmap, kvmap;
+  {
+    // the rows of 128 / QPK nodes and one KV head's query heads, 64 channels
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.D), static_cast<cuuint64_t>(g.H),
+                                static_cast<cuuint64_t>(t.num_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.D) * 2,
+                                   static_cast<cuuint64_t>(g.H) * g.D * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g.QPK),
+                               static_cast<cuuint32_t>(tree::BM / g.QPK)};
+    if (encode_tensor_map(&qmap, dt, 3, const_cast<void *>(query), dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  {
+    // 16-bit: 64-channel swizzled boxes of a cache block's rows; 8-bit: its whole
+    // rows, swizzled by their length
+    const cuuint64_t eb = static_cast<cuuint64_t>(g.elem_bytes);
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(g.D), static_cast<cuuint64_t>(g.KVH),
+                                static_cast<cuuint64_t>(g.num_blocks * g.BS), 2};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(g.D) * eb,
+                                   static_cast<cuuint64_t>(g.row_elems) * eb,
+                                   static_cast<cuuint64_t>(g.num_blocks * g.block_elems) * eb};
+    const cuuint32_t box[4] = {g.fp8 ? static_cast<cuuint32_t>(g.D) : 64u, 1,
+                               static_cast<cuuint32_t>(g.BS), 1};
+    const CUtensorMapSwizzle swz = !g.fp8 || g.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                         : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (encode_tensor_map(&kvmap, g.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : dt, 4,
+                          const_cast<void *>(kv_cache), dims, strides, box, swz) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+#define PKV_TREE(TT, DD)                                                                     \
+  if (g.D == DD)                                                                             \
+    return g.fp8 ? (p.pair ? tree::launch<TT, DD, true, true>(a, p, qmap, kvmap, stream)     \
+                           : tree::launch<TT, DD, true, false>(a, p, qmap, kvmap, stream))   \
+                 : (p.pair ? tree::launch<TT, DD, false, true>(a, p, qmap, kvmap, stream)    \
+                           : tree::launch<TT, DD, false, false>(a, p, qmap, kvmap, stream));
+  if (bf) {
     PKV_TREE(BF16, 128) PKV_TREE(BF16, 64)
   } else {
     PKV_TREE(FP16, 128) PKV_TREE(FP16, 64)
