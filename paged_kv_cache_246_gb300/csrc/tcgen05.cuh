@@ -77,6 +77,15 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// True in one lane of the (converged) warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---- MMA -----------------------------------------------------------------
 // Shared-memory matrix descriptor, 128-byte swizzle (layout type 2), fixed
 // version field 0b01 at bits 46-47.  Addresses and offsets in bytes.

@@ -6,9 +6,9 @@
 //
 // Rows are (node, query head of the KV group) pairs, node by node, in tiles of
 // 128: 128 / QPK nodes each.  The step reads the context's K and V once per
-// KV head, so it is bound by HBM up to some 250 rows (2 flops per row and byte
-// against 281 of the card) and by the tensor core above; mma.sync tiles of 16
-// rows, as the other decodes use, would read K and V from L2 once per tile.
+// KV head, so up to a tile's rows it is bound by HBM (2 flops per row and byte
+// against 281 of the card); mma.sync tiles of 16 rows, as the other decodes
+// use, would read K and V from L2 once per tile.
 //
 // CTA = one per SM, persistent.  The work is the list of (sequence, KV head,
 // 128-key tile) units in this order; every CTA takes an equal, contiguous
@@ -17,29 +17,33 @@
 // segment that is a whole (sequence, KV head) writes the output; a part writes
 // its (o, m, l) in fp32, and combine_kernel merges the parts in order.  So all
 // SMs read the same amount whatever the lengths are, and every CTA has at most
-// two partial segments (its first and its last).  Trees that need more than two
-// row tiles are cut into groups; group i runs on the CTAs i, i + groups, ...,
-// which walk the same units at the same time, so that K and V come from L2 for
-// all groups but one.
+// two partial segments (its first and its last).  Trees of several row tiles
+// are that many groups; group i runs on the CTAs i, i + groups, ..., which walk
+// the same units at the same time, so that K and V come from L2 for all groups
+// but one.
 //
-// Roles of the 12 warps:
-//   warp 0      TMA producer: query rows of each segment, K and V tiles of 128
-//               keys, one box (block_size rows x 64 channels, 128-byte swizzle)
-//               per cache block; blocks out of the visible range are loaded
-//               from an out-of-range coordinate and arrive as zeros.
+// Roles of the 16 warps:
+//   warps 0, 2  TMA producers of K (and each segment's query rows) and of V: tiles
+//               of 128 keys, one box (block_size rows x 64 channels, 128-byte
+//               swizzle) per cache block; blocks out of the visible range are
+//               loaded from an out-of-range coordinate and arrive as zeros.  (One
+//               producer for both would hold the next K back until a V stage is
+//               free, a product later than its own.)
 //   warp 1      MMA issuer (one thread): S = Q K^T into one of two score
 //               buffers in tensor memory, O += P V with P read from there.
-//   warps 2, 3  look through the V tiles that some row sees only in part (the
+//   warps 4-7   look through the V tiles that some row sees only in part (the
 //               tree's, and the window's edge): rows hidden from all are
 //               zeroed, values that are not finite are zeroed and the segment
 //               is marked, since 0 * NaN in the product would reach rows that
 //               do not see them (the rows that do get them back at the end).
 //               Over an 8-bit cache they also widen the V codes to fp16.
-//   warps 4-7, 8-11  softmax groups A and B: thread r owns row r.
-// With one row tile (PAIR = false) A takes the even key tiles and B the odd
-// ones, each with its own running maximum, sum and accumulator, and the two are
-// merged at the segment's end; with more (PAIR) A and B take a row tile each.
-// Either way one group's softmax runs under the other's products.
+//   warps 8-11, 12-15  softmax groups A and B: thread r owns row r.
+// Of every key tile group A takes the first 64 keys and B the last, each with
+// its own running maximum, sum and accumulator; the two are merged at the
+// segment's end.  So a tile's softmax takes half as long as with a thread for
+// all 128 keys, no group waits for the other, and two score buffers fit beside
+// the two accumulators: the products of one tile run under the softmax of the
+// next.
 //
 // The weights enter P V as two 16-bit terms (hi + lo): a single rounded term
 // puts up to 2^-9 of a bf16 weight into the output, as much as the output's own
@@ -66,7 +70,8 @@ using tc5::AB;
 using tc5::wait_or_abort;
 using tc5::warp_wait;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kGuards = 4;  // warps that look through V
 constexpr int BM = 128, BN = 128;
 constexpr int kMaskWords = PKV_TREE_MAX_NODES / 32;
 
@@ -77,8 +82,8 @@ struct Args {
   const uint8_t *cache;
   const int32_t *block_tables, *seq_lens;
   const float *alibi;
-  float *part_o;     // [CTA][2][row tile][D / 4][128][4]
-  float2 *part_ml;   // [CTA][2][row tile][128]: maximum (log2 units), sum
+  float *part_o;     // [CTA][2][D / 4][128][4]
+  float2 *part_ml;   // [CTA][2][128]: maximum (log2 units), sum
   int4 *record;      // [CTA]: sequence, KV head, further CTAs of the item that its last segment begins
   int64_t num_blocks, row_elems;
   int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window, groups;
@@ -113,12 +118,19 @@ struct Seg {
   Seq s;
   int b, g, j0, n;  // tiles j0 .. j0 + n - 1 of KV head g
   __device__ __forceinline__ bool whole() const { return n == s.tiles; }
+  // Of the segment's tiles all rows see those from calm_from to before calm_to
+  // whole: in front of them lies the window's edge (a node of depth nodes - 1
+  // sees least), behind them the tree.
+  __device__ __forceinline__ int calm_from(const Args &a) const {
+    return a.window > 0 ? (max(0, s.ctx + s.nodes - a.window - s.kv_start) + BN - 1) / BN - j0 : 0;
+  }
+  __device__ __forceinline__ int calm_to() const { return (s.ctx - s.kv_start) / BN - j0; }
 };
 
 // A CTA's segments, in order: every role walks them by itself.
 struct Walk {
-  int b, node0;
-  int64_t off, left;  // units into sequence b; units to go
+  int b, g, j, node0;  // tile j of KV head g of sequence b
+  int64_t left;        // units to go
   bool known = false;
   Seq s;
   __device__ __forceinline__ bool next(const Args &a, Seg &o) {
@@ -133,15 +145,18 @@ struct Walk {
       }
       o.s = s;
       o.b = b;
-      o.g = static_cast<int>(off / s.tiles);
-      o.j0 = static_cast<int>(off - static_cast<int64_t>(o.g) * s.tiles);
-      o.n = static_cast<int>(min(static_cast<int64_t>(s.tiles - o.j0), left));
+      o.g = g;
+      o.j0 = j;
+      o.n = static_cast<int>(min(static_cast<int64_t>(s.tiles - j), left));
       left -= o.n;
-      off += o.n;
-      if (off == static_cast<int64_t>(s.tiles) * a.KVH) {
-        ++b;
-        off = 0;
-        known = false;
+      j += o.n;
+      if (j == s.tiles) {
+        j = 0;
+        if (++g == a.KVH) {
+          g = 0;
+          ++b;
+          known = false;
+        }
       }
       return true;
     }
@@ -149,52 +164,64 @@ struct Walk {
   }
 };
 
-// Whether some row sees the tile of keys from kv0 on only in part.
-__device__ __forceinline__ bool edge_tile(const Args &a, const Seq &s, int kv0) {
-  return kv0 + BN > s.ctx || (a.window > 0 && kv0 < s.ctx + s.nodes - a.window);
-}
-
 // ---------------------------------------------------------------------------
 // Shared memory
 // ---------------------------------------------------------------------------
-template <class T, int D, bool KV8, bool PAIR>
+template <class T, int D, bool KV8>
 struct Lay {
   static constexpr int REG = 128 * 128;  // a 64-channel region of 128 rows
   static constexpr int NREG = D / 64;
   static constexpr int TILE = REG * NREG;
   static constexpr int TILE8 = BN * D;
   static constexpr int TERMS = std::is_same_v<T, FP16> ? 3 : 2;  // E4M3 terms of a query
-  // the largest rings that fit
-  static constexpr bool TIGHT = KV8 && PAIR && TERMS == 3 && D == 128;
+  // rings, as large as fit
   static constexpr int NK = KV8 ? 0 : (D == 128 ? 2 : 4);
   static constexpr int NV = KV8 ? 2 : (D == 128 ? 2 : 4);
-  static constexpr int N8K = !KV8 ? 0 : TIGHT ? 2 : D == 128 ? 3 : 6;
-  static constexpr int N8V = !KV8 ? 0 : TIGHT ? 1 : D == 128 ? 2 : 4;
-  static constexpr int NQ = KV8 ? 1 : PAIR ? 1 : 2;  // query buffers (of one or two row tiles)
+  static constexpr int N8K = !KV8 ? 0 : D == 128 ? 3 : 6;
+  static constexpr int N8V = !KV8 ? 0 : D == 128 ? 2 : 4;
+  static constexpr int NQ = KV8 ? 1 : 2;  // query buffers
   static constexpr int OFF_Q = 0;
-  static constexpr int Q_BYTES = KV8 ? (PAIR ? 2 : 1) * TERMS * TILE8 : 2 * TILE;
+  static constexpr int Q_BYTES = KV8 ? TERMS * TILE8 : NQ * TILE;
   static constexpr int OFF_K = OFF_Q + Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_K8 = OFF_V + NV * TILE;
   static constexpr int OFF_V8 = OFF_K8 + N8K * TILE8;
   static constexpr int OFF_MASK = OFF_V8 + N8V * TILE8;  // [words + 2][256 threads]
   static constexpr int OFF_ML = OFF_MASK + (kMaskWords + 2) * 256 * 4;  // [2][128] float2
-  static constexpr int OFF_EXP = OFF_ML + 2 * 128 * 8;                  // [2][2][128] 2^e of the queries
-  static constexpr int OFF_BAR = OFF_EXP + 2 * 2 * 128 * 4;
-  // copies landed (K, V, Q), stages free again (EK, EV, EQ), V looked through
-  // (VG), V codes widened (E8V), scores ready (S), weights ready (P), product
-  // done (O), both groups' maxima written (ML), both accumulators read (EPI)
+  static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+  // copies landed (K, V, Q), stages free again (EK, EV, EQ; EV also: both
+  // products of that tile done), V looked through (VG), V codes widened (E8V),
+  // scores ready (S, per buffer), weights ready (P, per buffer), both
+  // groups' maxima written (ML), both accumulators read (EPI).
+  // A wait names a phase by its parity, so every waiter of a barrier sees each
+  // of its phases, or knows by another barrier that the one before has
+  // completed and that the one after cannot have.
   static constexpr int NKT = KV8 ? N8K : NK, NVT = KV8 ? N8V : NV;
   static constexpr int B_K = 0, B_EK = B_K + NKT, B_V = B_EK + NKT, B_VG = B_V + NVT,
-                       B_EV = B_VG + NV, B_E8V = B_EV + NV, B_Q = B_E8V + N8V, B_EQ = B_Q + 2,
-                       B_S = B_EQ + 2, B_P = B_S + 2, B_O = B_P + 2, B_ML = B_O + 2,
-                       B_EPI = B_ML + 1, B_FIN = B_EPI + 1, NBAR = B_FIN + 1;
+                       B_EV = B_VG + NV, B_E8V = B_EV + NV, B_Q = B_E8V + N8V, B_EQ = B_Q + NQ,
+                       B_S = B_EQ + NQ, B_P = B_S + 2, B_ML = B_P + 2, B_EPI = B_ML + 1,
+                       B_FIN = B_EPI + 1, NBAR = B_FIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 512;
   // one CTA owns an SM and its tensor memory
   static constexpr int ALLOC = std::max(BYTES + 1024, 118 * 1024);
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 };
+
+// One arrival for the warp, behind what its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Registers of this warpgroup's threads from here on: every warp of it calls.
+template <bool MORE, int N>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // Words of the MISC area.
 enum { kTmem = 0, kAbort = 1, kIssuedK = 2, kIssuedV = 3, kIssuedQ = 4, kStart = 6, kFlags = 16, kScan = 32 };
@@ -235,20 +262,20 @@ __device__ __noinline__ void add_not_finite(const Args &a, const Seg &seg, int l
         part[static_cast<int64_t>((c0 + d) / 4) * 512 + (c0 + d) % 4] += v;
     }
   };
-  for (int j = seg.j0; j < seg.j0 + seg.n; ++j) {
-    const int kv0 = seg.s.kv_start + j * BN;
-    if (!edge_tile(a, seg.s, kv0)) continue;
+  for (int j = 0; j < seg.n; ++j) {
+    if (j >= seg.calm_from(a) && j < seg.calm_to()) continue;
+    const int kv0 = seg.s.kv_start + (seg.j0 + j) * BN;
     for (int pos = max(kv0, lo); pos < min(kv0 + BN, seg.s.ctx); ++pos) key(pos);
     for (int c = max(0, kv0 - seg.s.ctx); c < min(seg.s.nodes, kv0 + BN - seg.s.ctx); ++c)
       if (mask[(c / 32 + 1) * 256] >> (c % 32) & 1) key(seg.s.ctx + c);
   }
 }
 
-template <class T, int D, bool KV8, bool PAIR>
+template <class T, int D, bool KV8>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
                const __grid_constant__ CUtensorMap kvmap) {
-  using L = Lay<T, D, KV8, PAIR>;
+  using L = Lay<T, D, KV8>;
   using OPT = std::conditional_t<KV8, FP16, T>;  // operand type of P V
   constexpr bool TWO = !KV8 || std::is_same_v<T, FP16>;  // weights in two terms
   constexpr int NV = L::NV, NKT = L::NKT, NVT = L::NVT;
@@ -260,23 +287,24 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
   volatile uint32_t *abort_flag = misc + kAbort;
   volatile uint32_t *flags = misc + kFlags;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp-uniform to the compiler too
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const int64_t where = blockIdx.x;
   const int nodes_per_tile = BM / a.QPK;
   const int tile_rows = nodes_per_tile * a.QPK;
   const int group = blockIdx.x % a.groups, slot = blockIdx.x / a.groups;
   const int slots = gridDim.x / a.groups;
-  const int node0 = group * (PAIR ? 2 : 1) * nodes_per_tile;
+  const int node0 = group * nodes_per_tile;
 
   // ---- before the kernel ahead has completed: nothing that it may write ----
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) {
       uint32_t count = 1;
-      if (i >= L::B_VG && i < L::B_VG + NV) count = 64;
-      if (KV8 && i >= L::B_E8V && i < L::B_E8V + L::N8V) count = 64;
-      if (KV8 && (i == L::B_Q || i == L::B_Q + 1)) count = 128;
-      if (i == L::B_P || i == L::B_P + 1) count = 128;
-      if (i == L::B_ML || i == L::B_EPI) count = 256;
+      if (i >= L::B_VG && i < L::B_VG + NV) count = kGuards;
+      if (KV8 && i >= L::B_E8V && i < L::B_E8V + L::N8V) count = kGuards;
+      if (KV8 && i == L::B_Q) count = 8;
+      if (i == L::B_P || i == L::B_P + 1 || i == L::B_ML || i == L::B_EPI) count = 8;
       mbar_init(&bars[i], count);
     }
     misc[kAbort] = 0;
@@ -366,12 +394,25 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     tc5::fence_after_sync();
     walk.node0 = node0;
     walk.left = u1 - u0;
-    walk.b = walk.left > 0 ? static_cast<int>(start[0]) : 0;
-    walk.off = walk.left > 0 ? start[1] : 0;
+    walk.b = walk.g = walk.j = 0;
+    if (walk.left > 0) {
+      walk.b = static_cast<int>(start[0]);
+      Seq s;
+      bool bad;
+      seq_of(a, walk.b, node0, s, bad);
+      walk.g = static_cast<int>(start[1] / s.tiles);
+      walk.j = static_cast<int>(start[1] - static_cast<int64_t>(walk.g) * s.tiles);
+    }
   }
-  const uint32_t tmem = misc[kTmem];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[kTmem], 0);
 
-  auto producer = [&]() {
+  // K and the queries (V = false), or V
+  auto producer = [&](auto is_v) {
+    constexpr bool V = decltype(is_v)::value;
+    constexpr int STAGES = V ? NVT : NKT, FULL = V ? L::B_V : L::B_K;
+    constexpr int EMPTY = !V ? L::B_EK : KV8 ? L::B_E8V : L::B_EV;
+    constexpr int BYTES = KV8 ? L::TILE8 : L::TILE;
+    constexpr int OFF = KV8 ? (V ? L::OFF_V8 : L::OFF_K8) : (V ? L::OFF_V : L::OFF_K);
     const int TB = BN / a.BS;
     // lane l < TB: where cache block l of the segment's key tile j lies, or an
     // out-of-range row (zeros) outside the visible range or for a bad entry
@@ -400,58 +441,38 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       for (int j = 0; j < s.n; ++j, ++it) {
         const int coord = next;
         next = j + 1 < s.n ? coord_of(s, j + 1) : more ? coord_of(ahead, 0) : 0;
-        const int sk = it % NKT, sv = it % NVT;
-        if (it >= NKT && !warp_wait(&bars[L::B_EK + sk], ((it / NKT) - 1) & 1, abort_flag, where))
+        const int st = it % STAGES;
+        if (it >= STAGES &&
+            !warp_wait(&bars[EMPTY + st], ((it / STAGES) - 1) & 1, abort_flag, where))
           return;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&bars[L::B_K + sk], KV8 ? L::TILE8 : L::TILE);
-          misc[kIssuedK] = it + 1;
+          mbar_arrive_expect_tx(&bars[FULL + st], BYTES);
+          misc[V ? kIssuedV : kIssuedK] = it + 1;
         }
         __syncwarp();
         if (lane < TB) {
           if constexpr (KV8) {
-            tma_load_4d(smem + L::OFF_K8 + sk * L::TILE8 + lane * a.BS * D, &kvmap,
-                        &bars[L::B_K + sk], 0, s.g, coord, 0);
+            tma_load_4d(smem + OFF + st * L::TILE8 + lane * a.BS * D, &kvmap, &bars[FULL + st], 0,
+                        s.g, coord, V);
           } else {
             for (int r = 0; r < L::NREG; ++r)
-              tma_load_4d(smem + L::OFF_K + sk * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
-                          &bars[L::B_K + sk], 64 * r, s.g, coord, 0);
+              tma_load_4d(smem + OFF + st * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
+                          &bars[FULL + st], 64 * r, s.g, coord, V);
           }
         }
-        if (!KV8 && j == 0) {
+        if (!KV8 && !V && j == 0) {
           const int q = si % L::NQ;
           if (si >= L::NQ &&
               !warp_wait(&bars[L::B_EQ + q], ((si / L::NQ) - 1) & 1, abort_flag, where))
             return;
           if (lane == 0) {
-            constexpr int X = PAIR ? 2 : 1;
-            mbar_arrive_expect_tx(&bars[L::B_Q + q], X * L::NREG * tile_rows * 128);
+            mbar_arrive_expect_tx(&bars[L::B_Q + q], L::NREG * tile_rows * 128);
             misc[kIssuedQ] = si + 1;
-            for (int x = 0; x < X; ++x)
-              for (int r = 0; r < L::NREG; ++r)
-                tc5::tma_load_3d(smem + L::OFF_Q + (q + x) * L::TILE + r * L::REG, &qmap,
-                                 &bars[L::B_Q + q], 64 * r, s.g * a.QPK,
-                                 s.s.row + node0 + x * nodes_per_tile);
+            for (int r = 0; r < L::NREG; ++r)
+              tc5::tma_load_3d(smem + L::OFF_Q + q * L::TILE + r * L::REG, &qmap, &bars[L::B_Q + q],
+                               64 * r, s.g * a.QPK, s.s.row + node0);
           }
           __syncwarp();
-        }
-        const int ev = KV8 ? L::B_E8V : L::B_EV;
-        if (it >= NVT && !warp_wait(&bars[ev + sv], ((it / NVT) - 1) & 1, abort_flag, where))
-          return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars[L::B_V + sv], KV8 ? L::TILE8 : L::TILE);
-          misc[kIssuedV] = it + 1;
-        }
-        __syncwarp();
-        if (lane < TB) {
-          if constexpr (KV8) {
-            tma_load_4d(smem + L::OFF_V8 + sv * L::TILE8 + lane * a.BS * D, &kvmap,
-                        &bars[L::B_V + sv], 0, s.g, coord, 1);
-          } else {
-            for (int r = 0; r < L::NREG; ++r)
-              tma_load_4d(smem + L::OFF_V + sv * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
-                          &bars[L::B_V + sv], 64 * r, s.g, coord, 1);
-          }
         }
       }
       have = more;
@@ -459,7 +480,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     }
   };
 
-  auto issuer = [&]() {
+  auto issuer = [&](const bool one) {
     constexpr uint32_t ID_QK = tc5::idesc_f16(KV8 ? 0 : AB<OPT>::v, 0, BM, BN);
     constexpr uint32_t ID_PV = tc5::idesc_f16(AB<OPT>::v, 1, BM, D);
     auto desc8 = [&](uint32_t off) -> uint64_t {
@@ -469,98 +490,120 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     const uint64_t q_desc = KV8 ? desc8(L::OFF_Q) : tc5::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t k_desc = KV8 ? desc8(L::OFF_K8) : tc5::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     const uint64_t v_desc = tc5::sdesc_sw128(sbase + L::OFF_V, L::REG, 1024);
-    Seg s;
-    int base = 0;           // key tiles before the segment
-    int done[2] = {0, 0};   // weight tiles consumed per group
-    for (int si = 0; walk.next(a, s); ++si) {
-      const int q = si % L::NQ;
-      if (!wait_or_abort(&bars[L::B_Q + q], (si / L::NQ) & 1, abort_flag, where)) return;
-      if (KV8 && PAIR && !wait_or_abort(&bars[L::B_Q + 1], si & 1, abort_flag, where)) return;
+    // Scores run two tiles ahead of the products with V, across segments over
+    // a 16-bit cache; over an 8-bit one a segment's queries are made when the
+    // last one's softmax has ended, and its scores begin then.  This thread
+    // feeds the tensor core, whose queue is short: it keeps little state and
+    // waits as seldom as it can.
+    Walk walk_q = walk;
+    int tq = 0, jq = 0, nq = 0, segs = 0;  // scores: next tile, its place in its segment of nq
+    auto scores = [&]() -> bool {
+      if (jq == nq) {
+        Seg s;
+        s.n = 0;
+        walk_q.next(a, s);
+        jq = 0;
+        nq = __shfl_sync(0xffffffffu, s.n, 0);
+        if (nq == 0) return true;  // no more
+        if (!warp_wait(&bars[L::B_Q + segs % L::NQ], (segs / L::NQ) & 1, abort_flag, where))
+          return false;
+        ++segs;
+      }
+      const int sk = tq % NKT;
+      if (!warp_wait(&bars[L::B_K + sk], (tq / NKT) & 1, abort_flag, where)) return false;
       tc5::fence_after_sync();
-      const int ops = PAIR ? 2 * s.n : s.n;
-      // op i: group i & 1, key tile i (i / 2 where the groups share it)
-      auto qk = [&](int i) -> bool {
-        const int x = i & 1, t = base + (PAIR ? i >> 1 : i), sk = t % NKT;
-        if (!PAIR || x == 0) {
-          if (!wait_or_abort(&bars[L::B_K + sk], (t / NKT) & 1, abort_flag, where)) return false;
-          tc5::fence_after_sync();
+      const uint32_t sb = tmem + (tq & 1) * 128;
+      if (one) {
+      if constexpr (KV8) {
+        const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE8) >> 4);
+#pragma unroll
+        for (int e = 0; e < L::TERMS; ++e)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            tc5::mma_ss_f8(sb, q_desc + static_cast<uint64_t>((e * L::TILE8 + k * 32) >> 4),
+                           kb + static_cast<uint64_t>(k * 2), ID_QK, (e | k) ? 1u : 0u);
+      } else {
+        const uint64_t qb = q_desc + static_cast<uint64_t>((((segs - 1) % L::NQ) * L::TILE) >> 4);
+        const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = static_cast<uint64_t>(((k / 4) * L::REG + (k % 4) * 32) >> 4);
+          tc5::mma_ss(sb, qb + off, kb + off, ID_QK, k > 0 ? 1u : 0u);
         }
-        const uint32_t sb = tmem + x * 128;
-        if constexpr (KV8) {
-          const uint64_t qb = q_desc + static_cast<uint64_t>(((PAIR ? x : 0) * L::TERMS * L::TILE8) >> 4);
-          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE8) >> 4);
+      }
+      tc5::commit(&bars[L::B_S + (tq & 1)]);
+      }
+      __syncwarp();
+      ++tq;
+      ++jq;
+      return true;
+    };
+    int t = 0;
+    bool first = true;
+    while (true) {
+      Seg s;
+      s.n = 0;
+      walk.next(a, s);
+      const int n = __shfl_sync(0xffffffffu, s.n, 0);
+      if (n == 0) return;
+      if (KV8 || first) {
+        if (!scores()) return;
+        if ((!KV8 || n > 1) && !scores()) return;
+        first = false;
+      }
+      for (int j = 0; j < n; ++j, ++t) {
+        const int sv = t % NV, buf = t & 1;
+        if (!warp_wait(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
+        if (!warp_wait(&bars[L::B_P + buf], (t / 2) & 1, abort_flag, where)) return;
+        tc5::fence_after_sync();
+        if (one) {
 #pragma unroll
-          for (int e = 0; e < L::TERMS; ++e)
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t pb = tmem + buf * 128 + x * 64, ob = tmem + 256 + x * 128;
+          // keys 64 x .. of the tile: 16 of them are 2048 bytes of V
+          const uint64_t vb = v_desc + static_cast<uint64_t>((sv * L::TILE + x * 64 * 128) >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              tc5::mma_ss_f8(sb, qb + static_cast<uint64_t>((e * L::TILE8 + k * 32) >> 4),
-                             kb + static_cast<uint64_t>(k * 2), ID_QK, (e | k) ? 1u : 0u);
-        } else {
-          const uint64_t qb = q_desc + static_cast<uint64_t>(((q + (PAIR ? x : 0)) * L::TILE) >> 4);
-          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE) >> 4);
+          for (int k = 0; k < 4; ++k)
+            tc5::mma_ts(ob, pb + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV,
+                        k > 0 || j > 0 ? 1u : 0u);
+          if constexpr (TWO) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = static_cast<uint64_t>(((k / 4) * L::REG + (k % 4) * 32) >> 4);
-            tc5::mma_ss(sb, qb + off, kb + off, ID_QK, k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              tc5::mma_ts(ob, pb + 32 + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, 1u);
           }
         }
-        tc5::commit(&bars[L::B_S + x]);
-        if (!PAIR || x == 1) tc5::commit(&bars[L::B_EK + sk]);
-        if (i == ops - 1) tc5::commit(&bars[L::B_EQ + q]);
-        return true;
-      };
-      if (!qk(0)) return;
-      if (ops > 1 && !qk(1)) return;
-      for (int i = 0; i < ops; ++i) {
-        const int x = i & 1, t = base + (PAIR ? i >> 1 : i), sv = t % NV;
-        if (!PAIR || x == 0) {
-          if (!KV8 && !wait_or_abort(&bars[L::B_V + sv], (t / NV) & 1, abort_flag, where)) return;
-          if (!wait_or_abort(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
+        tc5::commit(&bars[L::B_EV + sv]);
         }
-        if (!wait_or_abort(&bars[L::B_P + x], done[x] & 1, abort_flag, where)) return;
-        tc5::fence_after_sync();
-        const uint32_t pb = tmem + x * 128, ob = tmem + 256 + x * 128;
-        const uint64_t vb = v_desc + static_cast<uint64_t>((sv * L::TILE) >> 4);
-        const uint32_t acc0 = i >= 2 ? 1u : 0u;
-#pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          tc5::mma_ts(ob, pb + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, k > 0 ? 1u : acc0);
-        if constexpr (TWO) {
-#pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            tc5::mma_ts(ob, pb + 64 + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, 1u);
-        }
-        tc5::commit(&bars[L::B_O + x]);
-        if (!PAIR || x == 1) tc5::commit(&bars[L::B_EV + sv]);
-        ++done[x];
-        if (i + 2 < ops && !qk(i + 2)) return;
+        __syncwarp();
+        if ((!KV8 || j + 2 < n) && !scores()) return;
       }
-      base += s.n;
     }
   };
 
-  // Warps 2 and 3 take half a V tile's rows each.
+  // Each of these warps takes ROWS of a V tile's rows.
   auto guard = [&]() {
-    const int rows0 = (warp - 2) * (BN / 2);
+    constexpr int ROWS = BN / kGuards;
+    const int rows0 = (warp - 4) * ROWS;
     Seg s;
     int it = 0;
     for (int si = 0; walk.next(a, s); ++si) {
-      // a mark that no segment under way uses: the other warp is at most NV tiles
+      const int calm0 = s.calm_from(a), calm1 = s.calm_to();
+      // a mark that no segment under way uses: the other warps are at most NV tiles
       // ahead, and segments more than NV + 1 tiles ago have ended
-      if (warp == 2 && lane == 0) flags[(si + kFlagSlots / 2) % kFlagSlots] = 0;
+      if (warp == 4 && lane == 0) flags[(si + kFlagSlots / 2) % kFlagSlots] = 0;
       for (int j = 0; j < s.n; ++j, ++it) {
         const int kv0 = s.s.kv_start + (s.j0 + j) * BN;
-        const bool edge = edge_tile(a, s.s, kv0);
+        const bool edge = j < calm0 || j >= calm1;
         const int lo = s.s.kv_lo - kv0, hi = s.s.L - kv0;  // rows outside [lo, hi) are hidden from all
         const int sv = it % NV;
         bool found = false;
         if constexpr (!KV8) {
           if (!warp_wait(&bars[L::B_V + sv], (it / NV) & 1, abort_flag, where)) return;
           if (edge) {
-            for (int i = lane; i < L::NREG * (BN / 2) * 8; i += 32) {
-              const int r = rows0 + (i / 8) % (BN / 2);
+            for (int i = lane; i < L::NREG * ROWS * 8; i += 32) {
+              const int r = rows0 + (i / 8) % ROWS;
               uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_V + sv * L::TILE +
-                                                   (i / (BN / 2 * 8)) * L::REG + r * 128) + i % 8;
+                                                   (i / (ROWS * 8)) * L::REG + r * 128) + i % 8;
               const uint4 u = *p;
               if (r < lo || r >= hi) {
                 *p = make_uint4(0, 0, 0, 0);
@@ -591,8 +634,8 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           const uint8_t *src = smem + L::OFF_V8 + s8 * L::TILE8;
           uint8_t *dst = smem + L::OFF_V + sv * L::TILE + (cc / 4) * L::REG;
           const int k0 = (2 * cc) % 8;
-#pragma unroll 8
-          for (int i = 0; i < BN / 2 / RPI; ++i) {
+#pragma unroll 4
+          for (int i = 0; i < ROWS / RPI; ++i) {
             const int r = rows0 + RPI * i + r0;
             const int chunk = D == 128 ? (cc ^ (r & 7)) : (cc ^ ((r >> 1) & 3));
             uint4 u = *reinterpret_cast<const uint4 *>(src + r * D + chunk * 16);
@@ -621,77 +664,74 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           }
           if (found) flags[si % kFlagSlots] = 1;
           fence_proxy_async_smem();
-          mbar_arrive(&bars[L::B_E8V + s8]);
+          warp_arrive(&bars[L::B_E8V + s8]);
         }
-        mbar_arrive(&bars[L::B_VG + sv]);
+        warp_arrive(&bars[L::B_VG + sv]);
       }
     }
   };
 
   auto softmax = [&]() {
-    const int x = warp >= 8 ? 1 : 0;
+    constexpr int HN = BN / 2;            // keys of a tile that this group takes
+    const int x = warp >= 12 ? 1 : 0;     // the first ones or the last
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t sb = tmem + lane_base + x * 128;
-    const int node = node0 + (PAIR ? x * nodes_per_tile : 0) + r / a.QPK;
+    const int node = node0 + r / a.QPK;
     const bool row_ok = r < tile_rows;
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::OFF_MASK) + x * 128 + r;  // word w: [(w + 1) * 256]
     float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
-    float *q_exp = reinterpret_cast<float *>(smem + L::OFF_EXP);
-    constexpr int X = PAIR ? 2 : 1;
-    const bool rec = threadIdx.x == 128;
+    const bool rec = threadIdx.x == 256;
     if (rec) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-    // the row's query as E4M3 terms of q * 2^-e, for segment number si
-    auto queries = [&](const Seg &s, int si) -> bool {
+    // The row's query as E4M3 terms of q * 2^-e, for segment number si; each
+    // group makes half of the row.  Returns 2^e.
+    auto queries = [&](const Seg &s, int si, float &scale) -> bool {
       if (si > 0 && !warp_wait(&bars[L::B_EQ], (si - 1) & 1, abort_flag, where)) return false;
-      uint4 v[D / 8];
+      // Loops that are not unrolled: this runs once a segment, out of cold
+      // instruction memory.  The row is read twice rather than held.
       const bool valid = row_ok && node < s.s.nodes;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
-      if (valid) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.query + (static_cast<int64_t>(s.s.row + node) * a.H + s.g * a.QPK + r % a.QPK) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
-      }
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          a.query + (static_cast<int64_t>(s.s.row + node) * a.H + s.g * a.QPK + r % a.QPK) * D);
       uint32_t top = 0;  // the largest finite |q|, as bits
+#pragma unroll 1
+      for (int i = 0; valid && i < D / 8; i += 8) {
+        uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+        for (int k = 0; k < 8; ++k) v[k] = __ldg(src + i + k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = T::to_f2(word_of(v[i], k));
+        for (int k = 0; k < 32; ++k) {
+          const float2 f = T::to_f2(word_of(v[k / 4], k % 4));
           top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
         }
+      }
       // largest |q| 2^-e in [2^7, 2^8); queries below 2^-57 stay below that
       const int e = max(static_cast<int>(top >> 23) - 134, -64);
       const float mul = __int_as_float((127 - e) << 23);
-      uint8_t *dst = smem + L::OFF_Q + (PAIR ? x : 0) * L::TERMS * L::TILE8;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
+      scale = __int_as_float((127 + e) << 23);
+      uint8_t *dst = smem + L::OFF_Q;
+#pragma unroll 1
+      for (int c = x * (D / 32); c < (x + 1) * (D / 32); ++c) {  // 16 channels
+        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (valid) {
+          v[0] = __ldg(src + 2 * c);
+          v[1] = __ldg(src + 2 * c + 1);
+        }
         uint32_t w[L::TERMS][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 &u = v[2 * c + k / 2];
-          const float2 f0 = T::to_f2(word_of(u, 2 * (k % 2)));
-          const float2 f1 = T::to_f2(word_of(u, 2 * (k % 2) + 1));
-          float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul), scaled_query(f1.x, mul),
-                        scaled_query(f1.y, mul)};
-#pragma unroll
-          for (int t = 0; t < L::TERMS; t += 2) {
-            uint32_t lo;
-            split_e4m3x4(y[0], y[1], y[2], y[3], w[t][k], lo);
-            if (t + 1 < L::TERMS) w[t + 1][k] = lo;
-            if (t + 2 < L::TERMS) {
-              // what both terms leave over
-              const uint2 h = e4m3x4_to_h4(w[t][k]), g = e4m3x4_to_h4(lo);
-              const float2 ha = FP16::to_f2(h.x), hb = FP16::to_f2(h.y);
-              const float2 ga = FP16::to_f2(g.x), gb = FP16::to_f2(g.y);
-              y[0] = y[0] - ha.x - ga.x;
-              y[1] = y[1] - ha.y - ga.y;
-              y[2] = y[2] - hb.x - gb.x;
-              y[3] = y[3] - hb.y - gb.y;
-            }
+          const float2 f0 = T::to_f2(word_of(v[k / 2], 2 * (k % 2)));
+          const float2 f1 = T::to_f2(word_of(v[k / 2], 2 * (k % 2) + 1));
+          const float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul),
+                              scaled_query(f1.x, mul), scaled_query(f1.y, mul)};
+          split_e4m3x4(y[0], y[1], y[2], y[3], w[0][k], w[1][k]);
+          if constexpr (L::TERMS == 3) {
+            // what both terms leave over
+            const uint2 h0 = e4m3x4_to_h4(w[0][k]), h1 = e4m3x4_to_h4(w[1][k]);
+            const float2 ha = FP16::to_f2(h0.x), hb = FP16::to_f2(h0.y);
+            const float2 ga = FP16::to_f2(h1.x), gb = FP16::to_f2(h1.y);
+            uint32_t rest;
+            split_e4m3x4(y[0] - ha.x - ga.x, y[1] - ha.y - ga.y, y[2] - hb.x - gb.x,
+                         y[3] - hb.y - gb.y, w[2][k], rest);
           }
         }
         const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
@@ -700,87 +740,95 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           *reinterpret_cast<uint4 *>(dst + t * L::TILE8 + off) =
               make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
       }
-      q_exp[((si & 1) * 2 + x) * 128 + r] = __int_as_float((127 + e) << 23);
       fence_proxy_async_smem();
-      mbar_arrive(&bars[L::B_Q + x]);
+      warp_arrive(&bars[L::B_Q]);
       return true;
     };
 
-    Seg s, ahead;
-    bool have = walk.next(a, s);
-    if (KV8 && have && (PAIR || x == 0) && !queries(s, 0)) return;
-    int last_b = -1, here = 0;
-    int used[2] = {0, 0};  // products per group before the segment
-    for (int si = 0; have; ++si) {
-      const bool more = walk.next(a, ahead);
-      if (s.b != last_b) {
-        // the node's ancestors, those inside the window: a bit each
-        last_b = s.b;
-#pragma unroll
-        for (int w = 0; w < kMaskWords + 2; ++w) mask[w * 256] = 0;
-        int depth = -1;
-        if (row_ok && node < s.s.nodes) {
-          for (int c = node; c >= 0;) {
-            ++depth;
-            if (a.window <= 0 || depth < a.window) mask[(c / 32 + 1) * 256] |= 1u << (c % 32);
-            int p = __ldg(a.tb.parents + s.s.row + c);
-            if (p < -1 || p >= c) {
-              record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(s.s.row) + c);
-              p = -1;
-            }
-            c = p;
+    int here = 0;  // the node's position
+    // The node's ancestors, those inside the window: a bit each.
+    auto look_up = [&](const Seg &s) {
+#pragma unroll 1
+      for (int w = 0; w < kMaskWords + 2; ++w) mask[w * 256] = 0;
+      int depth = -1;
+      if (row_ok && node < s.s.nodes) {
+        for (int c = node; c >= 0;) {
+          ++depth;
+          if (a.window <= 0 || depth < a.window) mask[(c / 32 + 1) * 256] |= 1u << (c % 32);
+          int p = __ldg(a.tb.parents + s.s.row + c);
+          if (p < -1 || p >= c) {
+            record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(s.s.row) + c);
+            p = -1;
           }
+          c = p;
         }
-        here = s.s.ctx + max(depth, 0);
       }
+      here = s.s.ctx + max(depth, 0);
+    };
+
+    const bool biased = a.alibi != nullptr;
+    Seg s, ahead;
+    float q_scale = 1.f;
+    bool have = walk.next(a, s), more = false;
+    if (KV8 && have && !queries(s, 0, q_scale)) return;
+    int last_b = -1;
+    int base = 0;  // key tiles before the segment
+    for (int si = 0; have; ++si) {
       const bool valid = row_ok && node < s.s.nodes;
       const bool busy = __any_sync(0xffffffffu, valid);
+      // a new sequence's path: behind the first tile's work where that can do without
+      const bool fresh = s.b != last_b;
+      const bool later = fresh && a.window <= 0 && !biased && s.s.kv_start + (s.j0 + 1) * BN <= s.s.ctx;
+      if (fresh && !later) look_up(s);
+      last_b = s.b;
       const int lo = a.window > 0 ? max(0, here - a.window + 1) : 0;
       const int head = s.g * a.QPK + r % a.QPK;
-      float sl2 = a.scale_log2;
-      const float slope = a.alibi && row_ok ? __ldg(a.alibi + head) * kLog2e : 0.f;
-      const bool biased = a.alibi != nullptr;
+      const float sl2 = KV8 ? a.scale_log2 * q_scale : a.scale_log2;
+      const float slope = biased && row_ok ? __ldg(a.alibi + head) * kLog2e : 0.f;
       // log2 units of a score and of the maximum: the scale is folded into the
       // exponent's FMA, with ALiBi into the scores
-      float unit = biased ? 1.f : sl2;
+      const float unit = biased ? 1.f : sl2;
       float m = -INFINITY, l = 0.f;
-      const int n = PAIR ? s.n : (s.n + 1 - x) / 2;
-      for (int k = 0; k < n; ++k) {
-        if (!warp_wait(&bars[L::B_S + x], (used[x] + k) & 1, abort_flag, where)) return;
-        tc5::fence_after_sync();
-        if (KV8 && k == 0) {
-          // scores are there, so the queries' scale is: written by this thread, or by group A's
-          sl2 *= q_exp[((si & 1) * 2 + (PAIR ? x : 0)) * 128 + r];
-          unit = biased ? 1.f : sl2;
+      for (int k = 0; k < s.n; ++k) {
+        const int t = base + k, buf = t & 1;
+        const uint32_t sb = tmem + lane_base + buf * 128 + x * HN;
+        if (!warp_wait(&bars[L::B_S + buf], (t / 2) & 1, abort_flag, where)) return;
+        if (rec) {
+          // the scores are there: their keys are read, after the last ones the queries.
+          // (As commits of the issuing thread these would hold the tensor core's queue.)
+          mbar_arrive(&bars[L::B_EK + t % NKT]);
+          if (k == s.n - 1) mbar_arrive(&bars[L::B_EQ + si % L::NQ]);
         }
+        __syncwarp();
+        tc5::fence_after_sync();
         if (busy) {
-          uint32_t raw[BN];
+          uint32_t raw[HN];
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
+          for (int c = 0; c < HN / 32; ++c)
             tc5::tmem_ld32(sb + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * c));
           tc5::tmem_ld_wait();
-          const int kv0 = s.s.kv_start + (s.j0 + (PAIR ? k : 2 * k + x)) * BN;
+          const int kv0 = s.s.kv_start + (s.j0 + k) * BN + x * HN;
           if (biased) {
             const float b0 = slope * static_cast<float>(kv0 - here);
 #pragma unroll
-            for (int e = 0; e < BN; ++e)
+            for (int e = 0; e < HN; ++e)
               raw[e] = __float_as_uint(fmaf(__uint_as_float(raw[e]), sl2,
                                             fmaf(slope, static_cast<float>(e), b0)));
           }
-          const bool full = !valid || (kv0 + BN <= s.s.ctx && kv0 >= lo);
+          const bool full = !valid || (kv0 + HN <= s.s.ctx && kv0 >= lo);
           if (__any_sync(0xffffffffu, !full)) {
             const int off = kv0 - s.s.ctx;  // the node that stands at kv0
-            // nodes of the row's path behind the tile: each puts a step of depth
-            // between a key of the tile and the row
+            // nodes of the row's path behind these keys: each puts a step of depth
+            // between a key and the row
             int behind = 0;
             if (biased)
               for (int w = 0; w < kMaskWords; ++w) {
-                const int z = off + BN - 32 * w;  // first bit behind the tile
+                const int z = off + HN - 32 * w;  // first bit behind
                 const uint32_t b = mask[(w + 1) * 256];
                 behind += __popc(z <= 0 ? b : z >= 32 ? 0u : b >> z);
               }
 #pragma unroll
-            for (int c = BN / 32 - 1; c >= 0; --c) {
+            for (int c = HN / 32 - 1; c >= 0; --c) {
               const int p0 = kv0 + 32 * c, o = off + 32 * c;
               // the row's visible context positions and path nodes among these 32 keys
               const int from = max(lo - p0, 0), to = min(s.s.ctx - p0, 32);
@@ -788,7 +836,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
               if (to > from) in_ctx = (to >= 32 ? ~0u : (1u << to) - 1u) & (~0u << from);
               if (o > -32 && o < 32 * kMaskWords) {
                 const int w = (o + 32) / 32;  // one word of padding at each end
-                in_tree = __funnelshift_r(mask[w * 256], w <= kMaskWords ? mask[(w + 1) * 256] : 0u, o & 31);
+                in_tree = __funnelshift_r(mask[w * 256], mask[(w + 1) * 256], o & 31);
               }
               if (biased && __any_sync(0xffffffffu, in_tree != 0)) {
 #pragma unroll
@@ -815,7 +863,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
             const unsigned long long mul2 = f2pack(mul, mul), negmu2 = f2pack(-mu, -mu);
             unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = 0; c < HN / 32; ++c) {
               uint32_t hi[16], low[16];
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -833,7 +881,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
                 }
               }
               tc5::tmem_st16(sb + 16 * c, hi);
-              if constexpr (TWO) tc5::tmem_st16(sb + 64 + 16 * c, low);
+              if constexpr (TWO) tc5::tmem_st16(sb + HN / 2 + 16 * c, low);
             }
             float s0, s1;
             f2unpack(fadd2(fadd2(ps2[0], ps2[1]), fadd2(ps2[2], ps2[3])), s0, s1);
@@ -843,21 +891,21 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           // stands; only where a row's sum is out of range (or m not set) is
           // the maximum looked for and the pass repeated.
           float alpha = 1.f, ps = 0.f;
-          bool moved = false, slow = valid && m == -INFINITY;
-          if (!__any_sync(0xffffffffu, slow)) {
+          bool moved = false;
+          bool look = __any_sync(0xffffffffu, valid && m == -INFINITY);
+          if (!look) {
             ps = exps(m == -INFINITY ? 0.f : m * unit);
-            slow = valid && !(ps <= 32768.f);
+            look = __any_sync(0xffffffffu, valid && !(ps <= 32768.f));
           }
-          if (__any_sync(0xffffffffu, slow)) {
-            float pm[8];
+          if (look) {
+            float pm[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) pm[q] = -INFINITY;
+            for (int q = 0; q < 4; ++q) pm[q] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < BN; e += 2)
-              pm[(e / 2) & 7] =
-                  fmax3(pm[(e / 2) & 7], __uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
-            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]),
-                                   fmaxf(pm[6], pm[7]));
+            for (int e = 0; e < HN; e += 2)
+              pm[(e / 2) & 3] =
+                  fmax3(pm[(e / 2) & 3], __uint_as_float(raw[e]), __uint_as_float(raw[e + 1]));
+            const float mx = fmax3(pm[0], pm[1], fmaxf(pm[2], pm[3]));
             if (m == -INFINITY) {
               m = mx;
             } else if ((mx - m) * unit > 8.f) {
@@ -871,10 +919,12 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           l = l * alpha + ps;
           if (__any_sync(0xffffffffu, moved)) {
             // the accumulator holds the product before this one once that has completed
-            if (!warp_wait(&bars[L::B_O + x], (used[x] + k - 1) & 1, abort_flag, where)) return;
+            // (the one before that has: these scores came after it)
+            if (!warp_wait(&bars[L::B_EV + (t - 1) % NV], ((t - 1) / NV) & 1, abort_flag, where))
+              return;
             tc5::fence_after_sync();
             const uint32_t ob = tmem + lane_base + 256 + x * 128;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tc5::tmem_ld32(ob + 32 * c, o);
@@ -887,34 +937,32 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           tc5::tmem_st_wait();
         }
         // the other group has read this accumulator's last segment
-        if (!PAIR && k == 0 && si > 0 &&
-            !warp_wait(&bars[L::B_EPI], (si - 1) & 1, abort_flag, where))
+        if (k == 0 && si > 0 && !warp_wait(&bars[L::B_EPI], (si - 1) & 1, abort_flag, where))
           return;
         tc5::fence_before_sync();
-        mbar_arrive(&bars[L::B_P + x]);
+        warp_arrive(&bars[L::B_P + buf]);
+        if (k == 0) {
+          if (later) look_up(s);
+          more = walk.next(a, ahead);
+        }
       }
+      base += s.n;
       // the next segment's queries, while this one's last products run
-      if (KV8 && more && (PAIR || x == 0) && !queries(ahead, si + 1)) return;
+      if (KV8 && more && !queries(ahead, si + 1, q_scale)) return;
 
       // ---- the segment's end ----
-      // f0, f1: what the two accumulators (PAIR: this group's own) are multiplied by
-      float f0 = 1.f, f1 = 0.f, top = m * unit;
-      used[0] += PAIR ? s.n : (s.n + 1) / 2;
-      used[1] += PAIR ? s.n : s.n / 2;
-      if constexpr (!PAIR) {
-        ml[x * 128 + r] = make_float2(top, l);
-        mbar_arrive(&bars[L::B_ML]);
-        if (!warp_wait(&bars[L::B_ML], si & 1, abort_flag, where)) return;
-        const float2 p = ml[r], q = ml[128 + r];
-        top = fmaxf(p.x, q.x);
-        f0 = p.x == -INFINITY ? 0.f : fast_exp2(p.x - top);
-        f1 = q.x == -INFINITY ? 0.f : fast_exp2(q.x - top);
-        l = f0 * p.y + f1 * q.y;
-        if (!warp_wait(&bars[L::B_O], (used[0] - 1) & 1, abort_flag, where)) return;
-        if (s.n > 1 && !warp_wait(&bars[L::B_O + 1], (used[1] - 1) & 1, abort_flag, where)) return;
-      } else {
-        if (!warp_wait(&bars[L::B_O + x], (used[x] - 1) & 1, abort_flag, where)) return;
-      }
+      float top = m * unit;
+      ml[x * 128 + r] = make_float2(top, l);
+      warp_arrive(&bars[L::B_ML]);
+      if (!warp_wait(&bars[L::B_ML], si & 1, abort_flag, where)) return;
+      const float2 first = ml[r], last = ml[128 + r];
+      top = fmaxf(first.x, last.x);
+      // what the two accumulators are multiplied by
+      float f0 = first.x == -INFINITY ? 0.f : fast_exp2(first.x - top);
+      float f1 = last.x == -INFINITY ? 0.f : fast_exp2(last.x - top);
+      l = f0 * first.y + f1 * last.y;
+      if (!warp_wait(&bars[L::B_EV + (base - 1) % NV], ((base - 1) / NV) & 1, abort_flag, where))
+        return;
       tc5::fence_after_sync();
       const bool whole = s.whole();
       if (whole) {
@@ -922,28 +970,22 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         f0 *= inv;
         f1 *= inv;
       }
-      const int at = (blockIdx.x * 2 + (s.j0 > 0 ? 0 : 1)) * X + (PAIR ? x : 0);
+      const int at = blockIdx.x * 2 + (s.j0 > 0 ? 0 : 1);
       uint16_t *out = a.out + (static_cast<int64_t>(s.s.row + node) * a.H + head) * D;
       float *part = a.part_o + (static_cast<int64_t>(at) * (D / 4) * BM + r) * 4;
-      constexpr int COLS = PAIR ? D : D / 2;  // each group stores its half of the row
-      const int col0 = PAIR ? 0 : x * COLS;
+      constexpr int COLS = D / 2;  // each group stores its half of the row
+      const int col0 = x * COLS;
       if (busy) {
-        const uint32_t ob = tmem + lane_base + 256 + (PAIR ? x * 128 : 0) + col0;
-#pragma unroll
+        const uint32_t ob = tmem + lane_base + 256 + col0;
+#pragma unroll 1
         for (int c = 0; c < COLS / 32; ++c) {
-          uint32_t o[32];
+          uint32_t o[32], o1[32];
           tc5::tmem_ld32(ob + 32 * c, o);
+          tc5::tmem_ld32(ob + 128 + 32 * c, o1);
           tc5::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-          if (!PAIR && s.n > 1) {
-            uint32_t o1[32];
-            tc5::tmem_ld32(ob + 128 + 32 * c, o1);
-            tc5::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
-          }
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
           if (valid && whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(out + col0 + 32 * c);
             uint32_t w[16];
@@ -960,15 +1002,13 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
                   make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
-        if (!whole && (PAIR || x == 0) && valid)
+        if (!whole && x == 0 && valid)
           a.part_ml[static_cast<int64_t>(at) * BM + r] = make_float2(top, l);
         if (flags[si % kFlagSlots] && valid)
           add_not_finite<T, D, KV8>(a, s, lo, col0, COLS, mask, whole ? out : nullptr, part);
       }
-      if constexpr (!PAIR) {
-        tc5::fence_before_sync();
-        mbar_arrive(&bars[L::B_EPI]);
-      }
+      tc5::fence_before_sync();
+      warp_arrive(&bars[L::B_EPI]);
       if (rec && s.j0 == 0 && !whole) {
         // how many of the following CTAs the rest of the item goes to
         const int64_t end = u1 - s.n + s.s.tiles;
@@ -982,19 +1022,30 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     tc5::fence_before_sync();
   };
 
-  if (warp == 0) {
-    producer();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      issuer();
-      // every product that was issued has completed before tensor memory is released
-      tc5::commit(&bars[L::B_FIN]);
-      mbar_wait_bounded(&bars[L::B_FIN], 0, where);
-    }
-  } else if (warp < 4) {
+  // The four warpgroups' registers: 512 for a thread of each, as at the launch
+  // (4 x 128), but where they are needed.
+  if (warp >= 8) {
+    set_registers<true, 168>();
+    softmax();
+  } else if (warp >= 4) {
+    set_registers<false, 104>();
     guard();
   } else {
-    softmax();
+    set_registers<false, 72>();
+    if (warp == 0) {
+      producer(std::false_type{});
+    } else if (warp == 2) {
+      producer(std::true_type{});
+    } else if (warp == 1) {
+      const bool one = tc5::elect_one();
+      issuer(one);
+      __syncwarp();
+      // every product that was issued has completed before tensor memory is released
+      if (one) {
+        tc5::commit(&bars[L::B_FIN]);
+        mbar_wait_bounded(&bars[L::B_FIN], 0, where);
+      }
+    }
   }
   __syncwarp();
   __syncthreads();
@@ -1016,28 +1067,27 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 }
 
 // ---------------------------------------------------------------------------
-// The parts of the items that were cut: block (CTA, row tile x 8 rows) merges
+// The parts of the items that were cut: block (CTA, 8 rows) merges
 // those of the item that the CTA's last segment begins, if it begins one: the
 // CTA's own second partial segment, then the first one of every following CTA.
 // Thread = (row, four channels).
 // ---------------------------------------------------------------------------
-template <class T, int D, bool PAIR>
+template <class T, int D>
 __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
-  constexpr int X = PAIR ? 2 : 1;
   grid_dependency_wait();
   grid_launch_dependents();
   const int cta = blockIdx.x;
   const int4 rec = a.record[cta];
   if (rec.z <= 0) return;
-  const int x = blockIdx.y / (BM / 8), r = (blockIdx.y % (BM / 8)) * 8 + threadIdx.x % 8;
+  const int r = blockIdx.y * 8 + threadIdx.x % 8;
   const int d4 = threadIdx.x / 8;
   const int nodes_per_tile = BM / a.QPK;
-  const int node = ((cta % a.groups) * X + x) * nodes_per_tile + r / a.QPK;
+  const int node = cta % a.groups * nodes_per_tile + r / a.QPK;
   Seq s;
   bool bad;
   if (r >= nodes_per_tile * a.QPK || !seq_of(a, rec.x, 0, s, bad) || node >= s.nodes) return;
   auto place = [&](int i) -> int64_t {
-    return static_cast<int64_t>((cta + i * a.groups) * 2 + (i == 0 ? 1 : 0)) * X + x;
+    return static_cast<int64_t>(cta + i * a.groups) * 2 + (i == 0 ? 1 : 0);
   };
   float top = -INFINITY;
   for (int i = 0; i <= rec.z; ++i) top = fmaxf(top, a.part_ml[place(i) * BM + r].x);
@@ -1064,7 +1114,6 @@ __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
 // Host
 // ---------------------------------------------------------------------------
 struct Plan {
-  bool pair;
   int groups, ctas;
   size_t part_o, part_ml, bytes;  // offsets behind the records, and the whole
 };
@@ -1072,36 +1121,34 @@ struct Plan {
 static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g, int sms) {
   Plan p;
   const int per_tile = BM / g.QPK;
-  p.pair = max_nodes > per_tile;
-  const int per_group = (p.pair ? 2 : 1) * per_tile;
-  p.groups = (max_nodes + per_group - 1) / per_group;
+  p.groups = (max_nodes + per_tile - 1) / per_tile;
   int64_t keys = max_seq_len;
   if (g.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(g.window) + max_nodes + BN);
   const int64_t units = static_cast<int64_t>(num_seqs) * g.KVH * std::max<int64_t>(1, (keys + BN - 1) / BN);
   const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units));
   p.ctas = static_cast<int>(slots) * p.groups;
-  const size_t parts = static_cast<size_t>(p.ctas) * 2 * (p.pair ? 2 : 1) * BM;
+  const size_t parts = static_cast<size_t>(p.ctas) * 2 * BM;
   p.part_ml = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
   p.part_o = p.part_ml + parts * sizeof(float2);
   p.bytes = p.part_o + parts * g.D * sizeof(float);
   return p;
 }
 
-template <class T, int D, bool KV8, bool PAIR>
+template <class T, int D, bool KV8>
 static cudaError_t launch(const Args &a, const Plan &p, const CUtensorMap &qmap,
                           const CUtensorMap &kvmap, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto kern = tree_tc_kernel<T, D, KV8, PAIR>;
+  auto kern = tree_tc_kernel<T, D, KV8>;
   cudaError_t e = allow_shared_memory(kern, done, 0);
   if (e != cudaSuccess) return e;
   {
-    PdlLaunch cfg(dim3(p.ctas), kThreads, Lay<T, D, KV8, PAIR>::ALLOC, stream);
+    PdlLaunch cfg(dim3(p.ctas), kThreads, Lay<T, D, KV8>::ALLOC, stream);
     e = cudaLaunchKernelEx(&cfg.c, kern, a, qmap, kvmap);
     if (e != cudaSuccess) return e;
   }
   if (p.ctas == p.groups) return cudaSuccess;  // one CTA has all of a group's work: no parts
-  PdlLaunch cfg(dim3(p.ctas, (PAIR ? 2 : 1) * (BM / 8)), 8 * D / 4, 0, stream);
-  return cudaLaunchKernelEx(&cfg.c, combine_kernel<T, D, PAIR>, a);
+  PdlLaunch cfg(dim3(p.ctas, BM / 8), 8 * D / 4, 0, stream);
+  return cudaLaunchKernelEx(&cfg.c, combine_kernel<T, D>, a);
 }
 
 }  // namespace tree
@@ -1176,12 +1223,10 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
                           const_cast<void *>(kv_cache), dims, strides, box, swz) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-#define PKV_TREE(TT, DD)                                                                     \
-  if (g.D == DD)                                                                             \
-    return g.fp8 ? (p.pair ? tree::launch<TT, DD, true, true>(a, p, qmap, kvmap, stream)     \
-                           : tree::launch<TT, DD, true, false>(a, p, qmap, kvmap, stream))   \
-                 : (p.pair ? tree::launch<TT, DD, false, true>(a, p, qmap, kvmap, stream)    \
-                           : tree::launch<TT, DD, false, false>(a, p, qmap, kvmap, stream));
+#define PKV_TREE(TT, DD)                                                   \
+  if (g.D == DD)                                                           \
+    return g.fp8 ? tree::launch<TT, DD, true>(a, p, qmap, kvmap, stream)   \
+                 : tree::launch<TT, DD, false>(a, p, qmap, kvmap, stream);
   if (bf) {
     PKV_TREE(BF16, 128) PKV_TREE(BF16, 64)
   } else {
