@@ -157,6 +157,10 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 // A bounded wait of a CTA whose roles stop together: false when it ran out
 // (PKV_ERR_TIMEOUT recorded, the abort flag raised) or another role raised the
 // flag.
+static __device__ __noinline__ void give_up(volatile uint32_t *abort_flag, int64_t where) {
+  *abort_flag = 1u;
+  record_error(PKV_ERR_TIMEOUT, where);
+}
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
                                               volatile uint32_t *abort_flag, int64_t where) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -165,8 +169,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1u;
-      record_error(PKV_ERR_TIMEOUT, where);
+      give_up(abort_flag, where);
       return false;
     }
   }

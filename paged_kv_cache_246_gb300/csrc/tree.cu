@@ -29,8 +29,9 @@
 //               loaded from an out-of-range coordinate and arrive as zeros.  (One
 //               producer for both would hold the next K back until a V stage is
 //               free, a product later than its own.)
-//   warp 1      MMA issuer (one thread): S = Q K^T into one of two score
-//               buffers in tensor memory, O += P V with P read from there.
+//   warp 1      MMA issuer: S = Q K^T into one of two score buffers in tensor
+//               memory, O += P V with P read from there.
+//   warp 3      over an 8-bit cache: makes each segment's queries.
 //   warps 4-7   look through the V tiles that some row sees only in part (the
 //               tree's, and the window's edge): rows hidden from all are
 //               zeroed, values that are not finite are zeroed and the segment
@@ -177,18 +178,19 @@ struct Lay {
   // rings, as large as fit
   static constexpr int NK = KV8 ? 0 : (D == 128 ? 2 : 4);
   static constexpr int NV = KV8 ? 2 : (D == 128 ? 2 : 4);
-  static constexpr int N8K = !KV8 ? 0 : D == 128 ? 3 : 6;
-  static constexpr int N8V = !KV8 ? 0 : D == 128 ? 2 : 4;
-  static constexpr int NQ = KV8 ? 1 : 2;  // query buffers
+  static constexpr int N8K = !KV8 ? 0 : D == 64 ? 6 : TERMS == 2 ? 3 : 2;
+  static constexpr int N8V = !KV8 ? 0 : D == 64 ? 4 : TERMS == 2 ? 2 : 1;
+  static constexpr int NQ = 2;  // query buffers
   static constexpr int OFF_Q = 0;
-  static constexpr int Q_BYTES = KV8 ? TERMS * TILE8 : NQ * TILE;
+  static constexpr int Q_BYTES = NQ * (KV8 ? TERMS * TILE8 : TILE);
   static constexpr int OFF_K = OFF_Q + Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * TILE;
   static constexpr int OFF_K8 = OFF_V + NV * TILE;
   static constexpr int OFF_V8 = OFF_K8 + N8K * TILE8;
   static constexpr int OFF_MASK = OFF_V8 + N8V * TILE8;  // [words + 2][256 threads]
   static constexpr int OFF_ML = OFF_MASK + (kMaskWords + 2) * 256 * 4;  // [2][128] float2
-  static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+  static constexpr int OFF_EXP = OFF_ML + 2 * 128 * 8;  // [NQ][128] 2^e of the queries
+  static constexpr int OFF_BAR = OFF_EXP + NQ * 128 * 4;
   // copies landed (K, V, Q), stages free again (EK, EV, EQ; EV also: both
   // products of that tile done), V looked through (VG), V codes widened (E8V),
   // scores ready (S, per buffer), weights ready (P, per buffer), both
@@ -303,7 +305,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       uint32_t count = 1;
       if (i >= L::B_VG && i < L::B_VG + NV) count = kGuards;
       if (KV8 && i >= L::B_E8V && i < L::B_E8V + L::N8V) count = kGuards;
-      if (KV8 && i == L::B_Q) count = 8;
+      if (i >= L::B_EQ && i < L::B_EQ + L::NQ) count = 8;
       if (i == L::B_P || i == L::B_P + 1 || i == L::B_ML || i == L::B_EPI) count = 8;
       mbar_init(&bars[i], count);
     }
@@ -413,34 +415,39 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     constexpr int EMPTY = !V ? L::B_EK : KV8 ? L::B_E8V : L::B_EV;
     constexpr int BYTES = KV8 ? L::TILE8 : L::TILE;
     constexpr int OFF = KV8 ? (V ? L::OFF_V8 : L::OFF_K8) : (V ? L::OFF_V : L::OFF_K);
-    const int TB = BN / a.BS;
-    // lane l < TB: where cache block l of the segment's key tile j lies, or an
-    // out-of-range row (zeros) outside the visible range or for a bad entry
-    auto coord_of = [&](const Seg &s, int j) -> int {
-      int coord = -a.BS;
-      if (lane < TB) {
-        const int lb = (s.s.kv_start + (s.j0 + j) * BN) / a.BS + lane;
-        const int p0 = lb * a.BS;
-        if (p0 < s.s.L && p0 + a.BS > s.s.kv_lo) {
-          const int64_t e = static_cast<int64_t>(s.b) * a.max_blocks_per_seq + lb;
-          const int pb = __ldg(a.block_tables + e);
-          if (pb < 0 || pb >= a.num_blocks)
-            record_error(PKV_ERR_BOUNDS, e);
-          else
-            coord = pb * a.BS;
-        }
-      }
-      return coord;
+    const int TB = BN / a.BS, TPB = 32 / TB;  // blocks of a tile; tiles whose blocks a warp holds
+    // Lane l: the table's entry for block l of the TPB tiles from the segment's
+    // tile j on, loaded a batch ahead: a load under way for every 4 or 8 tiles.
+    auto entry = [&](const Seg &s, int j) -> int {
+      const int lb = (s.s.kv_start + (s.j0 + j) * BN) / a.BS + lane;
+      const int p0 = lb * a.BS;
+      return p0 < s.s.L && p0 + a.BS > s.s.kv_lo
+                 ? __ldg(a.block_tables + static_cast<int64_t>(s.b) * a.max_blocks_per_seq + lb)
+                 : -1;
+    };
+    // Where the lane's block lies, or an out-of-range row (zeros) outside the
+    // visible range or for a bad entry.
+    auto coord_of = [&](const Seg &s, int j, int pb) -> int {
+      const int lb = (s.s.kv_start + (s.j0 + j) * BN) / a.BS + lane;
+      const int p0 = lb * a.BS;
+      if (p0 >= s.s.L || p0 + a.BS <= s.s.kv_lo) return -a.BS;
+      if (pb >= 0 && pb < a.num_blocks) return pb * a.BS;
+      if (j + lane / TB < s.n)
+        record_error(PKV_ERR_BOUNDS, static_cast<int64_t>(s.b) * a.max_blocks_per_seq + lb);
+      return -a.BS;
     };
     Seg s, ahead;
     bool have = walk.next(a, s);
-    int next = have ? coord_of(s, 0) : 0;
+    int next = have ? entry(s, 0) : 0, coords = 0;
     int it = 0;  // key tiles
     for (int si = 0; have; ++si) {
       const bool more = walk.next(a, ahead);
       for (int j = 0; j < s.n; ++j, ++it) {
-        const int coord = next;
-        next = j + 1 < s.n ? coord_of(s, j + 1) : more ? coord_of(ahead, 0) : 0;
+        if (j % TPB == 0) {
+          coords = coord_of(s, j, next);
+          next = j + TPB < s.n ? entry(s, j + TPB) : more ? entry(ahead, 0) : 0;
+        }
+        const int coord = __shfl_sync(0xffffffffu, coords, (j % TPB) * TB + lane % TB);
         const int st = it % STAGES;
         if (it >= STAGES &&
             !warp_wait(&bars[EMPTY + st], ((it / STAGES) - 1) & 1, abort_flag, where))
@@ -480,6 +487,80 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     }
   };
 
+  // Over an 8-bit cache: each row's query as E4M3 terms of q * 2^-e, a segment
+  // ahead of its scores.  Lane = 16 channels of a row; one pass's loads run
+  // under the pass before.
+  auto queries = [&]() {
+    constexpr int LPR = D / 16, RPP = 32 / LPR;  // lanes of a row, rows of a pass
+    float *q_exp = reinterpret_cast<float *>(smem + L::OFF_EXP);
+    const int c = lane % LPR;
+    Seg s;
+#pragma unroll 1
+    for (int si = 0; walk.next(a, s); ++si) {
+      const int q = si % L::NQ;
+      if (si >= L::NQ && !warp_wait(&bars[L::B_EQ + q], ((si / L::NQ) - 1) & 1, abort_flag, where))
+        return;
+      uint8_t *dst = smem + L::OFF_Q + q * L::TERMS * L::TILE8;
+      const int rows = min(tile_rows, (s.s.nodes - node0) * a.QPK);
+      auto row_at = [&](int r) {
+        return reinterpret_cast<const uint4 *>(
+            a.query + (static_cast<int64_t>(s.s.row + node0 + r / a.QPK) * a.H + s.g * a.QPK +
+                       r % a.QPK) * D + c * 16);
+      };
+      int r = min(lane / LPR, rows - 1);
+      uint4 n0 = __ldg(row_at(r)), n1 = __ldg(row_at(r) + 1);
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += RPP) {
+        const uint4 v0 = n0, v1 = n1;
+        const int here = r;
+        r = min(r0 + RPP + lane / LPR, rows - 1);
+        n0 = __ldg(row_at(r));
+        n1 = __ldg(row_at(r) + 1);
+        // the row's largest finite |q|, as bits of a 16-bit value: whole numbers
+        // compare as the values do
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w = word_of(k < 4 ? v0 : v1, k % 4);
+          w &= ~not_finite<T>(w) & 0x7fff7fffu;
+          top = max(top, max(w & 0xffffu, w >> 16));
+        }
+#pragma unroll
+        for (int d = 1; d < LPR; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        // largest |q| 2^-e in [2^7, 2^8); queries below 2^-57 stay below that
+        const int e = max(static_cast<int>(__float_as_uint(T::to_f(static_cast<uint16_t>(top))) >> 23) - 134, -64);
+        const float mul = __int_as_float((127 - e) << 23);
+        uint32_t w[L::TERMS][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f0 = T::to_f2(word_of(k < 2 ? v0 : v1, 2 * (k % 2)));
+          const float2 f1 = T::to_f2(word_of(k < 2 ? v0 : v1, 2 * (k % 2) + 1));
+          const float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul),
+                              scaled_query(f1.x, mul), scaled_query(f1.y, mul)};
+          split_e4m3x4(y[0], y[1], y[2], y[3], w[0][k], w[1][k]);
+          if constexpr (L::TERMS == 3) {
+            // what both terms leave over
+            const uint2 h0 = e4m3x4_to_h4(w[0][k]), h1 = e4m3x4_to_h4(w[1][k]);
+            const float2 ha = FP16::to_f2(h0.x), hb = FP16::to_f2(h0.y);
+            const float2 ga = FP16::to_f2(h1.x), gb = FP16::to_f2(h1.y);
+            uint32_t rest;
+            split_e4m3x4(y[0] - ha.x - ga.x, y[1] - ha.y - ga.y, y[2] - hb.x - gb.x,
+                         y[3] - hb.y - gb.y, w[2][k], rest);
+          }
+        }
+        const int off = D == 128 ? here * 128 + ((c ^ (here & 7)) << 4)
+                                 : here * 64 + ((c ^ ((here >> 1) & 3)) << 4);
+#pragma unroll
+        for (int t = 0; t < L::TERMS; ++t)
+          *reinterpret_cast<uint4 *>(dst + t * L::TILE8 + off) =
+              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+        if (c == 0) q_exp[q * BM + here] = __int_as_float((127 + e) << 23);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bars[L::B_Q + q]);
+    }
+  };
+
   auto issuer = [&](const bool one) {
     constexpr uint32_t ID_QK = tc5::idesc_f16(KV8 ? 0 : AB<OPT>::v, 0, BM, BN);
     constexpr uint32_t ID_PV = tc5::idesc_f16(AB<OPT>::v, 1, BM, D);
@@ -490,11 +571,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     const uint64_t q_desc = KV8 ? desc8(L::OFF_Q) : tc5::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t k_desc = KV8 ? desc8(L::OFF_K8) : tc5::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     const uint64_t v_desc = tc5::sdesc_sw128(sbase + L::OFF_V, L::REG, 1024);
-    // Scores run two tiles ahead of the products with V, across segments over
-    // a 16-bit cache; over an 8-bit one a segment's queries are made when the
-    // last one's softmax has ended, and its scores begin then.  This thread
-    // feeds the tensor core, whose queue is short: it keeps little state and
-    // waits as seldom as it can.
+    // Scores run two tiles ahead of the products with V, across segments.  This
+    // warp feeds the tensor core, whose queue is short: it waits as seldom as it
+    // can, and its control flow is uniform, so that descriptors stay in uniform
+    // registers (one lane on its own: 109 cycles a product against 64).
     Walk walk_q = walk;
     int tq = 0, jq = 0, nq = 0, segs = 0;  // scores: next tile, its place in its segment of nq
     auto scores = [&]() -> bool {
@@ -514,69 +594,69 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       tc5::fence_after_sync();
       const uint32_t sb = tmem + (tq & 1) * 128;
       if (one) {
-      if constexpr (KV8) {
-        const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE8) >> 4);
+        if constexpr (KV8) {
+          const uint64_t qb = q_desc + static_cast<uint64_t>((((segs - 1) % L::NQ) * L::TERMS * L::TILE8) >> 4);
+          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE8) >> 4);
 #pragma unroll
-        for (int e = 0; e < L::TERMS; ++e)
+          for (int e = 0; e < L::TERMS; ++e)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            tc5::mma_ss_f8(sb, q_desc + static_cast<uint64_t>((e * L::TILE8 + k * 32) >> 4),
-                           kb + static_cast<uint64_t>(k * 2), ID_QK, (e | k) ? 1u : 0u);
-      } else {
-        const uint64_t qb = q_desc + static_cast<uint64_t>((((segs - 1) % L::NQ) * L::TILE) >> 4);
-        const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE) >> 4);
+            for (int k = 0; k < D / 32; ++k)
+              tc5::mma_ss_f8(sb, qb + static_cast<uint64_t>((e * L::TILE8 + k * 32) >> 4),
+                             kb + static_cast<uint64_t>(k * 2), ID_QK, (e | k) ? 1u : 0u);
+        } else {
+          const uint64_t qb = q_desc + static_cast<uint64_t>((((segs - 1) % L::NQ) * L::TILE) >> 4);
+          const uint64_t kb = k_desc + static_cast<uint64_t>((sk * L::TILE) >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = static_cast<uint64_t>(((k / 4) * L::REG + (k % 4) * 32) >> 4);
-          tc5::mma_ss(sb, qb + off, kb + off, ID_QK, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = static_cast<uint64_t>(((k / 4) * L::REG + (k % 4) * 32) >> 4);
+            tc5::mma_ss(sb, qb + off, kb + off, ID_QK, k > 0 ? 1u : 0u);
+          }
         }
-      }
-      tc5::commit(&bars[L::B_S + (tq & 1)]);
+        tc5::commit(&bars[L::B_S + (tq & 1)]);
       }
       __syncwarp();
       ++tq;
       ++jq;
       return true;
     };
-    int t = 0;
-    bool first = true;
-    while (true) {
-      Seg s;
-      s.n = 0;
-      walk.next(a, s);
-      const int n = __shfl_sync(0xffffffffu, s.n, 0);
-      if (n == 0) return;
-      if (KV8 || first) {
-        if (!scores()) return;
-        if ((!KV8 || n > 1) && !scores()) return;
-        first = false;
-      }
-      for (int j = 0; j < n; ++j, ++t) {
-        const int sv = t % NV, buf = t & 1;
+    // step u: the products with V of tile u - 2, then the scores of tile u
+    int n = 0, j = 0;  // tiles of the products' segment, place in it
+    for (int u = 0;; ++u) {
+      if (u >= 2) {
+        if (j == n) {
+          Seg s;
+          s.n = 0;
+          walk.next(a, s);
+          n = __shfl_sync(0xffffffffu, s.n, 0);
+          j = 0;
+          if (n == 0) return;
+        }
+        const int t = u - 2, sv = t % NV, buf = t & 1;
         if (!warp_wait(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
         if (!warp_wait(&bars[L::B_P + buf], (t / 2) & 1, abort_flag, where)) return;
         tc5::fence_after_sync();
         if (one) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t pb = tmem + buf * 128 + x * 64, ob = tmem + 256 + x * 128;
-          // keys 64 x .. of the tile: 16 of them are 2048 bytes of V
-          const uint64_t vb = v_desc + static_cast<uint64_t>((sv * L::TILE + x * 64 * 128) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc5::mma_ts(ob, pb + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV,
-                        k > 0 || j > 0 ? 1u : 0u);
-          if constexpr (TWO) {
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t pb = tmem + buf * 128 + x * 64, ob = tmem + 256 + x * 128;
+            // keys 64 x .. of the tile: 16 of them are 2048 bytes of V
+            const uint64_t vb = v_desc + static_cast<uint64_t>((sv * L::TILE + x * 64 * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc5::mma_ts(ob, pb + 32 + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, 1u);
+              tc5::mma_ts(ob, pb + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV,
+                          k > 0 || j > 0 ? 1u : 0u);
+            if constexpr (TWO) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc5::mma_ts(ob, pb + 32 + k * 8, vb + static_cast<uint64_t>(k * 128), ID_PV, 1u);
+            }
           }
-        }
-        tc5::commit(&bars[L::B_EV + sv]);
+          tc5::commit(&bars[L::B_EV + sv]);
         }
         __syncwarp();
-        if ((!KV8 || j + 2 < n) && !scores()) return;
+        ++j;
       }
+      if (!scores()) return;
     }
   };
 
@@ -600,6 +680,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         if constexpr (!KV8) {
           if (!warp_wait(&bars[L::B_V + sv], (it / NV) & 1, abort_flag, where)) return;
           if (edge) {
+#pragma unroll 1
             for (int i = lane; i < L::NREG * ROWS * 8; i += 32) {
               const int r = rows0 + (i / 8) % ROWS;
               uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_V + sv * L::TILE +
@@ -631,27 +712,30 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           if (!warp_wait(&bars[L::B_V + s8], (it / L::N8V) & 1, abort_flag, where)) return;
           if (it >= NV && !warp_wait(&bars[L::B_EV + sv], ((it / NV) - 1) & 1, abort_flag, where))
             return;
-          const uint8_t *src = smem + L::OFF_V8 + s8 * L::TILE8;
-          uint8_t *dst = smem + L::OFF_V + sv * L::TILE + (cc / 4) * L::REG;
-          const int k0 = (2 * cc) % 8;
-#pragma unroll 4
-          for (int i = 0; i < ROWS / RPI; ++i) {
-            const int r = rows0 + RPI * i + r0;
-            const int chunk = D == 128 ? (cc ^ (r & 7)) : (cc ^ ((r >> 1) & 3));
-            uint4 u = *reinterpret_cast<const uint4 *>(src + r * D + chunk * 16);
-            if (edge) {
-              if (r < lo || r >= hi) u = make_uint4(0, 0, 0, 0);
-              // bytes whose low 7 bits are all set: NaN
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-              uint32_t m[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t t = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                m[e] = (t >> 7) * 0xffu;
-                found |= t != 0;
+          uint8_t *src = smem + L::OFF_V8 + s8 * L::TILE8 + rows0 * D;
+          uint8_t *dst = smem + L::OFF_V + sv * L::TILE + (cc / 4) * L::REG + rows0 * 128;
+          if (edge) {
+            // bytes whose low 7 bits are all set are NaN
+#pragma unroll 1
+            for (int i = lane; i < ROWS * D / 4; i += 32) {
+              uint32_t *p = reinterpret_cast<uint32_t *>(src) + i;
+              const int r = rows0 + i / (D / 4);
+              const uint32_t w = *p, t = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (r < lo || r >= hi) {
+                *p = 0;
+              } else if (t) {
+                *p = w & ~((t >> 7) * 0xffu);
+                found = true;
               }
-              u = make_uint4(u.x & ~m[0], u.y & ~m[1], u.z & ~m[2], u.w & ~m[3]);
             }
+            __syncwarp();
+          }
+          const int k0 = (2 * cc) % 8;
+#pragma unroll 2
+          for (int i = 0; i < ROWS / RPI; ++i) {
+            const int r = RPI * i + r0;  // rows0 is a multiple of 8
+            const int chunk = D == 128 ? (cc ^ (r & 7)) : (cc ^ ((r >> 1) & 3));
+            const uint4 u = *reinterpret_cast<const uint4 *>(src + r * D + chunk * 16);
             const uint2 h0 = e4m3x4_to_h4(u.x), h1 = e4m3x4_to_h4(u.y);
             const uint2 h2 = e4m3x4_to_h4(u.z), h3 = e4m3x4_to_h4(u.w);
             const uint4 c0 = make_uint4(h0.x, h0.y, h1.x, h1.y);
@@ -683,68 +767,6 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     const bool rec = threadIdx.x == 256;
     if (rec) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-    // The row's query as E4M3 terms of q * 2^-e, for segment number si; each
-    // group makes half of the row.  Returns 2^e.
-    auto queries = [&](const Seg &s, int si, float &scale) -> bool {
-      if (si > 0 && !warp_wait(&bars[L::B_EQ], (si - 1) & 1, abort_flag, where)) return false;
-      // Loops that are not unrolled: this runs once a segment, out of cold
-      // instruction memory.  The row is read twice rather than held.
-      const bool valid = row_ok && node < s.s.nodes;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          a.query + (static_cast<int64_t>(s.s.row + node) * a.H + s.g * a.QPK + r % a.QPK) * D);
-      uint32_t top = 0;  // the largest finite |q|, as bits
-#pragma unroll 1
-      for (int i = 0; valid && i < D / 8; i += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __ldg(src + i + k);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 f = T::to_f2(word_of(v[k / 4], k % 4));
-          top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
-        }
-      }
-      // largest |q| 2^-e in [2^7, 2^8); queries below 2^-57 stay below that
-      const int e = max(static_cast<int>(top >> 23) - 134, -64);
-      const float mul = __int_as_float((127 - e) << 23);
-      scale = __int_as_float((127 + e) << 23);
-      uint8_t *dst = smem + L::OFF_Q;
-#pragma unroll 1
-      for (int c = x * (D / 32); c < (x + 1) * (D / 32); ++c) {  // 16 channels
-        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (valid) {
-          v[0] = __ldg(src + 2 * c);
-          v[1] = __ldg(src + 2 * c + 1);
-        }
-        uint32_t w[L::TERMS][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f0 = T::to_f2(word_of(v[k / 2], 2 * (k % 2)));
-          const float2 f1 = T::to_f2(word_of(v[k / 2], 2 * (k % 2) + 1));
-          const float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul),
-                              scaled_query(f1.x, mul), scaled_query(f1.y, mul)};
-          split_e4m3x4(y[0], y[1], y[2], y[3], w[0][k], w[1][k]);
-          if constexpr (L::TERMS == 3) {
-            // what both terms leave over
-            const uint2 h0 = e4m3x4_to_h4(w[0][k]), h1 = e4m3x4_to_h4(w[1][k]);
-            const float2 ha = FP16::to_f2(h0.x), hb = FP16::to_f2(h0.y);
-            const float2 ga = FP16::to_f2(h1.x), gb = FP16::to_f2(h1.y);
-            uint32_t rest;
-            split_e4m3x4(y[0] - ha.x - ga.x, y[1] - ha.y - ga.y, y[2] - hb.x - gb.x,
-                         y[3] - hb.y - gb.y, w[2][k], rest);
-          }
-        }
-        const int off = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-#pragma unroll
-        for (int t = 0; t < L::TERMS; ++t)
-          *reinterpret_cast<uint4 *>(dst + t * L::TILE8 + off) =
-              make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-      }
-      fence_proxy_async_smem();
-      warp_arrive(&bars[L::B_Q]);
-      return true;
-    };
-
     int here = 0;  // the node's position
     // The node's ancestors, those inside the window: a bit each.
     auto look_up = [&](const Seg &s) {
@@ -767,13 +789,11 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     };
 
     const bool biased = a.alibi != nullptr;
-    Seg s, ahead;
-    float q_scale = 1.f;
-    bool have = walk.next(a, s), more = false;
-    if (KV8 && have && !queries(s, 0, q_scale)) return;
+    const float *q_exp = reinterpret_cast<const float *>(smem + L::OFF_EXP);
+    Seg s;
     int last_b = -1;
     int base = 0;  // key tiles before the segment
-    for (int si = 0; have; ++si) {
+    for (int si = 0; walk.next(a, s); ++si) {
       const bool valid = row_ok && node < s.s.nodes;
       const bool busy = __any_sync(0xffffffffu, valid);
       // a new sequence's path: behind the first tile's work where that can do without
@@ -783,24 +803,26 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       last_b = s.b;
       const int lo = a.window > 0 ? max(0, here - a.window + 1) : 0;
       const int head = s.g * a.QPK + r % a.QPK;
-      const float sl2 = KV8 ? a.scale_log2 * q_scale : a.scale_log2;
+      float sl2 = a.scale_log2;
       const float slope = biased && row_ok ? __ldg(a.alibi + head) * kLog2e : 0.f;
       // log2 units of a score and of the maximum: the scale is folded into the
       // exponent's FMA, with ALiBi into the scores
-      const float unit = biased ? 1.f : sl2;
+      float unit = biased ? 1.f : sl2;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < s.n; ++k) {
         const int t = base + k, buf = t & 1;
         const uint32_t sb = tmem + lane_base + buf * 128 + x * HN;
         if (!warp_wait(&bars[L::B_S + buf], (t / 2) & 1, abort_flag, where)) return;
-        if (rec) {
-          // the scores are there: their keys are read, after the last ones the queries.
-          // (As commits of the issuing thread these would hold the tensor core's queue.)
-          mbar_arrive(&bars[L::B_EK + t % NKT]);
-          if (k == s.n - 1) mbar_arrive(&bars[L::B_EQ + si % L::NQ]);
-        }
+        // the scores are there: their keys are read.  (As a commit of the issuer's this
+        // would hold the tensor core's queue.)
+        if (rec) mbar_arrive(&bars[L::B_EK + t % NKT]);
         __syncwarp();
         tc5::fence_after_sync();
+        if (KV8 && k == 0) {
+          // scores are there, so their queries' scale is
+          sl2 *= q_exp[si % L::NQ * BM + r];
+          if (!biased) unit = sl2;
+        }
         if (busy) {
           uint32_t raw[HN];
 #pragma unroll
@@ -941,14 +963,11 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           return;
         tc5::fence_before_sync();
         warp_arrive(&bars[L::B_P + buf]);
-        if (k == 0) {
-          if (later) look_up(s);
-          more = walk.next(a, ahead);
-        }
+        if (k == 0 && later) look_up(s);
+        // after the last scores every warp is done with the queries and their scale
+        if (k == s.n - 1) warp_arrive(&bars[L::B_EQ + si % L::NQ]);
       }
       base += s.n;
-      // the next segment's queries, while this one's last products run
-      if (KV8 && more && !queries(ahead, si + 1, q_scale)) return;
 
       // ---- the segment's end ----
       float top = m * unit;
@@ -1016,8 +1035,6 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         while (slot + 1 + parts < shares && total * (slot + 1 + parts) / shares < end) ++parts;
         a.record[blockIdx.x] = make_int4(s.b, s.g, parts, 0);
       }
-      have = more;
-      s = ahead;
     }
     tc5::fence_before_sync();
   };
@@ -1036,6 +1053,8 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       producer(std::false_type{});
     } else if (warp == 2) {
       producer(std::true_type{});
+    } else if (KV8 && warp == 3) {
+      queries();
     } else if (warp == 1) {
       const bool one = tc5::elect_one();
       issuer(one);
