@@ -87,7 +87,7 @@ struct Args {
   float2 *part_ml;   // [CTA][2][128]: maximum (log2 units), sum
   int4 *record;      // [CTA]: sequence, KV head, further CTAs of the item that its last segment begins
   int64_t num_blocks, row_elems;
-  int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window, groups;
+  int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window, groups, item_units;
   float scale_log2, v_scale;
 };
 
@@ -130,7 +130,7 @@ struct Seg {
 
 // A CTA's segments, in order: every role walks them by itself.
 struct Walk {
-  int b, g, j, node0;  // tile j of KV head g of sequence b
+  int b, g, j, node0;  // unit j of KV head g of sequence b
   int64_t left;        // units to go
   bool known = false;
   Seq s;
@@ -144,14 +144,16 @@ struct Walk {
         }
         known = true;
       }
+      const int item = s.tiles + a.item_units;
+      const int take = static_cast<int>(min(static_cast<int64_t>(item - j), left));
       o.s = s;
       o.b = b;
       o.g = g;
-      o.j0 = j;
-      o.n = static_cast<int>(min(static_cast<int64_t>(s.tiles - j), left));
-      left -= o.n;
-      j += o.n;
-      if (j == s.tiles) {
+      o.j0 = max(j - a.item_units, 0);
+      j += take;
+      left -= take;
+      o.n = max(j - a.item_units, 0) - o.j0;
+      if (j == item) {
         j = 0;
         if (++g == a.KVH) {
           g = 0;
@@ -159,7 +161,7 @@ struct Walk {
           known = false;
         }
       }
-      return true;
+      if (o.n > 0) return true;
     }
     return false;
   }
@@ -190,7 +192,8 @@ struct Lay {
   static constexpr int OFF_MASK = OFF_V8 + N8V * TILE8;  // [words + 2][256 threads]
   static constexpr int OFF_ML = OFF_MASK + (kMaskWords + 2) * 256 * 4;  // [2][128] float2
   static constexpr int OFF_EXP = OFF_ML + 2 * 128 * 8;  // [NQ][128] 2^e of the queries
-  static constexpr int OFF_BAR = OFF_EXP + NQ * 128 * 4;
+  static constexpr int OFF_BAD = OFF_EXP + NQ * 128 * 4;                // [8][32] words of a pass that are not finite
+  static constexpr int OFF_BAR = OFF_BAD + 8 * 32 * 4;
   // copies landed (K, V, Q), stages free again (EK, EV, EQ; EV also: both
   // products of that tile done), V looked through (VG), V codes widened (E8V),
   // scores ready (S, per buffer), weights ready (P, per buffer), both
@@ -331,8 +334,9 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 
   // ---- this CTA's share of the units ----
   Walk walk;
-  int64_t total, u0, u1;
-  int shares;
+  int64_t total, u0, u1, per_share;
+  int shares, more_shares;  // the first more_shares shares have a unit more than per_share
+  auto share_start = [&](int i) -> int64_t { return i * per_share + min(i, more_shares); };
   {
     int64_t *scan = reinterpret_cast<int64_t *>(misc + kScan);  // [12 warps]
     auto units = [&](int b) -> int64_t {
@@ -340,7 +344,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       bool bad = false;
       int64_t u = 0;
       if (b < a.tb.num_seqs) {
-        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(s.tiles) * a.KVH;
+        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(s.tiles + a.item_units) * a.KVH;
         if (bad && blockIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
       }
       return u;
@@ -373,8 +377,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       total += all;
     }
     shares = static_cast<int>(min(static_cast<int64_t>(slots), total));  // no empty ones among them
-    u0 = slot < shares ? total * slot / shares : total;
-    u1 = slot < shares ? total * (slot + 1) / shares : total;
+    per_share = shares > 0 ? total / shares : 0;
+    more_shares = static_cast<int>(total - per_share * shares);
+    u0 = slot < shares ? share_start(slot) : total;
+    u1 = slot < shares ? share_start(slot + 1) : total;
     // the sequence that holds unit u0
     int64_t *start = reinterpret_cast<int64_t *>(misc + kStart);  // sequence, units into it
     auto find = [&](int b, int64_t incl, int64_t own) {
@@ -402,8 +408,9 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       Seq s;
       bool bad;
       seq_of(a, walk.b, node0, s, bad);
-      walk.g = static_cast<int>(start[1] / s.tiles);
-      walk.j = static_cast<int>(start[1] - static_cast<int64_t>(walk.g) * s.tiles);
+      const int item = s.tiles + a.item_units;
+      walk.g = static_cast<int>(start[1] / item);
+      walk.j = static_cast<int>(start[1] - static_cast<int64_t>(walk.g) * item);
     }
   }
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[kTmem], 0);
@@ -493,6 +500,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   auto queries = [&]() {
     constexpr int LPR = D / 16, RPP = 32 / LPR;  // lanes of a row, rows of a pass
     float *q_exp = reinterpret_cast<float *>(smem + L::OFF_EXP);
+    uint32_t *bad_q = reinterpret_cast<uint32_t *>(smem + L::OFF_BAD);
     const int c = lane % LPR;
     Seg s;
 #pragma unroll 1
@@ -516,37 +524,56 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         r = min(r0 + RPP + lane / LPR, rows - 1);
         n0 = __ldg(row_at(r));
         n1 = __ldg(row_at(r) + 1);
-        // the row's largest finite |q|, as bits of a 16-bit value: whole numbers
-        // compare as the values do
-        uint32_t top = 0;
+        // the row's largest |q| as a 16-bit value: whole numbers compare as the
+        // values do
+        uint32_t x[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        auto largest = [&]() -> uint32_t {
+          uint32_t two = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t w = word_of(k < 4 ? v0 : v1, k % 4);
-          w &= ~not_finite<T>(w) & 0x7fff7fffu;
-          top = max(top, max(w & 0xffffu, w >> 16));
+          for (int k = 0; k < 8; ++k) two = __vmaxu2(two, x[k] & 0x7fff7fffu);
+          uint32_t top = max(two & 0xffffu, two >> 16);
+#pragma unroll
+          for (int d = 1; d < LPR; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          return top;
+        };
+        uint32_t top = largest();
+        if (__any_sync(0xffffffffu, top >= T::kInf)) {
+          // the largest finite one; infinities become NaN (their codes would be finite)
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t w = k < 4 ? word_of(v0, k) : word_of(v1, k - 4);
+            bad_q[k * 32 + lane] = without_infinities<T>(w);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = bad_q[k * 32 + lane] & ~not_finite<T>(bad_q[k * 32 + lane]);
+          top = largest();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = bad_q[k * 32 + lane];
         }
-#pragma unroll
-        for (int d = 1; d < LPR; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         // largest |q| 2^-e in [2^7, 2^8); queries below 2^-57 stay below that
         const int e = max(static_cast<int>(__float_as_uint(T::to_f(static_cast<uint16_t>(top))) >> 23) - 134, -64);
         const float mul = __int_as_float((127 - e) << 23);
         uint32_t w[L::TERMS][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 f0 = T::to_f2(word_of(k < 2 ? v0 : v1, 2 * (k % 2)));
-          const float2 f1 = T::to_f2(word_of(k < 2 ? v0 : v1, 2 * (k % 2) + 1));
-          const float y[4] = {scaled_query(f0.x, mul), scaled_query(f0.y, mul),
-                              scaled_query(f1.x, mul), scaled_query(f1.y, mul)};
-          split_e4m3x4(y[0], y[1], y[2], y[3], w[0][k], w[1][k]);
-          if constexpr (L::TERMS == 3) {
-            // what both terms leave over
-            const uint2 h0 = e4m3x4_to_h4(w[0][k]), h1 = e4m3x4_to_h4(w[1][k]);
-            const float2 ha = FP16::to_f2(h0.x), hb = FP16::to_f2(h0.y);
-            const float2 ga = FP16::to_f2(h1.x), gb = FP16::to_f2(h1.y);
-            uint32_t rest;
-            split_e4m3x4(y[0] - ha.x - ga.x, y[1] - ha.y - ga.y, y[2] - hb.x - gb.x,
-                         y[3] - hb.y - gb.y, w[2][k], rest);
+          uint32_t half[L::TERMS][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // a pair as fp16: exact but for what lies 2^-31 below the row's largest
+            const float2 f = T::to_f2(x[2 * k + h]);
+            __half2 rest = __floats2half2_rn(f.x * mul, f.y * mul);
+#pragma unroll
+            for (int t = 0; t < L::TERMS; ++t) {
+              const __half2_raw raw = rest;
+              half[t][h] = __nv_cvt_halfraw2_to_fp8x2(raw, __NV_SATFINITE, __NV_E4M3);
+              if (t + 1 < L::TERMS) {
+                const __half2_raw code = __nv_cvt_fp8x2_to_halfraw2(half[t][h], __NV_E4M3);
+                rest = __hsub2(rest, __half2(code));
+              }
+            }
           }
+#pragma unroll
+          for (int t = 0; t < L::TERMS; ++t) w[t][k] = half[t][0] | half[t][1] << 16;
         }
         const int off = D == 128 ? here * 128 + ((c ^ (here & 7)) << 4)
                                  : here * 64 + ((c ^ ((here >> 1) & 3)) << 4);
@@ -1032,7 +1059,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         // how many of the following CTAs the rest of the item goes to
         const int64_t end = u1 - s.n + s.s.tiles;
         int parts = 0;
-        while (slot + 1 + parts < shares && total * (slot + 1 + parts) / shares < end) ++parts;
+        while (slot + 1 + parts < shares && share_start(slot + 1 + parts) < end) ++parts;
         a.record[blockIdx.x] = make_int4(s.b, s.g, parts, 0);
       }
     }
@@ -1091,6 +1118,11 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 // CTA's own second partial segment, then the first one of every following CTA.
 // Thread = (row, four channels).
 // ---------------------------------------------------------------------------
+// An infinite value stays what it is where its part's weight vanishes.
+__device__ __forceinline__ float scaled(float x, float w) {
+  return fabsf(x) < INFINITY ? w * x : x;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
   grid_dependency_wait();
@@ -1108,20 +1140,38 @@ __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
   auto place = [&](int i) -> int64_t {
     return static_cast<int64_t>(cta + i * a.groups) * 2 + (i == 0 ? 1 : 0);
   };
-  float top = -INFINITY;
-  for (int i = 0; i <= rec.z; ++i) top = fmaxf(top, a.part_ml[place(i) * BM + r].x);
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i <= rec.z; ++i) {
-    const float2 ml = a.part_ml[place(i) * BM + r];
-    const float4 p =
-        *reinterpret_cast<const float4 *>(a.part_o + ((place(i) * (D / 4) + d4) * BM + r) * 4);
-    const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-    l += w * ml.y;
-    // an infinite value stays what it is where its part's weight vanishes
-    o[0] += fabsf(p.x) < INFINITY ? w * p.x : p.x;
-    o[1] += fabsf(p.y) < INFINITY ? w * p.y : p.y;
-    o[2] += fabsf(p.z) < INFINITY ? w * p.z : p.z;
-    o[3] += fabsf(p.w) < INFINITY ? w * p.w : p.w;
+  float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int DEPTH = 8;  // parts whose loads are under way together
+#pragma unroll 1
+  for (int i0 = 0; i0 <= rec.z; i0 += DEPTH) {
+    float2 ml[DEPTH];
+    float4 p[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + i <= rec.z) {
+        ml[i] = a.part_ml[place(i0 + i) * BM + r];
+        p[i] = *reinterpret_cast<const float4 *>(a.part_o + ((place(i0 + i) * (D / 4) + d4) * BM + r) * 4);
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) now = fmaxf(now, ml[i].x);
+    const float f = top == -INFINITY ? 0.f : fast_exp2(top - now);
+    top = now;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = scaled(o[k], f);
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      const float w = ml[i].x == -INFINITY ? 0.f : fast_exp2(ml[i].x - top);
+      l += w * ml[i].y;
+      o[0] += scaled(p[i].x, w);
+      o[1] += scaled(p[i].y, w);
+      o[2] += scaled(p[i].z, w);
+      o[3] += scaled(p[i].w, w);
+    }
   }
   const float inv = a.v_scale / l;
   const int64_t row = static_cast<int64_t>(s.row + node) * a.H + rec.y * a.QPK + r % a.QPK;
@@ -1132,6 +1182,13 @@ __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+// What a (sequence, KV head) costs beside its tiles, in tiles: the softmax of
+// its first and last ones, the accumulators' way out, instructions that are not
+// at hand (3000 to 6000 cycles, a tile 2000).  These units come before the
+// item's tiles; without them a CTA whose share is short contexts took 1.6 times
+// the others' time (128 contexts of 100 .. 4096 tokens over an 8-bit cache).
+static int item_units(const Geometry &g) { return g.fp8 ? 6 : 4; }
+
 struct Plan {
   int groups, ctas;
   size_t part_o, part_ml, bytes;  // offsets behind the records, and the whole
@@ -1143,7 +1200,8 @@ static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g
   p.groups = (max_nodes + per_tile - 1) / per_tile;
   int64_t keys = max_seq_len;
   if (g.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(g.window) + max_nodes + BN);
-  const int64_t units = static_cast<int64_t>(num_seqs) * g.KVH * std::max<int64_t>(1, (keys + BN - 1) / BN);
+  const int64_t units = static_cast<int64_t>(num_seqs) * g.KVH *
+                        (std::max<int64_t>(1, (keys + BN - 1) / BN) + item_units(g));
   const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units));
   p.ctas = static_cast<int>(slots) * p.groups;
   const size_t parts = static_cast<size_t>(p.ctas) * 2 * BM;
@@ -1207,6 +1265,7 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
   a.BS = g.BS;
   a.window = g.window;
   a.groups = p.groups;
+  a.item_units = tree::item_units(g);
   a.scale_log2 = g.scale * kLog2e * g.k_scale;
   a.v_scale = g.v_scale;
   const bool bf = g.dtype == PKV_BF16;
