@@ -836,7 +836,11 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       // exponent's FMA, with ALiBi into the scores
       float unit = biased ? 1.f : sl2;
       float m = -INFINITY, l = 0.f;
-      for (int k = 0; k < s.n; ++k) {
+      bool unset = true;  // some row of the warp has no maximum yet
+      const int n = s.n, calm0 = s.calm_from(a), calm1 = s.calm_to();
+      int kv0 = s.s.kv_start + s.j0 * BN + x * HN;
+#pragma unroll 1
+      for (int k = 0; k < n; ++k, kv0 += BN) {
         const int t = base + k, buf = t & 1;
         const uint32_t sb = tmem + lane_base + buf * 128 + x * HN;
         if (!warp_wait(&bars[L::B_S + buf], (t / 2) & 1, abort_flag, where)) return;
@@ -856,7 +860,6 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           for (int c = 0; c < HN / 32; ++c)
             tc5::tmem_ld32(sb + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(raw + 32 * c));
           tc5::tmem_ld_wait();
-          const int kv0 = s.s.kv_start + (s.j0 + k) * BN + x * HN;
           if (biased) {
             const float b0 = slope * static_cast<float>(kv0 - here);
 #pragma unroll
@@ -864,8 +867,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
               raw[e] = __float_as_uint(fmaf(__uint_as_float(raw[e]), sl2,
                                             fmaf(slope, static_cast<float>(e), b0)));
           }
-          const bool full = !valid || (kv0 + HN <= s.s.ctx && kv0 >= lo);
-          if (__any_sync(0xffffffffu, !full)) {
+          if (k < calm0 || k >= calm1) {
             const int off = kv0 - s.s.ctx;  // the node that stands at kv0
             // nodes of the row's path behind these keys: each puts a step of depth
             // between a key and the row
@@ -908,8 +910,8 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           }
           // p = 2^(score - mu), written over the scores as one or two terms; returns the sum
           auto exps = [&](float mu) -> float {
-            const float mul = biased ? 1.f : sl2;
-            const unsigned long long mul2 = f2pack(mul, mul), negmu2 = f2pack(-mu, -mu);
+            const unsigned long long mul2 = f2pack(unit, unit), negmu2 = f2pack(-mu, -mu);
+            const unsigned long long minus = f2pack(-1.f, -1.f);
             unsigned long long ps2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < HN / 32; ++c) {
@@ -922,11 +924,14 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
                                mul2, negmu2),
                          x0, x1);
                 const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                ps2[(e / 2) & 3] = fadd2(ps2[(e / 2) & 3], f2pack(p0, p1));
+                const unsigned long long p = f2pack(p0, p1);
+                ps2[(e / 2) & 3] = fadd2(ps2[(e / 2) & 3], p);
                 hi[e / 2] = OPT::from_f2(p0, p1);
                 if constexpr (TWO) {
                   const float2 h = OPT::to_f2(hi[e / 2]);
-                  low[e / 2] = OPT::from_f2(p0 - h.x, p1 - h.y);
+                  float r0, r1;
+                  f2unpack(ffma2(f2pack(h.x, h.y), minus, p), r0, r1);
+                  low[e / 2] = OPT::from_f2(r0, r1);
                 }
               }
               tc5::tmem_st16(sb + 16 * c, hi);
@@ -939,14 +944,15 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           // The reference moves lazily: exponents are taken against m as it
           // stands; only where a row's sum is out of range (or m not set) is
           // the maximum looked for and the pass repeated.
-          float alpha = 1.f, ps = 0.f;
-          bool moved = false;
-          bool look = __any_sync(0xffffffffu, valid && m == -INFINITY);
+          float ps = 0.f;
+          bool look = unset;
           if (!look) {
-            ps = exps(m == -INFINITY ? 0.f : m * unit);
+            ps = exps(m * unit);
             look = __any_sync(0xffffffffu, valid && !(ps <= 32768.f));
           }
           if (look) {
+            float alpha = 1.f;
+            bool moved = false;
             float pm[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) pm[q] = -INFINITY;
@@ -962,27 +968,29 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
               m = mx;
               moved = valid;
             }
+            unset = __any_sync(0xffffffffu, valid && m == -INFINITY);
             tc5::tmem_st_wait();  // a first pass's weights are written before they are replaced
             ps = exps(m == -INFINITY ? 0.f : m * unit);
-          }
-          l = l * alpha + ps;
-          if (__any_sync(0xffffffffu, moved)) {
-            // the accumulator holds the product before this one once that has completed
-            // (the one before that has: these scores came after it)
-            if (!warp_wait(&bars[L::B_EV + (t - 1) % NV], ((t - 1) / NV) & 1, abort_flag, where))
-              return;
-            tc5::fence_after_sync();
-            const uint32_t ob = tmem + lane_base + 256 + x * 128;
+            l *= alpha;
+            if (__any_sync(0xffffffffu, moved)) {
+              // the accumulator holds the product before this one once that has completed
+              // (the one before that has: these scores came after it)
+              if (!warp_wait(&bars[L::B_EV + (t - 1) % NV], ((t - 1) / NV) & 1, abort_flag, where))
+                return;
+              tc5::fence_after_sync();
+              const uint32_t ob = tmem + lane_base + 256 + x * 128;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tc5::tmem_ld32(ob + 32 * c, o);
-              tc5::tmem_ld_wait();
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc5::tmem_ld32(ob + 32 * c, o);
+                tc5::tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc5::tmem_st32(ob + 32 * c, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc5::tmem_st32(ob + 32 * c, o);
+              }
             }
           }
+          l += ps;
           tc5::tmem_st_wait();
         }
         // the other group has read this accumulator's last segment
@@ -991,10 +999,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         tc5::fence_before_sync();
         warp_arrive(&bars[L::B_P + buf]);
         if (k == 0 && later) look_up(s);
-        // after the last scores every warp is done with the queries and their scale
-        if (k == s.n - 1) warp_arrive(&bars[L::B_EQ + si % L::NQ]);
       }
-      base += s.n;
+      // after the last scores every warp is done with the queries and their scale
+      warp_arrive(&bars[L::B_EQ + si % L::NQ]);
+      base += n;
 
       // ---- the segment's end ----
       float top = m * unit;
