@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["abi.cu", "kv_ops.cu", "decode.cu", "prefill.cu", "rope.cu", "select.cu",
-           "sparse.cu", "tree.cu", "tree_ops.cu"]
+           "sparse.cu", "tree.cu", "tree_bf16.cu", "tree_fp16.cu", "tree_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
