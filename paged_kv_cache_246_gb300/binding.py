@@ -9,8 +9,10 @@ library has not been built (``python -m paged_kv_cache_246_gb300.build_lib``).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -649,9 +651,9 @@ def rope_pair_axes(sections: Sequence[int], woven: bool = False) -> tuple:
 
 
 @functools.lru_cache(maxsize=64)
-def _pair_axes(axes: tuple) -> tuple:
+def _pair_axes(axes: bytes) -> tuple:
     """(array for the call, axes that it names)"""
-    if not axes or not all(isinstance(a, int) and 0 <= a < 4 for a in axes):
+    if not axes or max(axes) >= 4:
         raise ValueError("pair_axes must name an axis 0 .. 3 for every pair of channels")
     return (ctypes.c_uint8 * len(axes))(*axes), max(axes) + 1
 
@@ -670,8 +672,8 @@ def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: 
     if n != T:
         raise ValueError("positions and slot_mapping sizes disagree")
     max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
-    array, named = _pair_axes(tuple(pair_axes))
-    if len(array) != rot_dim // 2 or named > axes:
+    axis_array, named = _pair_axes(bytes(pair_axes))
+    if len(axis_array) != rot_dim // 2 or named > axes:
         raise ValueError(f"pair_axes must name one of the {axes} axes for each of the "
                          f"{rot_dim // 2} pairs")
     so = _row_stride(query_out, "query_out", T, q_row, dtype)
@@ -681,7 +683,7 @@ def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: 
     _call_on("kv_cache_write_rope_axes", stream,
              (kv_cache, query_out, query, key, value, slot_mapping, positions, cos_sin),
              query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(),
-             sv, T, positions.data_ptr(), T, axes, array, cos_sin.data_ptr(), max_position, rot_dim,
+             sv, T, positions.data_ptr(), T, axes, axis_array, cos_sin.data_ptr(), max_position, rot_dim,
              1 if interleaved else 0, kv_cache.data_ptr(), nb, slot_mapping.data_ptr(),
              ctypes.byref(params))
 
@@ -751,6 +753,11 @@ def paged_attn_tree_accept(accepted: torch.Tensor, num_accepted: torch.Tensor,
              cu_nodes.data_ptr(), n, T, _int32(max_nodes, "max_nodes"))
 
 
+_get_dtype, _get_shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_is_contiguous, _get_device = torch.Tensor.is_contiguous, torch.Tensor.get_device
+_data_ptr = torch.Tensor.data_ptr
+
+
 def kv_commit_tree(kv_caches: Sequence[torch.Tensor], accepted: torch.Tensor,
                    block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_nodes: torch.Tensor,
                    params: AttnParams, stream=None) -> None:
@@ -760,19 +767,22 @@ def kv_commit_tree(kv_caches: Sequence[torch.Tensor], accepted: torch.Tensor,
         return
     _, cache_dtype, _, _, _, _, block = _facts(params)
     nb = _is_cache(kv_caches[0], cache_dtype, block)
-    shape = kv_caches[0].shape
-    for k, c in enumerate(kv_caches):
-        if _is(c, "kv_caches", cache_dtype, 3) != shape:
-            raise ValueError("all caches must have the same number of blocks")
+    # a call a layer and check, without the interpreter between them
+    if (set(map(_get_dtype, kv_caches)) != {cache_dtype} or not all(map(_is_contiguous, kv_caches)) or
+            any(map(kv_caches[0].shape.__ne__, map(_get_shape, kv_caches)))):
+        raise ValueError("all caches must be contiguous, of the cache's type and of one shape")
+    if set(map(_get_device, kv_caches)) != {kv_caches[0].get_device()}:
+        raise ValueError("kv_commit_tree: all caches must be on one CUDA device")
     n, wide = _is_batch(block_tables, seq_lens)
     seqs, most = _is(accepted, "accepted", torch.int32, 2)
     if seqs != n:
         raise ValueError("accepted must be [num_seqs, max_accepted]")
     _is_trees(cu_nodes, n)
-    array = (ctypes.c_void_p * len(kv_caches))(*[c.data_ptr() for c in kv_caches])
-    _call_on("kv_commit_tree", stream, (*kv_caches, accepted, block_tables, seq_lens, cu_nodes),
-             array, len(kv_caches), nb, accepted.data_ptr(), most, block_tables.data_ptr(), wide,
-             seq_lens.data_ptr(), cu_nodes.data_ptr(), n, ctypes.byref(params))
+    pointers = array.array("Q", map(_data_ptr, kv_caches))
+    _call_on("kv_commit_tree", stream, (kv_caches[0], accepted, block_tables, seq_lens, cu_nodes),
+             pointers.buffer_info()[0], len(kv_caches), nb, accepted.data_ptr(), most,
+             block_tables.data_ptr(), wide, seq_lens.data_ptr(), cu_nodes.data_ptr(), n,
+             ctypes.byref(params))
 
 
 def check_wait_timeout(tag: int, stream=None) -> None:

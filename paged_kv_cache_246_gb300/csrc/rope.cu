@@ -242,8 +242,14 @@ rope_write_kernel(const Args a) {
 // first items' rows are on their way meanwhile); from there the heads' lanes
 // read them as the kernel above reads a table row.  The pairs' axes, 2 bits
 // each, are launch arguments.
+//
+// BULK: CTAs of 96 threads, 16 to an SM: while one waits for its table rows
+// others move theirs.  16384 tokens of 48 heads of 128: 65 us (6.3 TB/s), with
+// 192 threads 71, with 64 65, with 384 80; into an 8-bit cache 64 / 68 / 64 / 83.
+// Two of a thread's items loaded ahead spill (105), a row gathered by each warp
+// instead of the barrier is equal (71 against 71).
 template <class T, int D, bool KV8, bool INTER, bool BULK>
-__global__ void __launch_bounds__(BULK ? 192 : 512, BULK ? 8 : 1)
+__global__ void __launch_bounds__(BULK ? 96 : 512, BULK ? 16 : 1)
 rope_axes_write_kernel(const Args a, const Axes x) {
   __shared__ __align__(16) float row[128];
   grid_dependency_wait();
@@ -287,7 +293,7 @@ static cudaError_t launch_typed(const Args &a, const Axes *x, bool interleaved,
   if (e != cudaSuccess) return e;
   const bool bulk = a.num_tokens > 6LL * dev.sms;
   PdlLaunch cfg(dim3(static_cast<unsigned>(a.num_tokens)),
-                std::min(bulk ? 192 : 512, (items + 31) / 32 * 32), 0, stream);
+                std::min(!bulk ? 512 : x ? 96 : 192, (items + 31) / 32 * 32), 0, stream);
 #define PKV_ROPE_FORM(IN, BULK)                                                             \
   return x ? cudaLaunchKernelEx(&cfg.c, rope_axes_write_kernel<T, D, KV8, IN, BULK>, a, *x) \
            : cudaLaunchKernelEx(&cfg.c, rope_write_kernel<T, D, KV8, IN, BULK>, a)

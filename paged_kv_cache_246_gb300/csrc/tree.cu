@@ -7,28 +7,32 @@
 namespace pkv {
 namespace tree {
 
-// What a (sequence, KV head) costs beside its tiles, in tiles: the softmax of
-// its first and last ones, the accumulators' way out, instructions that are not
-// at hand (3000 to 6000 cycles, a tile 2000).  These units come before the
-// item's tiles; without them a CTA whose share is short contexts took 1.6 times
-// the others' time (128 contexts of 100 .. 4096 tokens over an 8-bit cache).
-static int item_units(const Geometry &g) { return g.fp8 ? 6 : 4; }
-
 struct Plan {
-  int groups, ctas;
+  int groups, ctas, item_units;
   size_t part_o, part_ml, bytes;  // offsets behind the records, and the whole
 };
 
 static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g, int sms) {
-  Plan p;
+  Plan p{};
   const int per_tile = BM / g.QPK;
   p.groups = (max_nodes + per_tile - 1) / per_tile;
   int64_t keys = max_seq_len;
   if (g.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(g.window) + max_nodes + BN);
-  const int64_t units = static_cast<int64_t>(num_seqs) * g.KVH *
-                        (std::max<int64_t>(1, (keys + BN - 1) / BN) + item_units(g));
-  const int64_t slots = std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units));
-  p.ctas = static_cast<int>(slots) * p.groups;
+  const int64_t tiles = std::max<int64_t>(1, (keys + BN - 1) / BN);
+  // Items (a sequence's KV head) of up to 2 tiles are not cut: the CTAs take
+  // whole ones, and the merge of parts is not launched (one context of 250
+  // tokens, 8 KV heads: 10.9 us, cut 12.6; of 500 14.0, cut 13.3).
+  // What an item costs beside its tiles, in tiles: the softmax of its first and
+  // last ones, the accumulators' way out, instructions that are not at hand
+  // (3000 to 6000 cycles, a tile 2000).  These units come before the item's
+  // tiles; without them a CTA whose share is short contexts took 1.6 times the
+  // others' time (128 contexts of 100 .. 4096 tokens, 8-bit cache: 290 us
+  // with 0, 232 with 5; 16384 x 64: 448 and 433).
+  p.item_units = tiles <= 2 ? 0 : g.fp8 ? 6 : 4;
+  const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH;
+  const int64_t units = p.item_units == 0 ? items : items * (tiles + p.item_units);
+  p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units))) * p.groups;
+  if (p.item_units == 0) return p;
   const size_t parts = static_cast<size_t>(p.ctas) * 2 * BM;
   p.part_ml = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
   p.part_o = p.part_ml + parts * sizeof(float2);
@@ -73,7 +77,7 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
   a.BS = g.BS;
   a.window = g.window;
   a.groups = p.groups;
-  a.item_units = tree::item_units(g);
+  a.item_units = p.item_units;
   a.scale_log2 = g.scale * kLog2e * g.k_scale;
   a.v_scale = g.v_scale;
   const bool bf = g.dtype == PKV_BF16;

@@ -114,6 +114,12 @@ struct Seg {
   __device__ __forceinline__ int calm_to() const { return (s.ctx - s.kv_start) / BN - j0; }
 };
 
+// Units of a (sequence, KV head): its tiles behind item_units more; one where
+// items are not cut (item_units 0).
+__device__ __forceinline__ int units_of(const Args &a, const Seq &s) {
+  return a.item_units > 0 ? s.tiles + a.item_units : 1;
+}
+
 // A CTA's segments, in order: every role walks them by itself.
 struct Walk {
   int b, g, j, node0;  // unit j of KV head g of sequence b
@@ -130,7 +136,7 @@ struct Walk {
         }
         known = true;
       }
-      const int item = s.tiles + a.item_units;
+      const int item = units_of(a, s);
       const int take = static_cast<int>(min(static_cast<int64_t>(item - j), left));
       o.s = s;
       o.b = b;
@@ -138,7 +144,7 @@ struct Walk {
       o.j0 = max(j - a.item_units, 0);
       j += take;
       left -= take;
-      o.n = max(j - a.item_units, 0) - o.j0;
+      o.n = a.item_units > 0 ? max(j - a.item_units, 0) - o.j0 : s.tiles;
       if (j == item) {
         j = 0;
         if (++g == a.KVH) {
@@ -330,7 +336,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       bool bad = false;
       int64_t u = 0;
       if (b < a.tb.num_seqs) {
-        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(s.tiles + a.item_units) * a.KVH;
+        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(units_of(a, s)) * a.KVH;
         if (bad && blockIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
       }
       return u;
@@ -394,7 +400,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       Seq s;
       bool bad;
       seq_of(a, walk.b, node0, s, bad);
-      const int item = s.tiles + a.item_units;
+      const int item = units_of(a, s);
       walk.g = static_cast<int>(start[1] / item);
       walk.j = static_cast<int>(start[1] - static_cast<int64_t>(walk.g) * item);
     }
@@ -778,7 +784,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::OFF_MASK) + x * 128 + r;  // word w: [(w + 1) * 256]
     float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
     const bool rec = threadIdx.x == 256;
-    if (rec) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (rec && a.item_units > 0) a.record[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     int here = 0;  // the node's position
     // The node's ancestors, those inside the window: a bit each.
@@ -1185,7 +1191,7 @@ static cudaError_t launch(const Args &a, int ctas, const CUtensorMap &qmap,
     e = cudaLaunchKernelEx(&cfg.c, kern, a, qmap, kvmap);
     if (e != cudaSuccess) return e;
   }
-  if (ctas == a.groups) return cudaSuccess;  // one CTA has all of a group's work: no parts
+  if (a.item_units == 0) return cudaSuccess;  // no parts
   PdlLaunch cfg(dim3(ctas, BM / 8), 8 * D / 4, 0, stream);
   return cudaLaunchKernelEx(&cfg.c, combine_kernel<T, D>, a);
 }
