@@ -408,6 +408,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[kTmem], 0);
 
   // K and the queries (V = false), or V
+  int issued = 0;  // copies of this role, to be drained after an abort
   auto producer = [&](auto is_v) {
     constexpr bool V = decltype(is_v)::value;
     constexpr int STAGES = V ? NVT : NKT, FULL = V ? L::B_V : L::B_K;
@@ -448,24 +449,21 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         }
         const int coord = __shfl_sync(0xffffffffu, coords, (j % TPB) * TB + lane % TB);
         const int st = it % STAGES;
+        uint64_t *full = &bars[FULL + st];
+        uint8_t *dst = smem + OFF + st * BYTES + lane * a.BS * (KV8 ? D : 128);
+        // little is left to do when the stage is free: this warp shares its
+        // scheduler with two of the softmax's
         if (it >= STAGES &&
             !warp_wait(&bars[EMPTY + st], ((it / STAGES) - 1) & 1, abort_flag, where))
           return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars[FULL + st], BYTES);
-          misc[V ? kIssuedV : kIssuedK] = it + 1;
-        }
+        if (lane == 0) mbar_arrive_expect_tx(full, BYTES);
         __syncwarp();
         if (lane < TB) {
-          if constexpr (KV8) {
-            tma_load_4d(smem + OFF + st * L::TILE8 + lane * a.BS * D, &kvmap, &bars[FULL + st], 0,
-                        s.g, coord, V);
-          } else {
-            for (int r = 0; r < L::NREG; ++r)
-              tma_load_4d(smem + OFF + st * L::TILE + r * L::REG + lane * a.BS * 128, &kvmap,
-                          &bars[FULL + st], 64 * r, s.g, coord, V);
-          }
+#pragma unroll
+          for (int r = 0; r < (KV8 ? 1 : L::NREG); ++r)
+            tma_load_4d(dst + r * L::REG, &kvmap, full, 64 * r, s.g, coord, V);
         }
+        issued = it + 1;
         if (!KV8 && !V && j == 0) {
           const int q = si % L::NQ;
           if (si >= L::NQ &&
@@ -1078,8 +1076,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     set_registers<false, 72>();
     if (warp == 0) {
       producer(std::false_type{});
+      if (lane == 0) misc[kIssuedK] = issued;
     } else if (warp == 2) {
       producer(std::true_type{});
+      if (lane == 0) misc[kIssuedV] = issued;
     } else if (KV8 && warp == 3) {
       queries();
     } else if (warp == 1) {
