@@ -8,14 +8,14 @@ namespace pkv {
 namespace tree {
 
 struct Plan {
-  int groups, ctas, item_units;
+  int tile_nodes, row_tiles, ctas, item_units;
   size_t part_o, part_ml, bytes;  // offsets behind the records, and the whole
 };
 
 static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g, int sms) {
   Plan p{};
-  const int per_tile = BM / g.QPK;
-  p.groups = (max_nodes + per_tile - 1) / per_tile;
+  p.tile_nodes = BM / g.QPK;
+  p.row_tiles = (max_nodes + p.tile_nodes - 1) / p.tile_nodes;
   int64_t keys = max_seq_len;
   if (g.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(g.window) + max_nodes + BN);
   const int64_t tiles = std::max<int64_t>(1, (keys + BN - 1) / BN);
@@ -29,9 +29,9 @@ static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g
   // others' time (128 contexts of 100 .. 4096 tokens, 8-bit cache: 290 us
   // with 0, 232 with 5; 16384 x 64: 448 and 433).
   p.item_units = tiles <= 2 ? 0 : g.fp8 ? 6 : 4;
-  const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH;
+  const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH * p.row_tiles;
   const int64_t units = p.item_units == 0 ? items : items * (tiles + p.item_units);
-  p.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / p.groups, units))) * p.groups;
+  p.ctas = static_cast<int>(std::min<int64_t>(sms, units));
   if (p.item_units == 0) return p;
   const size_t parts = static_cast<size_t>(p.ctas) * 2 * BM;
   p.part_ml = (static_cast<size_t>(p.ctas) * sizeof(int4) + 255) / 256 * 256;
@@ -76,7 +76,8 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
   a.QPK = g.QPK;
   a.BS = g.BS;
   a.window = g.window;
-  a.groups = p.groups;
+  a.tile_nodes = p.tile_nodes;
+  a.row_tiles = p.row_tiles;
   a.item_units = p.item_units;
   a.scale_log2 = g.scale * kLog2e * g.k_scale;
   a.v_scale = g.v_scale;

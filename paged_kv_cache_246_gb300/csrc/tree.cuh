@@ -29,9 +29,12 @@ struct Args {
   const float *alibi;
   float *part_o;     // [CTA][2][D / 4][128][4]
   float2 *part_ml;   // [CTA][2][128]: maximum (log2 units), sum
-  int4 *record;      // [CTA]: sequence, KV head, further CTAs of the item that its last segment begins
+  int4 *record;      // [CTA]: sequence, KV head, further CTAs, first node of the item that its last segment begins
   int64_t num_blocks, row_elems;
-  int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window, groups, item_units;
+  int max_blocks_per_seq, max_seq_len, H, KVH, QPK, BS, window;
+  int tile_nodes;  // nodes of a row tile: 128 / QPK
+  int row_tiles;   // of the widest tree that may come
+  int item_units;  // what an item costs beside its tiles, in tiles (0: items are not cut)
   float scale_log2, v_scale;
 };
 

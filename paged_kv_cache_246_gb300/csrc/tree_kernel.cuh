@@ -10,17 +10,16 @@
 // against 281 of the card); mma.sync tiles of 16 rows, as the other decodes
 // use, would read K and V from L2 once per tile.
 //
-// CTA = one per SM, persistent.  The work is the list of (sequence, KV head,
-// 128-key tile) units in this order; every CTA takes an equal, contiguous
-// share of it, found from seq_lens and cu_nodes on the device, and walks it
-// segment by segment (a segment: its part of one sequence's KV head).  A
-// segment that is a whole (sequence, KV head) writes the output; a part writes
-// its (o, m, l) in fp32, and combine_kernel merges the parts in order.  So all
-// SMs read the same amount whatever the lengths are, and every CTA has at most
-// two partial segments (its first and its last).  Trees of several row tiles
-// are that many groups; group i runs on the CTAs i, i + groups, ..., which walk
-// the same units at the same time, so that K and V come from L2 for all groups
-// but one.
+// CTA = one per SM, persistent.  The work is the list of units (row tile,
+// sequence, KV head, 128-key tile), in this order; every CTA takes an equal,
+// contiguous share of it, found from seq_lens and cu_nodes on the device, and
+// walks it segment by segment (a segment: its part of one item, a sequence's KV
+// head and row tile).  A segment that is a whole item writes the output; a part
+// writes its (o, m, l) in fp32, and combine_kernel merges the parts in order.
+// So all SMs do the same amount whatever the lengths and trees are, and every
+// CTA has at most two partial segments (its first and its last).  The first row
+// tiles of all trees come first, then the second ones: the CTAs of each walk the
+// same K and V side by side, from HBM once and from L2 for the others.
 //
 // Roles of the 16 warps:
 //   warps 0, 2  TMA producers of K (and each segment's query rows) and of V: tiles
@@ -84,15 +83,14 @@ struct Seq {
   int row, nodes, ctx, L, kv_lo, kv_start, tiles;
 };
 
-// Sequence b for a CTA whose rows begin at node0; false: nothing to do, `bad`
-// where what the tensors say cannot be.
-__device__ __forceinline__ bool seq_of(const Args &a, int b, int node0, Seq &s, bool &bad) {
+// Sequence b; false: nothing to do, `bad` where what the tensors say cannot be.
+__device__ __forceinline__ bool seq_of(const Args &a, int b, Seq &s, bool &bad) {
   bad = !nodes_of(a.tb, b, s.row, s.nodes);
   s.L = __ldg(a.seq_lens + b);
   if (bad || s.nodes == 0) return false;
   bad = s.L < s.nodes || s.L > a.max_seq_len ||
         s.L > static_cast<int64_t>(a.max_blocks_per_seq) * a.BS;
-  if (bad || s.nodes <= node0) return false;
+  if (bad) return false;
   s.ctx = s.L - s.nodes;
   // the first position that a node of depth 0 sees: deeper ones see less
   s.kv_lo = a.window > 0 ? max(0, s.ctx - a.window + 1) : 0;
@@ -104,6 +102,7 @@ __device__ __forceinline__ bool seq_of(const Args &a, int b, int node0, Seq &s, 
 struct Seg {
   Seq s;
   int b, g, j0, n;  // tiles j0 .. j0 + n - 1 of KV head g
+  int node0;        // the row tile's first node
   __device__ __forceinline__ bool whole() const { return n == s.tiles; }
   // Of the segment's tiles all rows see those from calm_from to before calm_to
   // whole: in front of them lies the window's edge (a node of depth nodes - 1
@@ -122,15 +121,20 @@ __device__ __forceinline__ int units_of(const Args &a, const Seq &s) {
 
 // A CTA's segments, in order: every role walks them by itself.
 struct Walk {
-  int b, g, j, node0;  // unit j of KV head g of sequence b
-  int64_t left;        // units to go
+  int row_tile, b, g, j;  // unit j of KV head g of sequence b
+  int64_t left;           // units to go
   bool known = false;
   Seq s;
   __device__ __forceinline__ bool next(const Args &a, Seg &o) {
-    while (left > 0 && b < a.tb.num_seqs) {
+    while (left > 0 && row_tile < a.row_tiles) {
+      if (b >= a.tb.num_seqs) {
+        b = 0;
+        ++row_tile;
+        continue;
+      }
       if (!known) {
         bool bad;
-        if (!seq_of(a, b, node0, s, bad)) {
+        if (!seq_of(a, b, s, bad) || s.nodes <= row_tile * a.tile_nodes) {
           ++b;
           continue;
         }
@@ -141,6 +145,7 @@ struct Walk {
       o.s = s;
       o.b = b;
       o.g = g;
+      o.node0 = row_tile * a.tile_nodes;
       o.j0 = max(j - a.item_units, 0);
       j += take;
       left -= take;
@@ -210,6 +215,13 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
+
+// Registers of a thread at the launch (the most that 512 threads can have, and
+// what the kernels use), and in the warpgroups of warps 0-3, 4-7 and 8-15.
+// Taking more than the launch's pool holds would wait for ever, so launch()
+// makes sure of the kernel's count.
+constexpr int kLaunchRegs = 128, kIssueRegs = 72, kGuardRegs = 104, kSoftmaxRegs = 168;
+static_assert(kIssueRegs + kGuardRegs + 2 * kSoftmaxRegs <= 4 * kLaunchRegs);
 
 // Registers of this warpgroup's threads from here on: every warp of it calls.
 template <bool MORE, int N>
@@ -288,11 +300,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int64_t where = blockIdx.x;
-  const int nodes_per_tile = BM / a.QPK;
-  const int tile_rows = nodes_per_tile * a.QPK;
-  const int group = blockIdx.x % a.groups, slot = blockIdx.x / a.groups;
-  const int slots = gridDim.x / a.groups;
-  const int node0 = group * nodes_per_tile;
+  const int tile_rows = a.tile_nodes * a.QPK;
 
   // ---- before the kernel ahead has completed: nothing that it may write ----
   if (threadIdx.x == 0) {
@@ -326,80 +334,103 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 
   // ---- this CTA's share of the units ----
   Walk walk;
-  int64_t total, u0, u1, per_share;
+  int64_t total = 0, u0, u1, per_share;
   int shares, more_shares;  // the first more_shares shares have a unit more than per_share
   auto share_start = [&](int i) -> int64_t { return i * per_share + min(i, more_shares); };
   {
-    int64_t *scan = reinterpret_cast<int64_t *>(misc + kScan);  // [12 warps]
-    auto units = [&](int b) -> int64_t {
+    int64_t *scan = reinterpret_cast<int64_t *>(misc + kScan);                 // [2][16 warps], by turns
+    int turn = 0;
+    int64_t *tile_units = reinterpret_cast<int64_t *>(smem + L::OFF_MASK);     // [row tiles], not in use yet
+    int64_t *start = reinterpret_cast<int64_t *>(misc + kStart);               // sequence, units into it
+    // a sequence's units in each of its first `n` row tiles
+    auto units = [&](int b, int &n) -> int64_t {
       Seq s;
       bool bad = false;
       int64_t u = 0;
+      n = 0;
       if (b < a.tb.num_seqs) {
-        if (seq_of(a, b, node0, s, bad)) u = static_cast<int64_t>(units_of(a, s)) * a.KVH;
+        if (seq_of(a, b, s, bad)) {
+          u = static_cast<int64_t>(units_of(a, s)) * a.KVH;
+          n = (s.nodes + a.tile_nodes - 1) / a.tile_nodes;
+        }
         if (bad && blockIdx.x == 0) record_error(PKV_ERR_BOUNDS, b);
       }
       return u;
     };
-    // inclusive sum over the CTA's threads; every thread gets the sum over all
-    auto block_scan = [&](int64_t v, int64_t &all) -> int64_t {
+    auto warp_scan = [&](int64_t v) -> int64_t {
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
         const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += o;
       }
-      if (lane == 31) scan[warp] = v;
-      __syncthreads();
-      int64_t before = 0;
-      all = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        all += scan[w];
-      }
-      __syncthreads();
-      return v + before;
+      return v;
     };
-    const int64_t mine = units(threadIdx.x);
-    int64_t first_all;
-    const int64_t first_incl = block_scan(mine, first_all);
-    total = first_all;
-    for (int b0 = kThreads; b0 < a.tb.num_seqs; b0 += kThreads) {
-      int64_t all;
-      block_scan(units(b0 + threadIdx.x), all);
+    // inclusive sum over the CTA's threads; every thread gets the sum over all
+    auto block_scan = [&](int64_t v, int64_t &all) -> int64_t {
+      int64_t *sums = scan + (turn ^= 16);
+      v = warp_scan(v);
+      if (lane == 31) sums[warp] = v;
+      __syncthreads();
+      const int64_t w = warp_scan(lane < kThreads / 32 ? sums[lane] : 0);
+      all = __shfl_sync(0xffffffffu, w, 31);
+      const int64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) % 32);
+      return warp > 0 ? v + before : v;
+    };
+    // the units of each row tile, up to the last one that a tree has
+    int my_tiles, tiles = 0;
+    const int64_t mine = units(threadIdx.x, my_tiles);
+    int64_t incl0 = 0;  // of the first row tile and the first kThreads sequences
+    for (int t = 0; t < a.row_tiles; ++t) {
+      int64_t v = my_tiles > t ? mine : 0, all;
+      for (int b = threadIdx.x + kThreads; b < a.tb.num_seqs; b += kThreads) {
+        int n;
+        const int64_t u = units(b, n);
+        if (n > t) v += u;
+      }
+      v = block_scan(v, all);
+      if (t == 0) incl0 = v;
+      if (all == 0) break;
+      if (threadIdx.x == 0) tile_units[t] = all;
       total += all;
+      tiles = t + 1;
     }
+    const int slots = gridDim.x, slot = blockIdx.x;
     shares = static_cast<int>(min(static_cast<int64_t>(slots), total));  // no empty ones among them
     per_share = shares > 0 ? total / shares : 0;
     more_shares = static_cast<int>(total - per_share * shares);
     u0 = slot < shares ? share_start(slot) : total;
     u1 = slot < shares ? share_start(slot + 1) : total;
-    // the sequence that holds unit u0
-    int64_t *start = reinterpret_cast<int64_t *>(misc + kStart);  // sequence, units into it
-    auto find = [&](int b, int64_t incl, int64_t own) {
-      if (u0 < incl && u0 >= incl - own) {
-        start[0] = b;
-        start[1] = u0 - (incl - own);
+    // the row tile and the sequence that hold unit u0
+    int tile = 0;
+    int64_t into = u0, base = 0;
+    if (tiles > 1) {
+      __syncthreads();
+      while (tile < tiles && into >= tile_units[tile]) into -= tile_units[tile++];
+    }
+    for (int b0 = 0; b0 < a.tb.num_seqs && base <= into; b0 += kThreads) {
+      int64_t all = total, own = mine, incl = incl0;
+      int n = my_tiles;
+      if (b0 > 0) own = units(b0 + threadIdx.x, n);
+      if (n <= tile) own = 0;
+      // the sum at hand is the first row tile's where all sequences have a thread
+      if (tile > 0 || a.tb.num_seqs > kThreads) incl = base + block_scan(own, all);
+      if (into < incl && into >= incl - own) {
+        start[0] = b0 + threadIdx.x;
+        start[1] = into - (incl - own);
       }
-    };
-    find(threadIdx.x, first_incl, mine);
-    int64_t base = first_all;
-    for (int b0 = kThreads; b0 < a.tb.num_seqs && base <= u0; b0 += kThreads) {
-      int64_t all;
-      const int64_t own = units(b0 + threadIdx.x), incl = base + block_scan(own, all);
-      find(b0 + threadIdx.x, incl, own);
       base += all;
     }
     tc5::fence_before_sync();
     __syncthreads();
     tc5::fence_after_sync();
-    walk.node0 = node0;
     walk.left = u1 - u0;
+    walk.row_tile = tile;
     walk.b = walk.g = walk.j = 0;
     if (walk.left > 0) {
       walk.b = static_cast<int>(start[0]);
       Seq s;
       bool bad;
-      seq_of(a, walk.b, node0, s, bad);
+      seq_of(a, walk.b, s, bad);
       const int item = units_of(a, s);
       walk.g = static_cast<int>(start[1] / item);
       walk.j = static_cast<int>(start[1] - static_cast<int64_t>(walk.g) * item);
@@ -474,7 +505,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
             misc[kIssuedQ] = si + 1;
             for (int r = 0; r < L::NREG; ++r)
               tc5::tma_load_3d(smem + L::OFF_Q + q * L::TILE + r * L::REG, &qmap, &bars[L::B_Q + q],
-                               64 * r, s.g * a.QPK, s.s.row + node0);
+                               64 * r, s.g * a.QPK, s.s.row + s.node0);
           }
           __syncwarp();
         }
@@ -499,10 +530,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       if (si >= L::NQ && !warp_wait(&bars[L::B_EQ + q], ((si / L::NQ) - 1) & 1, abort_flag, where))
         return;
       uint8_t *dst = smem + L::OFF_Q + q * L::TERMS * L::TILE8;
-      const int rows = min(tile_rows, (s.s.nodes - node0) * a.QPK);
+      const int rows = min(tile_rows, (s.s.nodes - s.node0) * a.QPK);
       auto row_at = [&](int r) {
         return reinterpret_cast<const uint4 *>(
-            a.query + (static_cast<int64_t>(s.s.row + node0 + r / a.QPK) * a.H + s.g * a.QPK +
+            a.query + (static_cast<int64_t>(s.s.row + s.node0 + r / a.QPK) * a.H + s.g * a.QPK +
                        r % a.QPK) * D + c * 16);
       };
       int r = min(lane / LPR, rows - 1);
@@ -777,7 +808,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     const int x = warp >= 12 ? 1 : 0;     // the first ones or the last
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int node = node0 + r / a.QPK;
+    const int row_node = r / a.QPK, row_head = r % a.QPK;
     const bool row_ok = r < tile_rows;
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::OFF_MASK) + x * 128 + r;  // word w: [(w + 1) * 256]
     float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
@@ -786,7 +817,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 
     int here = 0;  // the node's position
     // The node's ancestors, those inside the window: a bit each.
-    auto look_up = [&](const Seg &s) {
+    auto look_up = [&](const Seg &s, int node) {
 #pragma unroll 1
       for (int w = 0; w < kMaskWords + 2; ++w) mask[w * 256] = 0;
       int depth = -1;
@@ -807,18 +838,20 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 
     const float *q_exp = reinterpret_cast<const float *>(smem + L::OFF_EXP);
     Seg s;
-    int last_b = -1;
+    int last_b = -1, last_node = -1;
     int base = 0;  // key tiles before the segment
     for (int si = 0; walk.next(a, s); ++si) {
+      const int node = s.node0 + row_node;
       const bool valid = row_ok && node < s.s.nodes;
       const bool busy = __any_sync(0xffffffffu, valid);
       // a new sequence's path: behind the first tile's work where that can do without
-      const bool fresh = s.b != last_b;
+      const bool fresh = s.b != last_b || s.node0 != last_node;
       const bool later = fresh && a.window <= 0 && !ALIBI && s.s.kv_start + (s.j0 + 1) * BN <= s.s.ctx;
-      if (fresh && !later) look_up(s);
+      if (fresh && !later) look_up(s, node);
       last_b = s.b;
+      last_node = s.node0;
       const int lo = a.window > 0 ? max(0, here - a.window + 1) : 0;
-      const int head = s.g * a.QPK + r % a.QPK;
+      const int head = s.g * a.QPK + row_head;
       float sl2 = a.scale_log2;
       const float slope = ALIBI && row_ok ? __ldg(a.alibi + head) * kLog2e : 0.f;
       // log2 units of a score and of the maximum: the scale is folded into the
@@ -988,7 +1021,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           return;
         tc5::fence_before_sync();
         warp_arrive(&bars[L::B_P + buf]);
-        if (k == 0 && later) look_up(s);
+        if (k == 0 && later) look_up(s, node);
       }
       // after the last scores every warp is done with the queries and their scale
       warp_arrive(&bars[L::B_EQ + si % L::NQ]);
@@ -1057,23 +1090,23 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         // how many of the following CTAs the rest of the item goes to
         const int64_t end = u1 - s.n + s.s.tiles;
         int parts = 0;
-        while (slot + 1 + parts < shares && share_start(slot + 1 + parts) < end) ++parts;
-        a.record[blockIdx.x] = make_int4(s.b, s.g, parts, 0);
+        const int next = blockIdx.x + 1;
+        while (next + parts < shares && share_start(next + parts) < end) ++parts;
+        a.record[blockIdx.x] = make_int4(s.b, s.g, parts, s.node0);
       }
     }
     tc5::fence_before_sync();
   };
 
-  // The four warpgroups' registers: 512 for a thread of each, as at the launch
-  // (4 x 128), but where they are needed.
+  // the launch's registers, but where they are needed
   if (warp >= 8) {
-    set_registers<true, 168>();
+    set_registers<true, kSoftmaxRegs>();
     softmax();
   } else if (warp >= 4) {
-    set_registers<false, 104>();
+    set_registers<false, kGuardRegs>();
     guard();
   } else {
-    set_registers<false, 72>();
+    set_registers<false, kIssueRegs>();
     if (warp == 0) {
       producer(std::false_type{});
       if (lane == 0) misc[kIssuedK] = issued;
@@ -1132,13 +1165,12 @@ __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
   if (rec.z <= 0) return;
   const int r = blockIdx.y * 8 + threadIdx.x % 8;
   const int d4 = threadIdx.x / 8;
-  const int nodes_per_tile = BM / a.QPK;
-  const int node = cta % a.groups * nodes_per_tile + r / a.QPK;
+  const int node = rec.w + r / a.QPK;
   Seq s;
   bool bad;
-  if (r >= nodes_per_tile * a.QPK || !seq_of(a, rec.x, 0, s, bad) || node >= s.nodes) return;
+  if (r >= a.tile_nodes * a.QPK || !seq_of(a, rec.x, s, bad) || node >= s.nodes) return;
   auto place = [&](int i) -> int64_t {
-    return static_cast<int64_t>(cta + i * a.groups) * 2 + (i == 0 ? 1 : 0);
+    return static_cast<int64_t>(cta + i) * 2 + (i == 0 ? 1 : 0);
   };
   float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   constexpr int DEPTH = 8;  // parts whose loads are under way together
@@ -1183,9 +1215,17 @@ template <class T, int D, bool KV8, bool ALIBI>
 static cudaError_t launch(const Args &a, int ctas, const CUtensorMap &qmap,
                           const CUtensorMap &kvmap, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
+  static std::atomic<int> registers{0};
   auto kern = tree_tc_kernel<T, D, KV8, ALIBI>;
   cudaError_t e = allow_shared_memory(kern, done, 0);
   if (e != cudaSuccess) return e;
+  if (registers.load(std::memory_order_acquire) == 0) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    registers.store(at.numRegs, std::memory_order_release);
+  }
+  if (registers.load(std::memory_order_acquire) < kLaunchRegs) return cudaErrorLaunchOutOfResources;
   {
     PdlLaunch cfg(dim3(ctas), kThreads, Lay<T, D, KV8>::ALLOC, stream);
     e = cudaLaunchKernelEx(&cfg.c, kern, a, qmap, kvmap);

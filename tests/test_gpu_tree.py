@@ -145,6 +145,31 @@ def test_many_sequences():
     check(s, rows=rows)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_mixed_trees(fp8):
+    # some trees of several row tiles among small and empty ones: the row tiles' lists differ
+    s = TreeScene([600, 40, 0, 333, 129, 70, 2], [3, 200, 1, 33, 0, 90, 64], 8, 2, 64, 16, BF, fp8, seed=31, padding=2)
+    check(s, rows={0, 2, 3, 4, 130, 202, 203, 204, 236, 237, 290, 326, 327, 390})
+    check(s, max_nodes=B.PKV_TREE_MAX_NODES, max_len=20000, rows={0, 202, 203, 236, 326, 390})
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_scenes(seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda *v: v[int(torch.randint(len(v), (1,), generator=g))]
+    n = int(torch.randint(1, 7, (1,), generator=g))
+    top = pick(1, 5, 20, 70)
+    ctx = torch.randint(0, pick(3, 130, 700), (n,), generator=g).tolist()
+    nodes = torch.randint(0, top + 1, (n,), generator=g).tolist()
+    nodes[-1] = max(1, nodes[-1])
+    kv = pick(1, 2, 3)
+    s = TreeScene(ctx, nodes, kv * pick(1, 2, 4, 5, 8), kv, pick(64, 128), pick(16, 32), pick(BF, FP), pick(False, True),
+                  pick(0, 0, 1, 30, 200), pick(False, False, True), pick("bushy", "chain", "star", "forest"), seed,
+                  padding=pick(0, 3))
+    rows = set(torch.randint(0, s.rows, (12,), generator=g).tolist())
+    check(s, rows=rows)
+
+
 # ---- values ----------------------------------------------------------------------
 
 
