@@ -1,10 +1,11 @@
-"""GPU times of the block-sparse decode's calls, without the host's: captured in a CUDA graph over three sets of inputs and
-replayed (median of 7 replays of 30 calls).
+"""GPU times of the block-sparse decode's and the speculative step's calls, without the host's: captured in a CUDA graph over three
+sets of inputs and replayed (median of 7 replays of 30 calls).
 
-    python perf/gpu_times.py [cases] [more] [data] [step]
+    python perf/gpu_times.py [cases] [more] [data] [step] [tree] [tree_more]
 
 cases: those of operators.py; more: forms of them that it does not list; data: the selection over scores of other kinds; step: the
-four calls of a decode step against the dense cache write and decode.
+four calls of a decode step against the dense cache write and decode; tree: the cases of more_operators.py; tree_more: forms of
+them that it does not list, and the run of tokens that paged_attn_decode_multi takes.
 """
 from __future__ import annotations
 
@@ -15,11 +16,13 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import torch  # noqa: E402
 
+import perf.more_operators as tree_ops  # noqa: E402
 import perf.operators as ops  # noqa: E402
 from paged_kv_cache_246_gb300 import binding as B  # noqa: E402
 
-ops.own = True
+ops.own = tree_ops.own = True
 LISTED = {c["name"]: c for c in ops.listed()}
+TREES = {c["name"]: c for c in tree_ops.listed()}
 
 
 def gpu_us(calls, reps=30):
@@ -42,7 +45,7 @@ def gpu_us(calls, reps=30):
     return sorted(times)[3]
 
 
-def time_case(label, case, change=None):
+def time_case(label, case, change=None, ops=ops):
     states = [ops.prepare(case, seed) for seed in range(3)]
     for s in states:
         if change:
@@ -125,6 +128,41 @@ def step():
         torch.cuda.empty_cache()
 
 
+def tree():
+    for name, case in TREES.items():
+        time_case(name, case, ops=tree_ops)
+
+
+def tree_more():
+    for name, kw in (("axes_16384", dict(woven=True)), ("axes_16384", dict(fp8=True)),
+                     ("axes_16384", dict(rot=128, sections="16,24,24", interleaved=False, packed=True)),
+                     ("tree_1_short", dict(len_lo=250, len_hi=250)), ("tree_1_short", dict(len_lo=4000, len_hi=4000)),
+                     ("tree_64", dict(nodes_lo=1, nodes_hi=1)), ("tree_64", dict(nodes_lo=2, nodes_hi=40)),
+                     ("tree_64", dict(nodes_lo=64, nodes_hi=64)), ("tree_64", dict(alibi=True)), ("tree_64", dict(fp8=True)),
+                     ("tree_64", dict(len_lo=100, len_hi=600)), ("tree_128_fp8", dict(fp8=False)),
+                     ("tree_128_fp8", dict(dtype="fp16")), ("tree_32_mha", dict(window=0)),
+                     ("tree_32_mha", dict(nodes_lo=200, nodes_hi=256))):
+        time_case(f"{name} with {kw}", {**TREES[name], **kw}, ops=tree_ops)
+    # a captured step's bound on the nodes, far above them
+    time_case("tree_64, max_nodes 256", TREES["tree_64"], lambda s: s.update(max_nodes=256), tree_ops)
+    # a run of tokens through both calls
+    for tokens in (4, 8, 16, 32):
+        s = tree_ops.prepare({**TREES["tree_64"], "nodes_lo": tokens, "nodes_hi": tokens, "padding": 0}, 1)
+        p = B.make_params(32, 8, 128, 16, torch.bfloat16, 128 ** -0.5)
+        n, top = s["seq_lens"].numel(), s["max_len"]
+        s["parents"].copy_((torch.arange(n * tokens, device="cuda") % tokens - 1).int())
+        ws, multi = (torch.empty(max(16, size), dtype=torch.uint8, device="cuda") for size in (
+            B.paged_attn_decode_tree_workspace_size(n, tokens, top, p),
+            B.paged_attn_decode_multi_workspace_size(n, tokens, top, p)))
+        t = gpu_us([lambda: B.paged_attn_decode_tree(s["out"], s["query"], s["cache"], s["tables"], s["seq_lens"], s["cu"],
+                                                     s["parents"], tokens, top, p, ws)])
+        m = gpu_us([lambda: B.paged_attn_decode_multi(s["out"], s["query"], s["cache"], s["tables"], s["seq_lens"], tokens, top, p,
+                                                      multi)])
+        print(f"64 runs of {tokens} tokens behind 4096 .. 16384: tree {t:.1f} us, multi {m:.1f} us", flush=True)
+        del s
+        torch.cuda.empty_cache()
+
+
 if __name__ == "__main__":
-    for what in sys.argv[1:] or ["cases", "more", "data", "step"]:
-        {"cases": cases, "more": more, "data": data, "step": step}[what]()
+    for what in sys.argv[1:] or ["cases", "more", "data", "step", "tree", "tree_more"]:
+        {"cases": cases, "more": more, "data": data, "step": step, "tree": tree, "tree_more": tree_more}[what]()
