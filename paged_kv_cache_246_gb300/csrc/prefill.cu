@@ -125,9 +125,39 @@ struct Lay {
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 };
 
-using tc5::AB;
-using tc5::wait_or_abort;
-using tc5::warp_wait;
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
+                                              volatile uint32_t *abort_flag, int64_t where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1u;
+      record_error(PKV_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+
+// Warp-uniform verdict of a bounded wait performed by every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
+                                          volatile uint32_t *abort_flag, int64_t where) {
+  const bool got = wait_or_abort(bar, parity, abort_flag, where);
+  return __all_sync(0xffffffffu, got);
+}
+
+template <class T>
+struct AB;
+template <>
+struct AB<BF16> {
+  static constexpr int v = 1;
+};
+template <>
+struct AB<FP16> {
+  static constexpr int v = 0;
+};
+
 
 __device__ __forceinline__ uint32_t word4(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;

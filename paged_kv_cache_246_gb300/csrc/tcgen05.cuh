@@ -156,7 +156,7 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 
 // A bounded wait of a CTA whose roles stop together: false when it ran out
 // (PKV_ERR_TIMEOUT recorded, the abort flag raised) or another role raised the
-// flag.
+// flag.  (The prefill kernel has its own, with the report in line.)
 static __device__ __noinline__ void give_up(volatile uint32_t *abort_flag, int64_t where) {
   *abort_flag = 1u;
   record_error(PKV_ERR_TIMEOUT, where);

@@ -46,9 +46,10 @@
 // next.
 //
 // The weights enter P V as two 16-bit terms (hi + lo): a single rounded term
-// puts up to 2^-9 of a bf16 weight into the output, as much as the output's own
-// rounding.  Over an 8-bit cache P is fp16, whose 2^-12 does not show in a bf16
-// output: one term there, two for fp16 outputs.
+// puts up to 2^-8 of a bf16 weight into the output, as much as the output's own
+// rounding; two leave 2^-17.  Over an 8-bit cache P is fp16, whose 2^-11 does not
+// show in a bf16 output: one term there, two for fp16 outputs.  (One term for all:
+// four row tiles of 16384 keys 868 -> 750 us, one tree 55 -> 52.)
 // Over an 8-bit cache q.k runs on the codes as they are (kind::f8f6f4), each
 // query row scaled by a power of two to its own largest finite component and
 // split into E4M3 terms (two for the 8 bits of bf16, three for the 11 of fp16).
@@ -335,8 +336,12 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   // ---- this CTA's share of the units ----
   Walk walk;
   int64_t total = 0, u0, u1, per_share;
-  int shares, more_shares;  // the first more_shares shares have a unit more than per_share
-  auto share_start = [&](int i) -> int64_t { return i * per_share + min(i, more_shares); };
+  // more_shares of the shares, evenly spread, have a unit more than per_share: so
+  // the CTAs of equal row tiles begin at the same keys, and stay within L2's reach
+  // of each other (with the longer shares first four row tiles of 2 sequences
+  // read K and V 2.4 times from HBM)
+  int shares, more_shares;
+  auto share_start = [&](int i) -> int64_t { return i * per_share + i * more_shares / shares; };
   {
     int64_t *scan = reinterpret_cast<int64_t *>(misc + kScan);                 // [2][16 warps], by turns
     int turn = 0;

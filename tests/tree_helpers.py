@@ -89,8 +89,9 @@ def tolerance(s: TreeScene, out, spread, query=None):
     8-bit cache), which moves the output by as much of spread.  A score off by d
     moves its weight by 2 d of itself at most (its own and the sum's); d is that
     of fp32 sums of D products of at most max|q| max|k| (over an 8-bit cache also
-    the queries' 8-bit terms: off by 2^-12 of a component of a row, which holds
-    for two terms of 4 bits beside the row's largest), ALiBi's slope times
+    the queries' 8-bit terms: a row is scaled to a largest component of 2^7 or
+    more, its terms of 4 bits hold a component's 8 or 11 but for what lies below
+    half of E4M3's smallest step 2^-9, 2^-17 of the largest), ALiBi's slope times
     distance in fp32, and 2^x of the special-function unit (2^-22)."""
     half = torch.finfo(s.dtype).eps / 2
     weights = torch.finfo(FP).eps / 2 if s.fp8 else half
