@@ -79,7 +79,7 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
   a.tile_nodes = p.tile_nodes;
   a.row_tiles = p.row_tiles;
   a.item_units = p.item_units;
-  a.scale_log2 = g.scale * kLog2e * g.k_scale;
+  a.scale_log2 = std::max(g.scale * kLog2e * g.k_scale, tree::kTiniest);
   a.v_scale = g.v_scale;
   const bool bf = g.dtype == PKV_BF16;
   const CUtensorMapDataType dt =
@@ -125,9 +125,12 @@ cudaError_t launch_tree_decode(void *out, const void *query, const TreeBatch &t,
 }
 
 cudaError_t read_device_error_tree(unsigned long long *out) {
+  // both are cleared; the first one that holds something is told
+  unsigned long long other = 0;
   cudaError_t e = read_device_error_tree_bf16(out);
-  if (e != cudaSuccess || *out != 0) return e;
-  return read_device_error_tree_fp16(out);
+  if (e == cudaSuccess) e = read_device_error_tree_fp16(&other);
+  if (*out == 0) *out = other;
+  return e;
 }
 
 }  // namespace pkv

@@ -20,6 +20,9 @@ __device__ __forceinline__ bool nodes_of(const TreeBatch &t, int b, int &row, in
 // paged_attn_decode_tree (tree.cu): rows of a query tile, keys of a key tile.
 constexpr int BM = 128, BN = 128;
 
+// The least that scores are multiplied by: 0 would make NaN of the hidden ones' -infinity.
+constexpr float kTiniest = 0x1p-149f;
+
 struct Args {
   TreeBatch tb;
   uint16_t *out;

@@ -288,6 +288,15 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   using L = Lay<T, D, KV8>;
   using OPT = std::conditional_t<KV8, FP16, T>;  // operand type of P V
   constexpr bool TWO = !KV8 || std::is_same_v<T, FP16>;  // weights in two terms
+  // fp16 weights are held 2^5 times as large: one is off by up to half of the
+  // type's smallest step, 2^-25, so by 2^-30 of the row's largest, and 2^19 keys
+  // by no more than the output's rounding (unscaled, 2^14 keys).  A row's 64 keys
+  // then add up to 2^11 at most where its maximum is up to date, and to 2^15
+  // where that is 4 to 10 steps (of log2) late: then it moves.  (The lift costs
+  // nothing but with ALiBi, where scores rise tile by tile: 290 -> 303 us for 128
+  // contexts over an 8-bit cache.)
+  constexpr bool P16 = std::is_same_v<OPT, FP16>;
+  constexpr float kLift = P16 ? 5.f : 0.f, kLate = P16 ? 3.f : 8.f;
   constexpr int NV = L::NV, NKT = L::NKT, NVT = L::NVT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -878,7 +887,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         tc5::fence_after_sync();
         if (KV8 && k == 0) {
           // scores are there, so their queries' scale is
-          sl2 *= q_exp[si % L::NQ * BM + r];
+          sl2 = fmaxf(sl2 * q_exp[si % L::NQ * BM + r], kTiniest);
           if (!ALIBI) unit = sl2;
         }
         if (busy) {
@@ -988,17 +997,17 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
             if (m == -INFINITY) m = mx;
             unset = __any_sync(0xffffffffu, valid && m == -INFINITY);
           }
-          float ps = exps(m == -INFINITY ? 0.f : m * unit);
+          float ps = exps(m == -INFINITY ? 0.f : m * unit - kLift);
           if (__any_sync(0xffffffffu, valid && !(ps <= 32768.f))) {
             float alpha = 1.f;
             const float mx = largest();
-            const bool moved = valid && (mx - m) * unit > 8.f;
+            const bool moved = valid && (mx - m) * unit > kLate;
             if (moved) {
               alpha = fast_exp2((m - mx) * unit);
               m = mx;
             }
             tc5::tmem_st_wait();  // a first pass's weights are written before they are replaced
-            ps = exps(m == -INFINITY ? 0.f : m * unit);
+            ps = exps(m == -INFINITY ? 0.f : m * unit - kLift);
             l *= alpha;
             if (__any_sync(0xffffffffu, moved) && k > 0) {
               // the accumulator holds the product before this one once that has completed

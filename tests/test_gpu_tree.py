@@ -1,11 +1,13 @@
 """paged_attn_decode_tree against the fp64 oracle: sizes, masks and values
 where it can go wrong, bad indices, streams and graphs."""
+import dataclasses
+
 import pytest
 import torch
 
 import oracle as O
 from paged_kv_cache_246_gb300 import binding as B
-from sparse_helpers import codes
+from sparse_helpers import SCALE8, codes
 from tree_helpers import BF, FP, TreeScene, tolerance
 
 pytestmark = pytest.mark.gpu
@@ -280,6 +282,53 @@ def test_weights_keep_their_low_terms(dtype):
     d = 64 ** 0.5 * s.query.abs().max().double() * s.cache[0].abs().max().double() * 64 * 2.0 ** -24 + 2.0 ** -16
     tol = torch.finfo(dtype).eps / 2 * 1.01 * want.abs() + (2.0 ** -16 + 2 * d) * spread
     assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (FP, False), (BF, True), (FP, True)])
+def test_many_small_weights_beside_a_large_one(dtype, fp8):
+    """One key whose value is 0, and 2000 keys of weight 2^-26 beside it, whose
+    value is 1: together they are the output."""
+    s = TreeScene([2000] * 40, [2] * 40, 4, 4, 64, 16, dtype, fp8, seed=5)
+    rows = s.cache.view(2, -1, s.row)
+    one = 0x38                                      # 1.0 in E4M3
+    rows[0] = 0
+    rows[1] = one if fp8 else 1.0
+    for b in range(40):
+        rows[0, s.slot(b, 0)] = one if fp8 else 1.0
+        rows[1, s.slot(b, 0)] = 0
+    # 64 channels of q k / 8 are 18 nats
+    s.query[:] = 2.25 / (SCALE8 if fp8 else 1.0)
+    got = s.decode().cpu().double()
+    clean("small weights")
+    want, spread = s.expect()
+    # beside the usual, an fp16 weight is off by 2^-30 of the row's largest at most
+    tol = tolerance(s, want, spread) + 2002 * 2.0 ** -30 * (SCALE8 if fp8 else 1.0)
+    assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (FP, True)])
+def test_a_scale_that_vanishes(dtype, fp8, alibi):
+    """scale * k_scale below what fp32 holds: the scores are 0, not 0 * infinity
+    where they are hidden."""
+    s = TreeScene([70, 3], [9, 4], 4, 2, 64, 16, dtype, fp8, alibi=alibi, seed=6)
+    s.op = dataclasses.replace(s.op, scale=1e-44, k_scale=1e-30)
+    p = s.params()
+    p.scale, p.k_scale = 1e-44, 1e-30
+    got = s.decode(params=p).cpu().double()
+    clean("scale")
+    want, spread = s.expect()
+    assert ((got - want).abs() <= tolerance(s, want, spread)).all()
+
+
+def test_both_types_errors_are_cleared_together():
+    for dtype in (BF, FP):
+        s = TreeScene([20], [3], 2, 1, 64, 16, dtype)
+        s.tables[0, 0] = -3
+        s.decode()
+    torch.cuda.synchronize()
+    assert B.device_error()[0] == B.PKV_ERR_BOUNDS
+    clean("cleared")
 
 
 # ---- indices ---------------------------------------------------------------------
