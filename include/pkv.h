@@ -614,7 +614,8 @@ pkv_status kv_cache_write_rope_axes(void *query_out, int64_t query_out_stride, c
  * A tree whose parents are -1, 0, 1, ... is the run of tokens that
  * paged_attn_decode_multi takes.
  *
- *   out, query   [num_tokens][num_heads * head_size] elements
+ *   out, query   [num_tokens][num_heads * head_size] elements; they must not
+ *                overlap
  *   seq_lens     int32[num_seqs], at most max_seq_len and max_blocks_per_seq *
  *                block_size
  *   workspace    >= paged_attn_decode_tree_workspace_size(...) bytes of device
@@ -669,14 +670,16 @@ pkv_status paged_attn_tree_accept(int32_t *accepted, int32_t max_accepted, int32
  * were read before any is written.  The sequence then has seq_lens[b] - n_b +
  * num_accepted[b] tokens; what lies behind them is left as it was.
  *
- *   kv_caches    host array of num_layers device pointers, as kv_copy_blocks;
- *                num_layers <= 256
+ *   kv_caches    host array of num_layers device pointers, as kv_copy_blocks,
+ *                all different (their memory must not overlap); num_layers <=
+ *                256
  *   accepted     int32[num_seqs][max_accepted]: ascending node numbers below
  *                n_b, then negative numbers.  A path that breaks this, or a
  *                table entry out of range on its way, records PKV_ERR_BOUNDS
  *                and nothing of the sequence is moved.
  *   max_accepted 1 .. PKV_TREE_MAX_NODES
- * Positions of different sequences must not share cache slots.
+ * The nodes' positions, of one sequence or of several, must not share cache
+ * slots (context blocks may be shared).
  */
 pkv_status kv_commit_tree(void *const *kv_caches, int32_t num_layers, int64_t num_blocks,
                           const int32_t *accepted, int32_t max_accepted,

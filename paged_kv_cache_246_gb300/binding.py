@@ -658,19 +658,34 @@ def _pair_axes(axes: bytes) -> tuple:
     return (ctypes.c_uint8 * len(axes))(*axes), max(axes) + 1
 
 
+def _positions(positions: torch.Tensor, T: int) -> tuple:
+    """Axes, and elements from one axis to the next, of [axes, T] positions."""
+    if not isinstance(positions, _Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    if positions.dtype is not torch.int64 or positions.dim() != 2 or positions.shape[1] != T:
+        raise ValueError(f"positions must be {torch.int64} [axes, {T}], got {positions.dtype} "
+                         f"{list(positions.shape)}")
+    axes = positions.shape[0]
+    if positions.is_contiguous():
+        return axes, T
+    stride, one = positions.stride()
+    if (T > 1 and one != 1) or (axes > 1 and stride < T):
+        raise ValueError("each axis's positions must be contiguous, and behind the one before")
+    return axes, max(stride, T)
+
+
 def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
                              value: torch.Tensor, kv_cache: torch.Tensor, slot_mapping: torch.Tensor,
                              positions: torch.Tensor, cos_sin: torch.Tensor,
                              pair_axes: Sequence[int], params: AttnParams,
                              interleaved: bool = False, stream=None) -> None:
-    """kv_cache_write_rope with positions [num_axes, T]: pair i of a head turns
-    by the position on axis pair_axes[i] (rope_pair_axes makes the list)."""
+    """kv_cache_write_rope with positions [num_axes, T], whose rows may be slices
+    of wider ones: pair i of a head turns by the position on axis pair_axes[i]
+    (rope_pair_axes makes the list)."""
     dtype, cache_dtype, _, _, q_row, kv_row, block = _facts(params)
     nb = _is_cache(kv_cache, cache_dtype, block)
     T = _is(slot_mapping, "slot_mapping", torch.int64, 1)[0]
-    axes, n = _is(positions, "positions", torch.int64, 2)
-    if n != T:
-        raise ValueError("positions and slot_mapping sizes disagree")
+    axes, axis_stride = _positions(positions, T)
     max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
     axis_array, named = _pair_axes(bytes(pair_axes))
     if len(axis_array) != rot_dim // 2 or named > axes:
@@ -683,7 +698,7 @@ def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: 
     _call_on("kv_cache_write_rope_axes", stream,
              (kv_cache, query_out, query, key, value, slot_mapping, positions, cos_sin),
              query_out.data_ptr(), so, query.data_ptr(), sq, key.data_ptr(), sk, value.data_ptr(),
-             sv, T, positions.data_ptr(), T, axes, axis_array, cos_sin.data_ptr(), max_position, rot_dim,
+             sv, T, positions.data_ptr(), axis_stride, axes, axis_array, cos_sin.data_ptr(), max_position, rot_dim,
              1 if interleaved else 0, kv_cache.data_ptr(), nb, slot_mapping.data_ptr(),
              ctypes.byref(params))
 

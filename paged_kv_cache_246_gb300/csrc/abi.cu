@@ -691,6 +691,9 @@ pkv_status kv_commit_tree(void *const *kv_caches, int32_t num_layers, int64_t nu
     return PKV_ERR_INVALID;
   for (int l = 0; l < num_layers; ++l)
     if (!kv_caches[l] || !aligned(kv_caches[l], 16)) return PKV_ERR_INVALID;
+  // a cache named twice would be moved twice, at the same time
+  for (int l = 1; l < num_layers; ++l)
+    if (std::find(kv_caches, kv_caches + l, kv_caches[l]) != kv_caches + l) return PKV_ERR_INVALID;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   DeviceScope scope;
   if (scope.enter(s) != cudaSuccess) return PKV_ERR_CUDA;

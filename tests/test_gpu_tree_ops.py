@@ -102,6 +102,23 @@ def test_axes_bulk(dtype, D, heads, kv_heads, rot, inter, fp8):
     check_axes(s, 1111, rot, inter, True, B.rope_pair_axes((rot // 8, rot // 8, rot // 4)), 3)
 
 
+@pytest.mark.parametrize("T", [1, 30, 1000])
+def test_axes_rows_of_a_wider_tensor(T):
+    s = axes_scene(1100, FP, 64, 16, 4, 2, False, seed=T)
+    g, axes = torch.Generator().manual_seed(1), B.rope_pair_axes([8, 12, 12])
+    q, k, v = (torch.randn(T, w, generator=g).to(FP).to(DEV) for w in (s.H * s.D, s.row, s.row))
+    slots = torch.randperm(s.blocks * s.BS, generator=g)[:T].to(DEV)
+    wide = torch.full((3, 1200), -9, dtype=torch.int64)         # none of these is looked at
+    wide[:, 5:5 + T] = torch.randint(0, 200, (3, T), generator=g)
+    pos, table, outs = wide.to(DEV)[:, 5:5 + T], B.rope_table(200, 64, device=DEV), []
+    for positions in (pos, pos.contiguous()):
+        out, cache = torch.zeros_like(q), s.cache.to(DEV)
+        B.kv_cache_write_rope_axes(out, q, k, v, cache, slots, positions, table, axes, s.params())
+        clean("axes")
+        outs.append((out, cache))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_axes_in_place():
     s = axes_scene(600, BF, 128, 16, 8, 2, False, 2)
     check_axes(s, 500, 128, False, True, B.rope_pair_axes((16, 24, 24)), 3, in_place=True)

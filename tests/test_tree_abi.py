@@ -93,7 +93,7 @@ def test_accept_refusals(lib):
 
 
 def _commit(lib, p=None, **kw):
-    a = dict(caches=(ctypes.c_void_p * 2)(1 << 20, 1 << 20), layers=2, nb=4, acc=PTR, k=4, tables=PTR,
+    a = dict(caches=(ctypes.c_void_p * 2)(1 << 20, 1 << 21), layers=2, nb=4, acc=PTR, k=4, tables=PTR,
              mb=2, lens=PTR, cu=PTR, n=3)
     a.update(kw)
     return lib.kv_commit_tree(*a.values(), ctypes.byref(p or _p()), NUL)
@@ -106,6 +106,8 @@ def test_commit_refusals(lib):
                 dict(acc=NUL), dict(tables=NUL), dict(lens=NUL), dict(cu=NUL), dict(nb=0), dict(mb=0),
                 dict(n=-1), dict(n=65536), dict(k=0), dict(acc=ODD)):
         assert _commit(lib, **bad) == B.PKV_ERR_INVALID, bad
+    twice = (ctypes.c_void_p * 3)(1 << 20, 1 << 21, 1 << 20)    # a cache named twice
+    assert _commit(lib, caches=twice, layers=3) == B.PKV_ERR_INVALID
     assert _commit(lib, k=257) == B.PKV_ERR_UNSUPPORTED
     assert _commit(lib, _p(block_size=8)) == B.PKV_ERR_UNSUPPORTED
 
@@ -135,7 +137,9 @@ def test_binding_wants_what_it_says():
         B.kv_cache_write_rope_axes(q, q, kv, kv, cache, i64, positions, torch.zeros(8, 128), pair_axes, p)
 
     for bad in (dict(), dict(positions=i64), dict(pair_axes=axes[1:]), dict(pair_axes=()),
-                dict(pair_axes=(4,) * 64), dict(positions=i64.expand(2, 3).contiguous())):
+                dict(pair_axes=(4,) * 64), dict(positions=i64.expand(2, 3).contiguous()),
+                dict(positions=i64.expand(3, 3)), dict(positions=i64.expand(3, 3).contiguous().t()),
+                dict(positions=i64.expand(3, 3).int())):
         with pytest.raises(ValueError):     # the first: not on a GPU
             rope(**bad)
 
