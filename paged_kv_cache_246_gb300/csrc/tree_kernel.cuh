@@ -217,6 +217,19 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// Whether the phase with the given parity is through, without waiting for it.
+__device__ __forceinline__ bool mbar_look(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Registers of a thread at the launch (the most that 512 threads can have, and
 // what the kernels use), and in the warpgroups of warps 0-3, 4-7 and 8-15.
 // Taking more than the launch's pool holds would wait for ever, so launch()
@@ -332,7 +345,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
   if (warp == 1) tc5::tmem_alloc<512>(misc + kTmem);
   if constexpr (!KV8) {
     // rows that no copy writes (128 is no multiple of QPK): finite once and for all
-    for (int i = threadIdx.x; i < 2 * L::NREG * (BM - tile_rows) * 8; i += kThreads) {
+    for (int i = threadIdx.x; i < L::NQ * L::NREG * (BM - tile_rows) * 8; i += kThreads) {
       const int per = (BM - tile_rows) * 8;
       *reinterpret_cast<uint4 *>(smem + L::OFF_Q + (i / per) * L::REG + tile_rows * 128 +
                                  (i % per) * 16) = make_uint4(0, 0, 0, 0);
@@ -639,6 +652,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
     // registers (one lane on its own: 109 cycles a product against 64).
     Walk walk_q = walk;
     int tq = 0, jq = 0, nq = 0, segs = 0;  // scores: next tile, its place in its segment of nq
+    bool keys = false;  // its keys have been seen to be there
     auto scores = [&]() -> bool {
       if (jq == nq) {
         Seg s;
@@ -652,7 +666,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         ++segs;
       }
       const int sk = tq % NKT;
-      if (!warp_wait(&bars[L::B_K + sk], (tq / NKT) & 1, abort_flag, where)) return false;
+      if (!keys && !warp_wait(&bars[L::B_K + sk], (tq / NKT) & 1, abort_flag, where)) return false;
       tc5::fence_after_sync();
       const uint32_t sb = tmem + (tq & 1) * 128;
       if (one) {
@@ -694,8 +708,20 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           if (n == 0) return;
         }
         const int t = u - 2, sv = t % NV, buf = t & 1;
-        if (!warp_wait(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
-        if (!warp_wait(&bars[L::B_P + buf], (t / 2) & 1, abort_flag, where)) return;
+        // A wait costs this warp 120 cycles even where it is over: one look at the
+        // three barriers of the step, a lane at each, and waits for those that were
+        // not through (heads of 64 148 -> 145 us; over an 8-bit cache, whose weights
+        // come later, 199 -> 205).
+        uint32_t through = 0;
+        if constexpr (!KV8) {
+          uint64_t *bar = &bars[lane == 0 ? L::B_VG + sv : lane == 1 ? L::B_P + buf : L::B_K + tq % NKT];
+          const uint32_t parity = (lane == 0 ? t / NV : lane == 1 ? t / 2 : tq / NKT) & 1;
+          through = __ballot_sync(0xffffffffu, mbar_look(bar, parity));
+          __syncwarp();
+          keys = through & 4u;
+        }
+        if (!(through & 1u) && !warp_wait(&bars[L::B_VG + sv], (t / NV) & 1, abort_flag, where)) return;
+        if (!(through & 2u) && !warp_wait(&bars[L::B_P + buf], (t / 2) & 1, abort_flag, where)) return;
         tc5::fence_after_sync();
         if (one) {
 #pragma unroll
