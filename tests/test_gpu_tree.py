@@ -1,6 +1,9 @@
 """paged_attn_decode_tree against the fp64 oracle: sizes, masks and values
 where it can go wrong, bad indices, streams and graphs."""
 import dataclasses
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -470,6 +473,44 @@ def test_graph_replays_new_trees(fp8):
     assert n.lens.max() <= n.wide * n.BS
     check(n, got=out, rows={0, 29, 30, 31, 32, 42})
     del b
+
+
+_FIRST = """
+import sys
+sys.path[:0] = sys.argv[1:]
+import torch
+from paged_kv_cache_246_gb300 import binding as B
+from tree_helpers import BF, TreeScene, tolerance
+s = TreeScene([500, 20], [7, 3], 8, 2, dtype=BF)
+p, t = s.params(), [x.to("cuda:0") for x in (s.query, s.cache, s.tables, s.lens, s.cu, s.parents)]
+out = torch.zeros_like(t[0])
+ws = torch.empty(max(16, B.paged_attn_decode_tree_workspace_size(2, 7, 507, p)), dtype=torch.uint8, device="cuda:0")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    B.paged_attn_decode_tree(out, *t, 7, 507, p, ws)
+graph.replay()
+torch.cuda.synchronize()
+want, spread = s.expect()
+assert B.device_error()[0] == B.PKV_OK
+assert ((out.cpu().double() - want).abs() <= tolerance(s, want, spread)).all()
+print("captured")
+"""
+
+
+def test_the_first_call_of_a_process_is_captured():
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", _FIRST, os.path.dirname(here), here], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sequences_that_share_context_blocks(fp8):
+    s = TreeScene([160, 160, 165], [9, 20, 3], 8, 2, fp8=fp8, seed=8)
+    s.tables[1, :10] = s.tables[0, :10]
+    s.tables[2, :10] = s.tables[0, :10]
+    check(s)
 
 
 def test_workspace_is_refused_when_too_small():
