@@ -36,7 +36,12 @@
 //               zeroed, values that are not finite are zeroed and the segment
 //               is marked, since 0 * NaN in the product would reach rows that
 //               do not see them (the rows that do get them back at the end).
-//               Over an 8-bit cache they also widen the V codes to fp16.
+//               Over an 8-bit cache they also widen the V codes to fp16.  (In the
+//               other tiles all rows see an infinite value, whose channel then
+//               is not finite in any of them; which it is, since the two terms of a
+//               weight make inf - inf and 0 * inf of it, is looked up at the
+//               segment's end.  Looking through all tiles on the way costs heads of
+//               64 8 %: 145 -> 157 us.)
 //   warps 8-11, 12-15  softmax groups A and B: thread r owns row r.
 // Of every key tile group A takes the first 64 keys and B the last, each with
 // its own running maximum, sum and accumulator; the two are merged at the
@@ -261,9 +266,92 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// What the look through V took out of it goes back into the rows that see it:
-// every visible value that is not finite, in the tiles that rows see in part,
-// is added to the row's elements as they stand in memory.  Rare.
+// Whether any of N elements is not finite.
+template <class T, int N>
+__device__ __forceinline__ bool any_not_finite(const void *row) {
+  uint4 u[N / 8];
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) u[i] = __ldg(reinterpret_cast<const uint4 *>(row) + i);
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i)
+    any |= not_finite<T>(u[i].x) | not_finite<T>(u[i].y) | not_finite<T>(u[i].z) | not_finite<T>(u[i].w);
+  return any != 0;
+}
+
+// The key (half 0) or the value (half 1) at position pos, in block pb, which is in range.
+__device__ __forceinline__ const uint8_t *cache_row(const Args &a, const Seg &s, int half, int pb,
+                                                    int pos, int D, int elem_bytes) {
+  return a.cache + (((half * a.num_blocks + pb) * a.BS + pos % a.BS) * a.row_elems +
+                    static_cast<int64_t>(s.g) * D) * elem_bytes;
+}
+
+// Values that are not finite, and the rows that see them.  Any weight times
+// infinity is infinity, but for the weight 0 of a score of -infinity, which makes
+// NaN.  Such a score's key is not finite either (a query that is not finite has no
+// finite scores, and its row is NaN as it is), and a key that is not finite has no
+// finite score: so where key and value both are not, all rows that see them are NaN
+// in the value's channel.
+
+// The tiles that all rows see whole: a value of theirs that is not finite decides
+// its channel in every row.  Called by a warp, each lane with its row, where
+// some row's accumulator is not finite; the channels are c0 .. c0 + D / 2 - 1.  A
+// tile takes 5 us, 22 where all its values are infinite: the second that the
+// other roles wait is some 5 million such keys of one segment.
+template <class T, int D>
+__device__ __noinline__ void set_not_finite(const Args &a, const Seg &seg, int c0, bool write,
+                                            uint16_t *out, float *part) {
+  constexpr int COLS = D / 2, WORDS = COLS / 32;
+  const int32_t *trow = a.block_tables + static_cast<int64_t>(seg.b) * a.max_blocks_per_seq;
+  const int start = seg.s.kv_start + seg.j0 * BN;
+  const int end = start + min(seg.calm_to(), seg.n) * BN;
+  uint32_t up[WORDS] = {}, down[WORDS] = {};  // channels that hold +infinity, -infinity (NaN: both)
+#pragma unroll 2
+  for (int pos = start + max(seg.calm_from(a), 0) * BN + (threadIdx.x & 31); pos < end; pos += 32) {
+    const int pb = __ldg(trow + pos / a.BS);
+    if (pb < 0 || pb >= a.num_blocks) continue;
+    const uint8_t *row = cache_row(a, seg, 1, pb, pos, D, 2) + c0 * 2;
+    if (!any_not_finite<T, COLS>(row)) continue;
+    const bool key_too = any_not_finite<T, D>(cache_row(a, seg, 0, pb, pos, D, 2));
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w)
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row) + 4 * w + i);
+        uint32_t p = 0, n = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t e = word_of(u, c / 2) >> (c % 2 * 16) & 0xffffu;
+          const bool bad = (e & T::kInf) == T::kInf, nan = key_too || (e & 0x7fffu) != T::kInf;
+          if (bad && (nan || e < 0x8000u)) p |= 1u << c;
+          if (bad && (nan || e >= 0x8000u)) n |= 1u << c;
+        }
+        up[w] |= p << (8 * i);
+        down[w] |= n << (8 * i);
+      }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    up[w] = __reduce_or_sync(0xffffffffu, up[w]);
+    down[w] = __reduce_or_sync(0xffffffffu, down[w]);
+#pragma unroll 1
+    for (int e = 0; write && e < 32; ++e) {
+      const bool p = up[w] >> e & 1, n = down[w] >> e & 1;
+      if (!p && !n) continue;
+      const float v = p && n ? __int_as_float(0x7fffffff) : p ? INFINITY : -INFINITY;
+      const int c = c0 + 32 * w + e;
+      if (out)
+        out[c] = static_cast<uint16_t>(T::from_f2(v, 0.f));
+      else
+        part[static_cast<int64_t>(c / 4) * 512 + c % 4] = v;
+    }
+  }
+}
+
+// The tiles that rows see in part: what the look through V took out of them goes
+// back into the rows that see it; every visible value that is not finite is added
+// to the row's elements as they stand in memory.  Rare, as the one above.
 template <class T, int D, bool KV8>
 __device__ __noinline__ void add_not_finite(const Args &a, const Seg &seg, int lo, int c0, int cols,
                                             const uint32_t *mask, uint16_t *out, float *part) {
@@ -271,14 +359,20 @@ __device__ __noinline__ void add_not_finite(const Args &a, const Seg &seg, int l
   auto key = [&](int pos) {
     const int pb = __ldg(trow + pos / a.BS);
     if (pb < 0 || pb >= a.num_blocks) return;
-    const int64_t at = ((a.num_blocks + pb) * a.BS + pos % a.BS) * a.row_elems + seg.g * D + c0;
+    const uint8_t *row = cache_row(a, seg, 1, pb, pos, D, KV8 ? 1 : 2);
+    bool key_too = false, known = KV8;
     for (int d = 0; d < cols; ++d) {
       float v;
       if constexpr (KV8)
-        v = (a.cache[at + d] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
+        v = (row[c0 + d] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
       else
-        v = T::to_f(reinterpret_cast<const uint16_t *>(a.cache)[at + d]);
+        v = T::to_f(reinterpret_cast<const uint16_t *>(row)[c0 + d]);
       if (fabsf(v) < INFINITY) continue;
+      if (!known) {
+        key_too = any_not_finite<T, D>(cache_row(a, seg, 0, pb, pos, D, 2));
+        known = true;
+      }
+      if (key_too) v = __int_as_float(0x7fffffff);
       if (out)
         out[c0 + d] = static_cast<uint16_t>(T::from_f2(T::to_f(out[c0 + d]) + v, 0.f));
       else
@@ -1094,6 +1188,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       const int col0 = x * COLS;
       if (busy) {
         const uint32_t ob = tmem + lane_base + 256 + col0;
+        float bad[4] = {0.f, 0.f, 0.f, 0.f};  // NaN: some element is not finite
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; ++c) {
           uint32_t o[32], o1[32];
@@ -1103,6 +1198,10 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+          if constexpr (!KV8) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(o[e]), 0.f, bad[e & 3]);
+          }
           if (valid && whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(out + col0 + 32 * c);
             uint32_t w[16];
@@ -1121,6 +1220,13 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
         }
         if (!whole && x == 0 && valid)
           a.part_ml[static_cast<int64_t>(at) * BM + r] = make_float2(top, l);
+        if constexpr (!KV8) {
+          // of the rows with a finite score and no NaN or +infinity among them (the
+          // others are NaN, or 0 here, as the formula says)
+          const bool there = valid && l > 0.f && l < INFINITY;
+          if (__any_sync(0xffffffffu, there && !(bad[0] + bad[1] + bad[2] + bad[3] == 0.f)))
+            set_not_finite<T, D>(a, s, col0, there, whole ? out : nullptr, part);
+        }
         if (flags[si % kFlagSlots] && valid)
           add_not_finite<T, D, KV8>(a, s, lo, col0, COLS, mask, whole ? out : nullptr, part);
       }
@@ -1245,7 +1351,8 @@ __global__ void __launch_bounds__(8 * D / 4) combine_kernel(const Args a) {
       o[3] += scaled(p[i].w, w);
     }
   }
-  const float inv = a.v_scale / l;
+  // nothing but -infinity is NaN, whatever the values
+  const float inv = l > 0.f ? a.v_scale / l : __int_as_float(0x7fffffff);
   const int64_t row = static_cast<int64_t>(s.row + node) * a.H + rec.y * a.QPK + r % a.QPK;
   *reinterpret_cast<uint2 *>(a.out + row * D + d4 * 4) =
       make_uint2(T::from_f2(o[0] * inv, o[1] * inv), T::from_f2(o[2] * inv, o[3] * inv));
