@@ -1188,19 +1188,35 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
       const int col0 = x * COLS;
       if (busy) {
         const uint32_t ob = tmem + lane_base + 256 + col0;
-        float bad[4] = {0.f, 0.f, 0.f, 0.f};  // NaN: some element is not finite
+        // sums of 0 times the elements: NaN where one is not finite.  (Packed, as the merge
+        // itself: ALiBi's kernels feel every instruction here, 64 contexts 594 us without the
+        // look, 608 so, 650 with both in single ones.  An 8-bit cache needs no look, and
+        // its merge is faster in single ones, 197 against 205 us for 128 contexts.)
+        unsigned long long bad = 0ull;
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; ++c) {
           uint32_t o[32], o1[32];
           tc5::tmem_ld32(ob + 32 * c, o);
           tc5::tmem_ld32(ob + 128 + 32 * c, o1);
           tc5::tmem_ld_wait();
+          if constexpr (KV8) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
-          if constexpr (!KV8) {
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) bad[e & 3] = fmaf(__uint_as_float(o[e]), 0.f, bad[e & 3]);
+            for (int e = 0; e < 32; e += 2) {
+              auto pair = [&](const uint32_t *v) {
+                return f2pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              };
+              const unsigned long long both =
+                  ffma2(pair(o1), f2pack(f1, f1), fmul2(pair(o), f2pack(f0, f0)));
+              bad = ffma2(both, 0ull, bad);
+              float even, odd;
+              f2unpack(both, even, odd);
+              o[e] = __float_as_uint(even);
+              o[e + 1] = __float_as_uint(odd);
+            }
           }
           if (valid && whole) {
             uint4 *dst = reinterpret_cast<uint4 *>(out + col0 + 32 * c);
@@ -1224,7 +1240,7 @@ tree_tc_kernel(const Args a, const __grid_constant__ CUtensorMap qmap,
           // of the rows with a finite score and no NaN or +infinity among them (the
           // others are NaN, or 0 here, as the formula says)
           const bool there = valid && l > 0.f && l < INFINITY;
-          if (__any_sync(0xffffffffu, there && !(bad[0] + bad[1] + bad[2] + bad[3] == 0.f)))
+          if (__any_sync(0xffffffffu, there && ((bad & 0x7fffffff7fffffffull) != 0)))
             set_not_finite<T, D>(a, s, col0, there, whole ? out : nullptr, part);
         }
         if (flags[si % kFlagSlots] && valid)
