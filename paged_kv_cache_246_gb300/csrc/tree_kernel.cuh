@@ -5,10 +5,15 @@
 // context's length plus its depth.
 //
 // Rows are (node, query head of the KV group) pairs, node by node, in tiles of
-// 128: 128 / QPK nodes each.  The step reads the context's K and V once per
-// KV head, so up to a tile's rows it is bound by HBM (2 flops per row and byte
-// against 281 of the card); mma.sync tiles of 16 rows, as the other decodes
-// use, would read K and V from L2 once per tile.
+// 128: 128 / QPK nodes each.  The step reads the context's K and V once per KV
+// head and row tile.  Of a 16-bit cache a key is 4 D bytes and, with both terms of
+// the weights (below), 6 D flops a row: 192 flops a byte for a full tile, against
+// 281 of the card, so one row tile is bound by HBM, and two by the products.  Of an
+// 8-bit cache it is 2 D bytes and the time of 4 D 16-bit flops for bf16 queries (two
+// E4M3 terms of q at twice that rate, one of the weights: 256 a byte), of 7 D for
+// fp16 ones (three and two: 448, so HBM binds tiles of up to 80 rows).  mma.sync
+// tiles of 16 rows, as the other decodes use, would read K and V from L2 once per
+// tile.
 //
 // CTA = one per SM, persistent.  The work is the list of units (row tile,
 // sequence, KV head, 128-key tile), in this order; every CTA takes an equal,
@@ -52,9 +57,13 @@
 //
 // The weights enter P V as two 16-bit terms (hi + lo): a single rounded term
 // puts up to 2^-8 of a bf16 weight into the output, as much as the output's own
-// rounding; two leave 2^-17.  Over an 8-bit cache P is fp16, whose 2^-11 does not
-// show in a bf16 output: one term there, two for fp16 outputs.  (One term for all:
-// four row tiles of 16384 keys 868 -> 750 us, one tree 55 -> 52.)
+// rounding; two leave 2^-17.  (One term for all: four row tiles of 16384 keys
+// 868 -> 750 us, one tree 55 -> 52.)  Over an 8-bit cache P is fp16: two terms
+// for fp16 outputs, one, 2^-11 of a weight, for bf16 outputs.  It shows a little
+// beside their rounding of 2^-8: 128 contexts of 100 .. 4096 tokens lie 1.672e-3 of
+// the output's norm off the 64-bit definition, with two terms 1.660e-3 as 32-bit
+// arithmetic with one rounding does; but the second takes 197 -> 230 us there, 366 -> 398
+// for 64 contexts of 4096 .. 16384.
 // Over an 8-bit cache q.k runs on the codes as they are (kind::f8f6f4), each
 // query row scaled by a power of two to its own largest finite component and
 // split into E4M3 terms (two for the 8 bits of bf16, three for the 11 of fp16).
