@@ -25,9 +25,13 @@ static Plan plan(int num_seqs, int max_nodes, int max_seq_len, const Geometry &g
   // What an item costs beside its tiles, in tiles: the softmax of its first and
   // last ones, the accumulators' way out, instructions that are not at hand
   // (3000 to 6000 cycles, a tile 2000).  These units come before the item's
-  // tiles; without them a CTA whose share is short contexts took 1.6 times the
-  // others' time (128 contexts of 100 .. 4096 tokens, 8-bit cache: 290 us
-  // with 0, 232 with 5; 16384 x 64: 448 and 433).
+  // tiles, so that a CTA whose share is short contexts has no more to do than the
+  // others.  With 1 / 2 / 3 / 4 / 5 / 6 / 8 units (us), 16-bit cache: one context of
+  // 32768 59 / 58 / 57 / 55 / 55 / 55 / 55, 64 of 4096 .. 16384 448 / 445 / 441 / 437 /
+  // 434 / 435 / 431, 128 of 100 .. 4096 242 / 226 / 222 / 218 / 217 / 217 / 221, heads of 64
+  // 145 / 145 / 146 / 145 / 146 / 146 / 147: equal within a hundredth from 4 to 6.  8-bit
+  // cache: 128 contexts 251 / 235 / 221 / 210 / 201 / 197 / 195, 64 378 / 375 / 371 / 369 / 369 /
+  // 365 / 364; fp16 queries 298 / 283 / 283 / 290 / 293 / 296 / 304.
   p.item_units = tiles <= 2 ? 0 : g.fp8 ? 6 : 4;
   const int64_t items = static_cast<int64_t>(num_seqs) * g.KVH * p.row_tiles;
   const int64_t units = p.item_units == 0 ? items : items * (tiles + p.item_units);
