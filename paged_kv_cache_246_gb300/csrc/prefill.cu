@@ -125,40 +125,6 @@ struct Lay {
   static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
-                                              volatile uint32_t *abort_flag, int64_t where) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1u;
-      record_error(PKV_ERR_TIMEOUT, where);
-      return false;
-    }
-  }
-}
-
-// Warp-uniform verdict of a bounded wait performed by every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
-                                          volatile uint32_t *abort_flag, int64_t where) {
-  const bool got = wait_or_abort(bar, parity, abort_flag, where);
-  return __all_sync(0xffffffffu, got);
-}
-
-template <class T>
-struct AB;
-template <>
-struct AB<BF16> {
-  static constexpr int v = 1;
-};
-template <>
-struct AB<FP16> {
-  static constexpr int v = 0;
-};
-
-
 __device__ __forceinline__ uint32_t word4(const uint4 &v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -314,7 +280,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         constexpr int N8K = L::N8K, N8V = L::N8V;
         const int sk8 = j % N8K, sv8 = j % N8V;
         if (j >= N8K &&
-            !warp_wait(&bars[L::B_E8K + sk8], ((j / N8K) - 1) & 1, abort_flag, where))
+            !tc5::warp_wait<true>(&bars[L::B_E8K + sk8], ((j / N8K) - 1) & 1, abort_flag, where))
           break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[L::B_K8F + sk8], L::TILE8);
         __syncwarp();
@@ -323,7 +289,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
                       &bars[L::B_K8F + sk8], 0, g, coord, 0);
         jk = j + 1;
         if (j >= N8V &&
-            !warp_wait(&bars[L::B_E8V + sv8], ((j / N8V) - 1) & 1, abort_flag, where))
+            !tc5::warp_wait<true>(&bars[L::B_E8V + sv8], ((j / N8V) - 1) & 1, abort_flag, where))
           break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[L::B_V8F + sv8], L::TILE8);
         __syncwarp();
@@ -333,7 +299,8 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         jv = j + 1;
       } else {
         const int sk = j % NK;
-        if (j >= NK && !warp_wait(&bars[L::B_EK + sk], ((j / NK) - 1) & 1, abort_flag, where))
+        if (j >= NK &&
+            !tc5::warp_wait<true>(&bars[L::B_EK + sk], ((j / NK) - 1) & 1, abort_flag, where))
           break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[L::B_KF + sk], L::TILE);
         __syncwarp();
@@ -344,7 +311,8 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         }
         jk = j + 1;
         const int sv = j % NV;
-        if (j >= NV && !warp_wait(&bars[L::B_EV + sv], ((j / NV) - 1) & 1, abort_flag, where))
+        if (j >= NV &&
+            !tc5::warp_wait<true>(&bars[L::B_EV + sv], ((j / NV) - 1) & 1, abort_flag, where))
           break;
         if (lane == 0) mbar_arrive_expect_tx(&bars[L::B_VF + sv], L::TILE);
         __syncwarp();
@@ -366,8 +334,8 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     // cycle this thread spends outside an MMA is a cycle the tensor core may
     // idle.  Waits are scalar; there is no warp-wide synchronisation here.
     // QK over an fp8 cache: kind::f8f6f4, E4M3 query terms x E4M3 key codes
-    constexpr uint32_t ID_QK = tc5::idesc_f16(KV8 ? 0 : AB<OPT>::v, 0, BM, BN);
-    constexpr uint32_t ID_PV = tc5::idesc_f16(AB<OPT>::v, 1, BM, D);
+    constexpr uint32_t ID_QK = tc5::idesc_f16(KV8 ? 0 : tc5::AB<OPT>::v, 0, BM, BN);
+    constexpr uint32_t ID_PV = tc5::idesc_f16(tc5::AB<OPT>::v, 1, BM, D);
     // Operand descriptors are built once; an MMA only adds a compile-time
     // offset (in 16-byte units) to a base.  8-bit operands are K-major rows
     // of D bytes: 128-byte swizzle for D = 128, 64-byte for D = 64.
@@ -385,7 +353,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     int k_ready = -1;  // highest key tile known to have landed
     auto need_k = [&](int j) -> bool {
       if (j <= k_ready) return true;
-      if (!wait_or_abort(&bars[KFT + j % NKT], (j / NKT) & 1, abort_flag, where))
+      if (!tc5::wait_or_abort<true>(&bars[KFT + j % NKT], (j / NKT) & 1, abort_flag, where))
         return false;
       tc5::fence_after_sync();
       k_ready = j;
@@ -413,8 +381,9 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       }
       tc5::commit(&bars[L::B_SF + x]);
     };
-    bool ok = wait_or_abort(&bars[QCONV ? L::B_Q2 : L::B_Q], 0, abort_flag, where);
-    if (QCONV && ok && qt[1].rows > 0) ok = wait_or_abort(&bars[L::B_Q2 + 1], 0, abort_flag, where);
+    bool ok = tc5::wait_or_abort<true>(&bars[QCONV ? L::B_Q2 : L::B_Q], 0, abort_flag, where);
+    if (QCONV && ok && qt[1].rows > 0)
+      ok = tc5::wait_or_abort<true>(&bars[L::B_Q2 + 1], 0, abort_flag, where);
     if (ok && ntiles > 0) {
       ok = need_k(0);
       if (ok) {
@@ -427,7 +396,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     // PV of tile x for key tile j, then the look-ahead QK of tile x
     auto step = [&](int x, int j, int sv, int &pf) -> bool {
       if (active(x, j)) {
-        if (!wait_or_abort(&bars[L::B_PF + x], pf & 1, abort_flag, where)) return false;
+        if (!tc5::wait_or_abort<true>(&bars[L::B_PF + x], pf & 1, abort_flag, where)) return false;
         tc5::fence_after_sync();
         const uint32_t pb = tmem + x * 128;
         const uint32_t ob = tmem + 256 + x * 128;
@@ -448,7 +417,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     };
     for (int j = 0; ok && j < ntiles; ++j) {
       const int sv = j % NV;
-      if (!wait_or_abort(&bars[L::B_VF + sv], (j / NV) & 1, abort_flag, where)) break;
+      if (!tc5::wait_or_abort<true>(&bars[L::B_VF + sv], (j / NV) & 1, abort_flag, where)) break;
       // Positions past the sequence end inside its last cache block hold
       // whatever the cache holds there (possibly non-finite); their P is
       // exactly 0, but 0 * NaN is NaN, so those V rows are zeroed before the
@@ -494,9 +463,11 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     };
     auto widen = [&](int j) -> bool {
       const int s = j % NV, s8 = j % L::N8V;
-      if (!warp_wait(&bars[L::B_V8F + s8], (j / L::N8V) & 1, abort_flag, where)) return false;
+      if (!tc5::warp_wait<true>(&bars[L::B_V8F + s8], (j / L::N8V) & 1, abort_flag, where))
+        return false;
       // the fp16 stage is free once the MMAs of the tile that used it are done
-      if (j >= NV && !warp_wait(&bars[L::B_EV + s], ((j / NV) - 1) & 1, abort_flag, where))
+      if (j >= NV &&
+          !tc5::warp_wait<true>(&bars[L::B_EV + s], ((j / NV) - 1) & 1, abort_flag, where))
         return false;
       const uint8_t *src = smem + L::OFF_STG + (L::N8K + s8) * L::TILE8;
       uint8_t *dst = smem + L::OFF_V + s * L::TILE;
@@ -564,7 +535,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       // strand a warp).
       constexpr int CH = L::TILE / 16 / 128;  // 16-byte chunks per thread
       int e = 0;
-      ok = warp_wait(&bars[L::B_Q], 0, abort_flag, where);
+      ok = tc5::warp_wait<true>(&bars[L::B_Q], 0, abort_flag, where);
       uint8_t *qt8 = smem + L::OFF_Q + x * L::TILE;
       const uint4 *q4 = reinterpret_cast<const uint4 *>(qt8);
       const int tid = (warp & 3) * 32 + lane;
@@ -597,7 +568,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
         am = __reduce_max_sync(0xffffffffu, am);
         if (lane == 0) misc[8 + x * 4 + (warp & 3)] = am;
         mbar_arrive(&bars[L::B_QS + x]);
-        ok = warp_wait(&bars[L::B_QS + x], 0, abort_flag, where);
+        ok = tc5::warp_wait<true>(&bars[L::B_QS + x], 0, abort_flag, where);
       }
       if (ok) {
         am = max(max(misc[8 + x * 4], misc[9 + x * 4]), max(misc[10 + x * 4], misc[11 + x * 4]));
@@ -634,7 +605,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
     const int n = t.j1 - t.j0;
     for (int k = 0; ok && k < n; ++k) {
       const int j = ALIBI ? t.j1 - 1 - k : t.j0 + k;  // this tile's k-th key tile
-      if (!warp_wait(&bars[L::B_SF + x], k & 1, abort_flag, where)) {
+      if (!tc5::warp_wait<true>(&bars[L::B_SF + x], k & 1, abort_flag, where)) {
         ok = false;
         break;
       }
@@ -774,7 +745,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       l = l * alpha + ps;
       if (__any_sync(0xffffffffu, resc)) {
         // O_x holds PV of the previous key tile once it has completed
-        if (!warp_wait(&bars[L::B_O + x], (k - 1) & 1, abort_flag, where)) {
+        if (!tc5::warp_wait<true>(&bars[L::B_O + x], (k - 1) & 1, abort_flag, where)) {
           ok = false;
           break;
         }
@@ -793,7 +764,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap qmap,
       tc5::fence_before_sync();
       mbar_arrive(&bars[L::B_PF + x]);
     }
-    if (ok && n > 0 && warp_wait(&bars[L::B_O + x], (n - 1) & 1, abort_flag, where)) {
+    if (ok && n > 0 && tc5::warp_wait<true>(&bars[L::B_O + x], (n - 1) & 1, abort_flag, where)) {
       tc5::fence_after_sync();
       const float inv = l > 0.f ? (KV8 ? a.v_scale : 1.f) / l : 0.f;
       const bool valid = row < t.rows;

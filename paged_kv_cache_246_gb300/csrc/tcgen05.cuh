@@ -156,11 +156,13 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 
 // A bounded wait of a CTA whose roles stop together: false when it ran out
 // (PKV_ERR_TIMEOUT recorded, the abort flag raised) or another role raised the
-// flag.  (The prefill kernel has its own, with the report in line.)
+// flag.  IN_LINE: the report stands where the wait does, as the prefill kernel has it;
+// the tree kernel, whose instructions do not all fit the cache, calls it.
 static __device__ __noinline__ void give_up(volatile uint32_t *abort_flag, int64_t where) {
   *abort_flag = 1u;
   record_error(PKV_ERR_TIMEOUT, where);
 }
+template <bool IN_LINE = false>
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
                                               volatile uint32_t *abort_flag, int64_t where) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -169,16 +171,22 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity,
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > kWaitLimitNs) {
-      give_up(abort_flag, where);
+      if constexpr (IN_LINE) {
+        *abort_flag = 1u;
+        record_error(PKV_ERR_TIMEOUT, where);
+      } else {
+        give_up(abort_flag, where);
+      }
       return false;
     }
   }
 }
 
 // Warp-uniform verdict of a bounded wait performed by every lane.
+template <bool IN_LINE = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
                                           volatile uint32_t *abort_flag, int64_t where) {
-  const bool got = wait_or_abort(bar, parity, abort_flag, where);
+  const bool got = wait_or_abort<IN_LINE>(bar, parity, abort_flag, where);
   return __all_sync(0xffffffffu, got);
 }
 
