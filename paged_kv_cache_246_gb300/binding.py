@@ -687,6 +687,9 @@ def kv_cache_write_rope_axes(query_out: torch.Tensor, query: torch.Tensor, key: 
     T = _is(slot_mapping, "slot_mapping", torch.int64, 1)[0]
     axes, axis_stride = _positions(positions, T)
     max_position, rot_dim = _is(cos_sin, "cos_sin", torch.float32, 2)
+    if type(pair_axes) not in (tuple, list, bytes):
+        # bytes() of a number are as many zeros, of an array its memory
+        pair_axes = tuple(map(operator.index, pair_axes))
     axis_array, named = _pair_axes(bytes(pair_axes))
     if len(axis_array) != rot_dim // 2 or named > axes:
         raise ValueError(f"pair_axes must name one of the {axes} axes for each of the "
