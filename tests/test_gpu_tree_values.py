@@ -1,10 +1,15 @@
 """paged_attn_decode_tree over values that are not finite deep in the context,
 against the fp64 oracle: what a row sees goes into it as the formula says,
 wherever the key lies and however small its weight."""
+import random
+
 import pytest
 import torch
 
+import oracle as O
+
 from paged_kv_cache_246_gb300 import binding as B
+from sparse_helpers import SCALE8
 from test_gpu_tree import DEV, check, clean, within
 from tree_helpers import BF, FP, TreeScene, tolerance
 
@@ -135,3 +140,75 @@ def test_not_finite_codes_in_the_context():
     check(s)
     torch.cuda.synchronize(DEV)
     assert B.device_error()[0] == B.PKV_OK
+
+
+def by_class(s: TreeScene):
+    """The formula, what is not finite said by cases: a row whose scores hold a
+    NaN or +infinity, or nothing but -infinity, is NaN; an infinite value makes
+    its channel infinite in the rows that see it, NaN where the weight is 0 (a
+    score of -infinity) or the other infinity is there too."""
+    out = torch.full((s.rows, s.H, s.D), float("nan"), dtype=torch.float64)
+    cache = s.cache.view(2, -1, s.KVH, s.D)
+    cache = cache.view(torch.float8_e4m3fn).double() * float(torch.tensor(SCALE8)) if s.fp8 else cache.double()
+    for b, (n, ctx) in enumerate(zip(s.nodes, s.ctx)):
+        if n == 0:
+            continue
+        slots = torch.tensor([s.slot(b, j) for j in range(ctx + n)])
+        depth = torch.tensor(s.depths(b))
+        place = torch.cat([torch.arange(ctx), ctx + depth])
+        ago = place - (ctx + depth)[:, None]
+        seen = torch.zeros(n, ctx + n, dtype=torch.bool)
+        seen[:, :ctx] = True
+        for t in range(n):
+            seen[t, [ctx + c for c in O.tree_ancestors(s.trees[b], t)]] = True
+        if s.window > 0:
+            seen &= ago > -s.window
+        rows = slice(int(s.cu[b]), int(s.cu[b + 1]))
+        for h in range(s.H):
+            k, v = cache[:, slots, h // (s.H // s.KVH)]
+            q = s.query[rows].double().view(n, s.H, s.D)[:, h]
+            x = (q[:, None] * k[None]).sum(2) * s.D ** -0.5 + (s.slopes[h] * ago if s.slopes else 0.0)
+            none = (seen & (x.isnan() | (x == INF))).any(1) | ~(seen & (x > -INF)).any(1)
+            w = torch.softmax(torch.where(seen, x.nan_to_num(0.0, 0.0, -INF), -INF), 1).nan_to_num(0.0)
+            both = (seen & (x == -INF)).double() @ (~v.isfinite()).double() > 0
+            up = (seen.double() @ (v.isnan() | (v == INF)).double() > 0) | both
+            down = (seen.double() @ (v.isnan() | (v == -INF)).double() > 0) | both
+            o = w @ v.nan_to_num(0.0, 0.0, 0.0)
+            o = torch.where(up & down, float("nan"), torch.where(up, INF, torch.where(down, -INF, o)))
+            o[none] = float("nan")
+            out[rows, h] = o
+    return out.view(s.rows, -1)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_drawn_values_that_are_not_finite(seed):
+    """Anywhere in keys, values and queries, seen by all, by some or by none."""
+    r = random.Random(seed)
+    n, longest, widest = r.randint(1, 4), r.choice([20, 200, 400, 900]), r.choice([3, 20, 80])
+    ctx, nodes = [r.randint(0, longest) for _ in range(n)], [r.randint(0, widest) for _ in range(n)]
+    nodes[-1] = max(1, nodes[-1])
+    kv, fp8 = r.choice([1, 2]), r.random() < 0.3
+    s = TreeScene(ctx, nodes, kv * r.choice([1, 2, 4, 5]), kv, r.choice([64, 128]), r.choice([16, 32]), r.choice([BF, FP]),
+                  fp8, r.choice([0, 0, 1, 30, 200, 300]), r.random() < 0.25,
+                  r.choice(["bushy", "chain", "star", "forest"]), seed)
+    rows = s.cache.view(2, -1, s.row)
+    kinds = [0x7F, 0xFF] if fp8 else [INF, -INF, INF, -INF, float("nan")]
+    for _ in range(r.randint(1, 12)):
+        b = r.randrange(n)
+        at = s.slot(b, r.randrange(ctx[b] + nodes[b])) if ctx[b] + nodes[b] and r.random() < 0.8 else r.randrange(rows.shape[1])
+        half, c = r.choice([0, 1, 1, 1]), r.randrange(s.row)
+        rows[half, at, c] = r.choice(kinds)
+        if r.random() < 0.3:                               # key and value of one token
+            rows[1 - half, at, c // s.D * s.D + r.randrange(s.D)] = r.choice(kinds)
+    if r.random() < 0.3:
+        s.query[r.randrange(s.rows), r.randrange(s.H * s.D)] = r.choice([INF, -INF, float("nan")])
+    got = s.decode().cpu().double()
+    clean("drawn")
+    want = by_class(s)
+    if not s.fp8:
+        s.cache[:] = s.cache.nan_to_num(0.0, 0.0, 0.0)     # for the tolerance
+    else:
+        s.cache[(s.cache & 0x7F) == 0x7F] = 0
+    s.query = s.query.nan_to_num(0.0, 0.0, 0.0)
+    _, spread = s.expect()                                 # of the finite values alone
+    within(got, want, tolerance(s, want.nan_to_num(0.0, 0.0, 0.0), spread), "drawn")
